@@ -270,11 +270,6 @@ def prepare(case, seed):
                   v_cache=_randn(g, (used, hkv, BS, d), dt), tables=tables, ctx=ctx.int().cuda(), cu=cu.int().cuda(),
                   out=torch.empty((T, hq, d), dtype=dt, device="cuda"), ctx_host=ctx.tolist(), qn_host=qn.tolist(),
                   max_q=int(qn.max()), status=torch.zeros(1, dtype=torch.int32, device="cuda"))
-        if own:
-            import paged_kv_cache_tables_gb300 as pkv
-            if op == "decode":
-                n = pkv.window_decode_workspace_size(case["seqs"], hq, hkv, d, W, sinks)
-                st["work"] = torch.empty(max(16, n), dtype=torch.uint8, device="cuda")
     return st
 
 
@@ -313,7 +308,7 @@ def _run_own(st, c):
         return {k: st[k] for k in ("q_out", "k_out")}
     if op == "decode":
         pkv.paged_window_decode_attention(st["out"], st["q"], st["k_cache"], st["v_cache"], st["tables"], st["ctx"],
-                                          c["window"], num_sinks=c["sinks"], workspace=st["work"], dev_status=st["status"])
+                                          c["window"], num_sinks=c["sinks"], dev_status=st["status"])
         return st["out"]
     pkv.paged_window_prefill_attention(st["out"], st["q"], st["cu"], st["max_q"], st["k_cache"], st["v_cache"],
                                        st["tables"], st["ctx"], c["window"], num_sinks=c["sinks"], dev_status=st["status"])
