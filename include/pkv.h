@@ -79,6 +79,8 @@ extern "C" {
                                    split range did not tile it exactly, or the blocks streamed
                                    differ from the planned total; the affected outputs are wrong.
                                    Never expected; a library bug if seen. */
+#define PKV_DEV_FREE_LIST 64    /* a free list held fewer blocks than a step needs, or has no room for those
+                                   given back, or its count is outside [0, capacity]; nothing was moved */
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char *pkv_status_string(int status);
@@ -372,6 +374,190 @@ int pkv_paged_decode_attention_static(void *out, const void *q, const void *k_ca
                                       const int32_t *context_lens, int num_seqs, int num_blocks,
                                       int num_q_heads, int num_kv_heads, int head_dim, int block_size,
                                       float scale, int dtype, int out_dtype, int *dev_status, void *stream);
+
+/* ---- sliding window, first tokens ------------------------------------------------
+ * Attention over a window: position p sees position t iff
+ *     t <= p  and  (t > p - window  or  t < num_sinks),
+ * the last `window` positions (its own among them) and the first num_sinks of
+ * the sequence.  window >= 1, num_sinks >= 0; a window of at least the context
+ * is plain causal attention.  Blocks that hold no visible position are not
+ * read, and their table entries may be anything (-1 after pkv_release_blocks).
+ * The pages describe no window; it is the form long contexts are served in.
+ */
+
+/*
+ * pkv_paged_window_decode_attention -- pkv_paged_decode_attention over a
+ * window: the query of sequence s sits at position context_lens[s] - 1.
+ * Arguments as there, without a workspace, and scale must be positive.  One
+ * launch; a range's parts meet through distributed shared memory of a
+ * thread-block cluster, in an order fixed by the context lengths, so equal
+ * inputs give equal bits.  Hidden positions of a block that is read may hold
+ * anything (NaN, infinity) in K and V.  context_lens is read after the wait
+ * for the work enqueued before the call.  Further limits: num_seqs *
+ * num_kv_heads * 16 and num_seqs * max_blocks_per_seq below 2^31,
+ * max_blocks_per_seq <= 2^26 (PKV_ERR_UNSUPPORTED).
+ */
+int pkv_paged_window_decode_attention(void *out, const void *q, const void *k_cache, const void *v_cache,
+                                      const int32_t *block_tables, int max_blocks_per_seq,
+                                      const int32_t *context_lens, int num_seqs, int num_blocks, int num_q_heads,
+                                      int num_kv_heads, int head_dim, int block_size, int window, int num_sinks,
+                                      float scale, int dtype, int out_dtype, int *dev_status, void *stream);
+
+/*
+ * pkv_paged_window_prefill_attention -- pkv_paged_prefill_attention over a
+ * window: row i of chunk c sits at position context_lens[c] - q_len + i.
+ * Arguments as there; scale must be positive; out and q are 16-B aligned.  A
+ * chunk whose rows lie outside [0, total_q) is skipped and sets
+ * PKV_DEV_BAD_CHUNK.  Positions that no row of the chunk sees may hold
+ * anything; an infinity or NaN in V at a position that some of a chunk's rows
+ * see can reach neighbouring rows that do not (a hidden weight is a
+ * multiplication by zero), as it can in pkv_paged_prefill_attention.
+ */
+int pkv_paged_window_prefill_attention(void *out, const void *q, const int32_t *cu_seqlens, int num_seqs,
+                                       int max_q_len, int total_q, const void *k_cache, const void *v_cache,
+                                       const int32_t *block_tables, int max_blocks_per_seq,
+                                       const int32_t *context_lens, int num_blocks, int num_q_heads, int num_kv_heads,
+                                       int head_dim, int block_size, int window, int num_sinks, float scale, int dtype,
+                                       int out_dtype, int *dev_status, void *stream);
+
+/* ---- queries and keys: norm, rotary positions, append ---------------------------- */
+
+/* Scalings of the rotation's frequencies f_i = base^(-2 i / rotary_dim) for
+ * contexts longer than a model was trained on.
+ *   PLAIN   f_i
+ *   LINEAR  f_i / factor (position interpolation)
+ *   NTK     base * factor^(rotary_dim / (rotary_dim - 2)) in place of base
+ *   BANDS   by turns t_i = original_context f_i / 2 pi over the original
+ *           context: f_i above `high` turns, f_i / factor below `low`, and
+ *           s f_i + (1 - s) f_i / factor, s = (t_i - low) / (high - low),
+ *           between (customary: low 1, high 4)
+ *   YARN    "YaRN: Efficient Context Window Extension" (arXiv 2309.00071):
+ *           f_i below the pair that makes `high` turns, f_i / factor above the
+ *           pair that makes `low`, a linear ramp over the pairs between
+ *           (customary: low 1, high 32); cos and sin are multiplied by
+ *           0.1 ln(factor) + 1 */
+#define PKV_ROPE_PLAIN 0
+#define PKV_ROPE_LINEAR 1
+#define PKV_ROPE_NTK 2
+#define PKV_ROPE_BANDS 3
+#define PKV_ROPE_YARN 4
+
+/*
+ * Fills freqs (HOST array, rotary_dim / 2 entries) with the frequencies as
+ * turns per position in 64-bit fixed point, round(f_i / 2 pi * 2^64), and
+ * *mscale with the factor on cos and sin.  The caller keeps them on the device
+ * for the calls below.  base > 1; factor >= 1 (not read by PLAIN);
+ * original_context > 0 and 0 < low < high (read by BANDS and YARN).
+ * rotary_dim: a multiple of 16, 16 to 128.  Pure host code.
+ */
+int pkv_rope_frequencies(int64_t *freqs, float *mscale, int rotary_dim, double base, int scaling, double factor,
+                         double original_context, double low, double high);
+
+/*
+ * pkv_qk_rope -- per-head RMS norm (optional) and rotary positions of the
+ * step's queries and keys, in one pass.  For each token and each head row x:
+ *     y = x * rsqrt(mean(x^2) + eps) * weight     (where the weight is given)
+ *     (y_i, y_j) -> mscale * (y_i cos a - y_j sin a, y_i sin a + y_j cos a),
+ *     a = positions[token] * f_k, for the pairs k of the first rotary_dim
+ *     dimensions: (2k, 2k + 1) when interleaved, else (k, k + rotary_dim / 2);
+ * the other dimensions stay y.  Computed in fp32 from the 16-bit input, the
+ * angle exactly modulo a turn at any int32 position, rounded once at the store.
+ *   q, k          device, num_tokens rows of num_q_heads / num_kv_heads heads
+ *                 of head_dim contiguous elements; q_stride / k_stride
+ *                 elements from a token to the next, multiples of 8 (slices of
+ *                 a fused projection's rows); 16-B aligned
+ *   q_out, k_out  as q and k, with strides of their own that keep the rows
+ *                 apart.  q_out may be q and k_out may be k (same stride); any
+ *                 other sharing of memory between an output and an input row
+ *                 is PKV_ERR_INVALID_ARG
+ *   positions     device int32 [num_tokens], any value
+ *   freqs         device copy of pkv_rope_frequencies' array, 8-B aligned
+ *   q_weight, k_weight  device [head_dim] of weight_dtype (dtype or F32), 16-B
+ *                 aligned, or NULL: no norm of these heads
+ *   eps           finite, >= 0 (read with a weight)
+ * head_dim 64 or 128, rotary_dim a multiple of 16 up to head_dim.
+ * num_tokens == 0 is a no-op.
+ */
+int pkv_qk_rope(void *q_out, int64_t q_out_stride, void *k_out, int64_t k_out_stride, const void *q, int64_t q_stride,
+                const void *k, int64_t k_stride, const int32_t *positions, const int64_t *freqs, int rotary_dim,
+                int interleaved, float mscale, const void *q_weight, const void *k_weight, int weight_dtype, float eps,
+                int num_tokens, int num_q_heads, int num_kv_heads, int head_dim, int dtype, void *stream);
+
+/*
+ * pkv_qk_rope_append -- pkv_qk_rope with the keys stored straight into the
+ * paged cache, and the values with them: q_out as there, and for every token
+ * with slot_mapping[t] >= 0 its rotated key rows and its value rows (copied
+ * unchanged) at cache[slot / 16][h][slot % 16][:], as pkv_kv_append.  Slots
+ * must be unique within a call; one outside the pool is skipped and sets
+ * PKV_DEV_BAD_SLOT.  The caches must not share memory with q, k, v or q_out.
+ */
+int pkv_qk_rope_append(void *q_out, int64_t q_out_stride, const void *q, int64_t q_stride, const void *k,
+                       int64_t k_stride, const void *v, int64_t v_stride, const int32_t *positions,
+                       const int64_t *slot_mapping, const int64_t *freqs, int rotary_dim, int interleaved,
+                       float mscale, const void *q_weight, const void *k_weight, int weight_dtype, float eps,
+                       int num_tokens, void *k_cache, void *v_cache, int num_blocks, int block_size, int num_q_heads,
+                       int num_kv_heads, int head_dim, int dtype, int *dev_status, void *stream);
+
+/* ---- the step's tables on the GPU ------------------------------------------------
+ * The block tables, slot map, positions and lengths that a step's kernels
+ * read, built by one launch from the sequences' lengths and a free list in
+ * device memory: a loop that decodes without a host round trip, or inside a
+ * captured graph, needs no upload.  The free list is a stack as the host pool's
+ * ("Project 17" Step 4): free_list[0 .. *free_count) hold the free ids, blocks
+ * are taken from its end and given back to it.  Tables must not share blocks
+ * between sequences (no prefix caching): there are no reference counts.
+ */
+#define PKV_TABLES_MAX_SEQS 16384
+
+/*
+ * pkv_step_tables -- grows the tables for the step and lays out its tokens.
+ * In the order of the sequences, s takes ceil((len + new) / 16) - ceil(len /
+ * 16) blocks, each the last id left on the list, into its next table entries.
+ *   seq_lens      device int32 [num_seqs], tokens in the cache before the step
+ *   new_lens      device int32 [num_seqs], tokens of this step (0: idle)
+ *   block_tables  device int32 [num_seqs][max_blocks_per_seq], the entries of
+ *                 the blocks taken are written, the others left as they are
+ *   free_list     device int32 [free_capacity], not written
+ *   free_count    device int32, ids on the list; free_count_out (may be the
+ *                 same) receives what is left
+ *   context_lens  device int32 [num_seqs] (may be seq_lens): len + new
+ *   cu_seqlens    device int32 [num_seqs + 1]: prefix sums of new_lens
+ *   slot_mapping  device int64 [max_tokens], and token_pos int32 [max_tokens]:
+ *                 each token's cache slot and position, in the order of
+ *                 the sequences; rows behind the last token get slot -1
+ *                 (which an append skips) and position 0
+ * All or nothing: where a length is negative or len + new exceeds the table
+ * (PKV_DEV_BAD_CONTEXT), new is negative or the tokens exceed max_tokens
+ * (PKV_DEV_BAD_CHUNK), or the list is short (PKV_DEV_FREE_LIST), no block is
+ * taken: cu_seqlens are 0, context_lens = seq_lens, every slot is -1 and
+ * *free_count_out = *free_count.  A block id outside [0, num_blocks) sets
+ * PKV_DEV_BAD_BLOCK_ID and its tokens' slots are -1.
+ * num_seqs <= PKV_TABLES_MAX_SEQS, max_blocks_per_seq <= 2^26.  Apart from the
+ * two pairs named, the arrays must not share memory.
+ */
+int pkv_step_tables(const int32_t *seq_lens, const int32_t *new_lens, int num_seqs, int32_t *block_tables,
+                    int max_blocks_per_seq, const int32_t *free_list, int free_capacity, const int32_t *free_count,
+                    int32_t *free_count_out, int num_blocks, int block_size, int32_t *context_lens,
+                    int32_t *cu_seqlens, int64_t *slot_mapping, int32_t *token_pos, int max_tokens, int *dev_status,
+                    void *stream);
+
+/*
+ * pkv_release_blocks -- gives blocks back to the free list.  Of a sequence with
+ * finished[s] != 0 (finished may be NULL: none) every block of its seq_lens[s]
+ * tokens; of another, when window > 0, the blocks that its next token at
+ * position seq_lens[s] and all later ones cannot see: logical blocks j with
+ * ceil(num_sinks / 16) <= j and 16 (j + 1) <= seq_lens[s] - window + 1.
+ * Entries that are negative (given back before) are passed over; each block
+ * given back leaves -1 in its entry.  The ids go on the list's end in the order
+ * of the sequences, and of the entries within one.  *free_count is updated in
+ * place.  An id >= num_blocks is left where it is and sets PKV_DEV_BAD_BLOCK_ID,
+ * a length outside [0, max_blocks_per_seq * 16] is clamped and sets
+ * PKV_DEV_BAD_CONTEXT; where the list has no room for all of them
+ * (PKV_DEV_FREE_LIST), nothing is moved.
+ */
+int pkv_release_blocks(int32_t *block_tables, int max_blocks_per_seq, const int32_t *seq_lens, const int32_t *finished,
+                       int num_seqs, int window, int num_sinks, int32_t *free_list, int free_capacity,
+                       int32_t *free_count, int num_blocks, int block_size, int *dev_status, void *stream);
 
 /* ---- host block pool ----------------------------------------------------------
  * A preallocated set of physical block ids with a free list used as a stack

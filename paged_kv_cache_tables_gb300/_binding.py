@@ -19,6 +19,9 @@ LIB_PATH = os.path.join(_HERE, "libpkv.so")
 PKV_OK = 0
 DTYPE_F16, DTYPE_BF16, DTYPE_F32 = 0, 1, 2
 DEV_BAD_BLOCK_ID, DEV_BAD_CONTEXT, DEV_WAIT_TIMEOUT, DEV_BAD_SLOT, DEV_BAD_CHUNK, DEV_SPLIT = 1, 2, 4, 8, 16, 32
+DEV_FREE_LIST = 64
+ROPE_PLAIN, ROPE_LINEAR, ROPE_NTK, ROPE_BANDS, ROPE_YARN = 0, 1, 2, 3, 4
+TABLES_MAX_SEQS = 16384
 
 _lib = None
 
@@ -73,6 +76,7 @@ def lib():
         raise RuntimeError("libpkv.so is not built (%s); run paged_kv_cache_tables_gb300.build.build()" % LIB_PATH)
     L = ctypes.CDLL(LIB_PATH)
     P, I, I64, F, SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
+    D = ctypes.c_double
     sig = {
         "pkv_status_string": ([I], ctypes.c_char_p),
         "pkv_last_cuda_error": ([], ctypes.c_char_p),
@@ -88,6 +92,15 @@ def lib():
         "pkv_paged_mixed_append_attention": ([P, P, P, P, P, P, I, I, I, I, P, P, P, I, P, I, I, I, I, I, F, I, I, P,
                                               SZ, P, P, I, P, P], I),
         "pkv_mixed_split": ([I, P, I, P, I, I, I, I, I], I),
+        "pkv_paged_window_decode_attention": ([P, P, P, P, P, I, P, I, I, I, I, I, I, I, I, F, I, I, P, P], I),
+        "pkv_paged_window_prefill_attention": ([P, P, P, I, I, I, P, P, P, I, P, I, I, I, I, I, I, I, F, I, I, P, P],
+                                               I),
+        "pkv_rope_frequencies": ([P, ctypes.POINTER(F), I, D, I, D, D, D, D], I),
+        "pkv_qk_rope": ([P, I64, P, I64, P, I64, P, I64, P, P, I, I, F, P, P, I, F, I, I, I, I, I, P], I),
+        "pkv_qk_rope_append": ([P, I64, P, I64, P, I64, P, I64, P, P, P, I, I, F, P, P, I, F, I, P, P, I, I, I, I, I,
+                                I, P, P], I),
+        "pkv_step_tables": ([P, P, I, P, I, P, I, P, P, I, I, P, P, P, P, I, P, P], I),
+        "pkv_release_blocks": ([P, I, P, P, I, I, I, P, I, P, I, I, P, P], I),
         "pkv_copy_blocks": ([P, I64, P, I64, P, I, I64, P, P], I),
         "pkv_pool_create": ([I, P], P),
         "pkv_pool_destroy": ([P], None),
@@ -320,6 +333,215 @@ def copy_blocks(dst, src, pairs, dev_status=None, stream=None):
                                src.shape[0], ctypes.c_void_p(pairs.data_ptr()), pairs.shape[0], block_bytes,
                                _status_ptr(dev_status), _stream(stream))
     _check("pkv_copy_blocks", st)
+
+
+# The calls below check shapes against one another, take tensors of any one
+# device (the call runs with that device current, on its current stream unless
+# one is given) and pass plain integers.
+
+def _code(name, dtype):
+    import torch
+    code = {torch.float16: DTYPE_F16, torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32}.get(dtype)
+    if code is None:
+        raise TypeError("%s must be float16, bfloat16 or float32, got %s" % (name, dtype))
+    return code
+
+
+def _ptr(name, t, dtype, shape, device):
+    """Address of a contiguous tensor of this dtype, shape and device (index)."""
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if t.get_device() != device:
+        raise ValueError("%s must be a CUDA tensor on the device of the others" % name)
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
+
+
+def _rows(name, t, dtype, shape, device):
+    """(address, elements between tokens) of [T, heads, d] rows whose heads are
+    contiguous within a token (a slice of a fused projection's rows will do)."""
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if t.get_device() != device:
+        raise ValueError("%s must be a CUDA tensor on the device of the others" % name)
+    T, H, d = shape
+    st = t.stride()
+    if T and (st[2] != 1 or (H > 1 and st[1] != d)):
+        raise ValueError("%s must hold each token's heads contiguously" % name)
+    return t.data_ptr(), st[0] if T > 1 else H * d
+
+
+def _device_of(name, t):
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("%s must be a CUDA tensor" % name)
+    return t.get_device()
+
+
+def _enqueue(func, device, stream, *args):
+    """Calls the entry point `func` with the tensors' device current, its last
+    argument the stream."""
+    import torch
+    fn = getattr(lib(), func)
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif stream.device_index != device:
+        raise ValueError("the stream belongs to another device than the tensors")
+    if torch.cuda.current_device() == device:
+        status = fn(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, stream.cuda_stream)
+    if status != PKV_OK:
+        raise PkvError(func, status)
+
+
+def _status_of(dev_status, device):
+    import torch
+    return None if dev_status is None else _ptr("dev_status", dev_status, torch.int32, (1,), device)
+
+
+def paged_window_decode_attention(out, q, k_cache, v_cache, block_tables, context_lens, window, num_sinks=0, scale=None,
+                                  dev_status=None, stream=None):
+    """pkv_paged_window_decode_attention: q/out [S, Hq, d]; block_tables int32
+    [S, max_blocks]; context_lens int32 [S].  Each query sees the last `window`
+    positions of its context and the first num_sinks."""
+    import torch
+    dev = _device_of("q", q)
+    S, Hq, d = q.shape
+    NB, Hkv, bs, _ = k_cache.shape
+    MB = block_tables.shape[1]
+    cache = (NB, Hkv, bs, d)
+    _enqueue("pkv_paged_window_decode_attention", dev, stream, _ptr("out", out, out.dtype, q.shape, dev),
+             _ptr("q", q, q.dtype, q.shape, dev), _ptr("k_cache", k_cache, q.dtype, cache, dev),
+             _ptr("v_cache", v_cache, q.dtype, cache, dev), _ptr("block_tables", block_tables, torch.int32, (S, MB), dev),
+             MB, _ptr("context_lens", context_lens, torch.int32, (S,), dev), S, NB, Hq, Hkv, d, bs, window, num_sinks,
+             1.0 / math.sqrt(d) if scale is None else scale, _code("q", q.dtype), _code("out", out.dtype),
+             _status_of(dev_status, dev))
+
+
+def paged_window_prefill_attention(out, q, cu_seqlens, max_q_len, k_cache, v_cache, block_tables, context_lens, window,
+                                   num_sinks=0, scale=None, dev_status=None, stream=None):
+    """pkv_paged_window_prefill_attention: q/out [total_q, Hq, d]; cu_seqlens
+    int32 [S + 1].  Each row sees the last `window` positions up to its own and
+    the first num_sinks."""
+    import torch
+    dev = _device_of("q", q)
+    T, Hq, d = q.shape
+    NB, Hkv, bs, _ = k_cache.shape
+    S, MB = block_tables.shape
+    cache = (NB, Hkv, bs, d)
+    _enqueue("pkv_paged_window_prefill_attention", dev, stream, _ptr("out", out, out.dtype, q.shape, dev),
+             _ptr("q", q, q.dtype, q.shape, dev), _ptr("cu_seqlens", cu_seqlens, torch.int32, (S + 1,), dev), S,
+             max_q_len, T, _ptr("k_cache", k_cache, q.dtype, cache, dev), _ptr("v_cache", v_cache, q.dtype, cache, dev),
+             _ptr("block_tables", block_tables, torch.int32, (S, MB), dev), MB,
+             _ptr("context_lens", context_lens, torch.int32, (S,), dev), NB, Hq, Hkv, d, bs, window, num_sinks,
+             1.0 / math.sqrt(d) if scale is None else scale, _code("q", q.dtype), _code("out", out.dtype),
+             _status_of(dev_status, dev))
+
+
+def rope_frequencies(rotary_dim, base=10000.0, scaling=ROPE_PLAIN, factor=1.0, original_context=0, low=1.0, high=32.0,
+                     device="cuda"):
+    """pkv_rope_frequencies: (freqs int64 [rotary_dim / 2] on `device`, mscale),
+    the arguments that qk_rope and qk_rope_append take."""
+    import torch
+    host = np.empty(max(int(rotary_dim) // 2, 1), dtype=np.int64)
+    m = ctypes.c_float(0.0)
+    _check("pkv_rope_frequencies",
+           lib().pkv_rope_frequencies(host.ctypes.data, ctypes.byref(m), rotary_dim, base, scaling, factor,
+                                      original_context, low, high))
+    return torch.from_numpy(host).to(device), m.value
+
+
+def _rope_args(q, k, positions, freqs, q_weight, k_weight):
+    """What the two entry points share: device, sizes, and their argument runs."""
+    import torch
+    dev = _device_of("q", q)
+    T, Hq, d = q.shape
+    Hkv = k.shape[1]
+    w = [x for x in (q_weight, k_weight) if x is not None]
+    if len(w) == 2 and w[0].dtype != w[1].dtype:
+        raise TypeError("q_weight and k_weight must have one dtype")
+    wt = w[0].dtype if w else q.dtype
+    weights = [None if x is None else _ptr(n, x, wt, (d,), dev) for n, x in (("q_weight", q_weight),
+                                                                             ("k_weight", k_weight))]
+    pos = _ptr("positions", positions, torch.int32, (T,), dev)
+    if freqs.dim() != 1:
+        raise ValueError("freqs must have 1 dim")
+    fr = _ptr("freqs", freqs, torch.int64, freqs.shape, dev)
+    return dev, T, Hq, Hkv, d, weights + [_code("weights", wt)], pos, fr, 2 * freqs.shape[0]
+
+
+def qk_rope(q_out, k_out, q, k, positions, freqs, interleaved=False, mscale=1.0, q_weight=None, k_weight=None, eps=1e-6,
+            stream=None):
+    """pkv_qk_rope: q, q_out [T, Hq, d] and k, k_out [T, Hkv, d], each token's
+    heads contiguous; positions int32 [T]; freqs and mscale from
+    rope_frequencies.  q_out may be q, and k_out k."""
+    dev, T, Hq, Hkv, d, weights, pos, fr, rot = _rope_args(q, k, positions, freqs, q_weight, k_weight)
+    _enqueue("pkv_qk_rope", dev, stream, *_rows("q_out", q_out, q.dtype, (T, Hq, d), dev),
+             *_rows("k_out", k_out, q.dtype, (T, Hkv, d), dev), *_rows("q", q, q.dtype, (T, Hq, d), dev),
+             *_rows("k", k, q.dtype, (T, Hkv, d), dev), pos, fr, rot, 1 if interleaved else 0, mscale, *weights, eps, T,
+             Hq, Hkv, d, _code("q", q.dtype))
+
+
+def qk_rope_append(q_out, q, k, v, positions, slot_mapping, freqs, k_cache, v_cache, interleaved=False, mscale=1.0,
+                   q_weight=None, k_weight=None, eps=1e-6, dev_status=None, stream=None):
+    """pkv_qk_rope_append: as qk_rope, the keys (rotated) and values [T, Hkv, d]
+    going to the caches [NB, Hkv, 16, d] by slot_mapping, int64 [T]."""
+    import torch
+    dev, T, Hq, Hkv, d, weights, pos, fr, rot = _rope_args(q, k, positions, freqs, q_weight, k_weight)
+    NB, _, bs, _ = k_cache.shape
+    cache = (NB, Hkv, bs, d)
+    _enqueue("pkv_qk_rope_append", dev, stream, *_rows("q_out", q_out, q.dtype, (T, Hq, d), dev),
+             *_rows("q", q, q.dtype, (T, Hq, d), dev), *_rows("k", k, q.dtype, (T, Hkv, d), dev),
+             *_rows("v", v, q.dtype, (T, Hkv, d), dev), pos, _ptr("slot_mapping", slot_mapping, torch.int64, (T,), dev),
+             fr, rot, 1 if interleaved else 0, mscale, *weights, eps, T,
+             _ptr("k_cache", k_cache, q.dtype, cache, dev), _ptr("v_cache", v_cache, q.dtype, cache, dev), NB, bs, Hq,
+             Hkv, d, _code("q", q.dtype), _status_of(dev_status, dev))
+
+
+def step_tables(seq_lens, new_lens, block_tables, free_list, free_count, num_blocks, context_lens, cu_seqlens,
+                slot_mapping, token_pos, free_count_out=None, dev_status=None, stream=None):
+    """pkv_step_tables: seq_lens, new_lens, context_lens int32 [S]; block_tables
+    int32 [S, max_blocks]; free_list int32 [capacity]; free_count int32 [1]
+    (updated in place unless free_count_out is given); cu_seqlens int32 [S + 1];
+    slot_mapping int64 and token_pos int32 [max_tokens].  context_lens may be
+    seq_lens."""
+    import torch
+    dev = _device_of("seq_lens", seq_lens)
+    S, MB = block_tables.shape
+    i32 = torch.int32
+    T = slot_mapping.shape[0]
+    count = _ptr("free_count", free_count, i32, (1,), dev)
+    _enqueue("pkv_step_tables", dev, stream, _ptr("seq_lens", seq_lens, i32, (S,), dev),
+             _ptr("new_lens", new_lens, i32, (S,), dev), S, _ptr("block_tables", block_tables, i32, (S, MB), dev), MB,
+             _ptr("free_list", free_list, i32, (free_list.numel(),), dev), free_list.numel(), count,
+             count if free_count_out is None else _ptr("free_count_out", free_count_out, i32, (1,), dev), num_blocks, 16,
+             _ptr("context_lens", context_lens, i32, (S,), dev), _ptr("cu_seqlens", cu_seqlens, i32, (S + 1,), dev),
+             _ptr("slot_mapping", slot_mapping, torch.int64, (T,), dev), _ptr("token_pos", token_pos, i32, (T,), dev), T,
+             _status_of(dev_status, dev))
+
+
+def release_blocks(block_tables, seq_lens, free_list, free_count, num_blocks, finished=None, window=0, num_sinks=0,
+                   dev_status=None, stream=None):
+    """pkv_release_blocks: blocks of finished sequences (finished int32 [S], non-
+    zero), and with window > 0 those no later token can see, go back to
+    free_list int32 [capacity] / free_count int32 [1]; their entries in
+    block_tables int32 [S, max_blocks] become -1."""
+    import torch
+    dev = _device_of("block_tables", block_tables)
+    S, MB = block_tables.shape
+    i32 = torch.int32
+    _enqueue("pkv_release_blocks", dev, stream, _ptr("block_tables", block_tables, i32, (S, MB), dev), MB,
+             _ptr("seq_lens", seq_lens, i32, (S,), dev),
+             None if finished is None else _ptr("finished", finished, i32, (S,), dev), S, window, num_sinks,
+             _ptr("free_list", free_list, i32, (free_list.numel(),), dev), free_list.numel(),
+             _ptr("free_count", free_count, i32, (1,), dev), num_blocks, 16, _status_of(dev_status, dev))
 
 
 def mixed_split(num_sms, cu_seqlens, num_prefill, context_lens, num_q_heads, num_kv_heads, head_dim, elem_bytes=2):

@@ -1,0 +1,443 @@
+// The step's metadata on the GPU: block tables grown from a device free list,
+// slot map, positions, cumulative and context lengths from the sequences'
+// lengths (pkv_step_tables), and blocks returned to the list
+// (pkv_release_blocks).
+//
+// Mathematics.  Sequence s holds len_s tokens in ceil(len_s / 16) blocks and
+// gets new_s more, so it takes need_s = ceil((len_s + new_s) / 16) -
+// ceil(len_s / 16) blocks.  With the exclusive prefix sums cu (of new) and bx
+// (of need), block k of the step is the k-th id from the end of the free list
+// and belongs to the last s with bx_s <= k; token t of the step belongs to the
+// last s with cu_s <= t and sits at position len_s + t - cu_s.
+//
+// What bounds it: latency.  The step of 4,020 sequences and 127,780 rows
+// writes 1.6 MB, 0.24 us at the measured copy rate; the launch, the reads of
+// the lengths and the scan are a chain of round trips several times as long.
+// So everything is one launch without a workspace: a small step is one CTA;
+// a larger one is one cluster of CTAs, each of which scans all lengths itself
+// (at most 16,384 of them, out of L2) and fills its share of the outputs, its
+// token's sequence found by bisection of the scans in shared memory.  The
+// cluster's barrier between the reads and the writes is what lets the outputs
+// replace the inputs in place.
+#include <cuda_runtime.h>
+
+#include "pkv.h"
+#include "pkv_cluster.cuh"
+#include "pkv_device.cuh"
+#include "pkv_host.h"
+
+namespace pkv {
+
+constexpr int kTabThreads = 1024;
+constexpr int kTabCluster = 8;
+
+struct TablesParams {
+    const int32_t *seq_lens, *new_lens;
+    int32_t *block_tables;
+    const int32_t *free_list;
+    const int32_t *free_count;
+    int32_t *free_count_out;
+    int32_t *context_lens, *cu_seqlens;
+    int64_t *slot_mapping;
+    int32_t *token_pos;
+    int *dev_status;
+    int S, max_blocks, free_capacity, num_blocks, max_tokens;
+    bool vec;   // slot_mapping and token_pos are 16-byte aligned
+};
+
+// Inclusive scan over the CTA of a pair of 64-bit values.
+struct Pair64 {
+    int64_t a, b;
+};
+
+__device__ __forceinline__ Pair64 cta_scan(Pair64 v, Pair64 *sh, Pair64 *total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int64_t a = __shfl_up_sync(0xffffffffu, v.a, off), b = __shfl_up_sync(0xffffffffu, v.b, off);
+        if (lane >= off) {
+            v.a += a;
+            v.b += b;
+        }
+    }
+    if (lane == 31) sh[warp] = v;
+    __syncthreads();
+    if (warp == 0) {
+        Pair64 w = lane < warps ? sh[lane] : Pair64{0, 0};
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int64_t a = __shfl_up_sync(0xffffffffu, w.a, off), b = __shfl_up_sync(0xffffffffu, w.b, off);
+            if (lane >= off) {
+                w.a += a;
+                w.b += b;
+            }
+        }
+        sh[lane] = w;
+    }
+    __syncthreads();
+    if (warp > 0) {
+        v.a += sh[warp - 1].a;
+        v.b += sh[warp - 1].b;
+    }
+    *total = sh[31];
+    return v;
+}
+
+// The last index s in [0, n) with prefix[s] <= x (prefix non-decreasing,
+// prefix[0] = 0 <= x): with x below the total, the one entry that holds x.
+__device__ __forceinline__ int last_at_most(const int *prefix, int n, int x) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (prefix[mid] <= x)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
+}
+
+__global__ void __launch_bounds__(kTabThreads) step_tables_kernel(const TablesParams p) {
+    extern __shared__ int tab_smem[];
+    __shared__ Pair64 sh_scan[32];
+    __shared__ int sh_bad;
+    const int S = p.S;
+    int *cu = tab_smem;          // [S + 1] tokens before each sequence
+    int *bx = cu + S + 1;        // [S + 1] blocks taken before each sequence
+    int *len = bx + S + 1;       // [S]
+    const int tid = threadIdx.x, nt = blockDim.x;
+    const int rank = (int)cluster_ctarank(), ranks = (int)cluster_nctarank();
+    // no early signal to the next kernel: the decode entry points read
+    // context_lens, written here, before their own wait
+    pdl_wait_primary();
+    if (tid == 0) sh_bad = 0;
+    __syncthreads();
+
+    // ---- lengths, checked; a thread takes `per` neighbouring sequences ----
+    const int per = (S + nt - 1) / nt;
+    const int s_lo = min(S, tid * per), s_hi = min(S, s_lo + per);
+    const int64_t limit = (int64_t)p.max_blocks * 16;
+    int bad = 0;
+    Pair64 sum{0, 0};
+    for (int s = s_lo; s < s_hi; ++s) {
+        const int l = p.seq_lens[s], n = p.new_lens[s];
+        len[s] = l;
+        if (l < 0 || (int64_t)l + max(n, 0) > limit) {
+            bad |= PKV_DEV_BAD_CONTEXT;
+        } else if (n < 0 || n > p.max_tokens) {
+            bad |= PKV_DEV_BAD_CHUNK;
+        } else {
+            sum.a += n;
+            sum.b += (int)(((int64_t)l + n + 15) >> 4) - (int)(((int64_t)l + 15) >> 4);
+        }
+    }
+    Pair64 total;
+    const Pair64 incl = cta_scan(sum, sh_scan, &total);
+    const int count = p.free_count[0];
+    if (total.a > p.max_tokens) bad |= PKV_DEV_BAD_CHUNK;
+    if (count < 0 || count > p.free_capacity || total.b > count) bad |= PKV_DEV_FREE_LIST;
+    if (bad) atomicOr(&sh_bad, bad);
+    {
+        int64_t a = incl.a - sum.a, b = incl.b - sum.b;
+        for (int s = s_lo; s < s_hi; ++s) {
+            const int l = len[s], n = p.new_lens[s];
+            cu[s] = (int)a;
+            bx[s] = (int)b;
+            a += n;
+            b += (int)(((int64_t)l + n + 15) >> 4) - (int)(((int64_t)l + 15) >> 4);
+        }
+    }
+    if (tid == 0) {
+        cu[S] = (int)total.a;
+        bx[S] = (int)total.b;
+    }
+    // every CTA has read the lengths and the count before any of them writes
+    // (the outputs may be the same arrays); also this CTA's barrier for the
+    // scans and the verdict
+    __syncthreads();
+    if (ranks > 1) cluster_sync();
+    const bool fail = sh_bad != 0;
+    if (fail && rank == 0 && tid == 0) set_status(p.dev_status, sh_bad);
+
+    // ---- per-sequence outputs ----
+    const int gt = rank * nt + tid, gn = ranks * nt;
+    for (int s = gt; s <= S; s += gn) {
+        p.cu_seqlens[s] = fail ? 0 : cu[s];
+        if (s < S) p.context_lens[s] = fail ? len[s] : len[s] + (cu[s + 1] - cu[s]);
+    }
+    if (gt == 0) p.free_count_out[0] = fail ? count : count - bx[S];
+
+    // ---- the blocks taken ----
+    const int taken = fail ? 0 : bx[S], tokens = fail ? 0 : cu[S];
+    int status = 0;
+    for (int k = gt; k < taken; k += gn) {
+        const int s = last_at_most(bx, S, k);
+        const int32_t id = p.free_list[count - 1 - k];
+        if (id < 0 || id >= p.num_blocks) status |= PKV_DEV_BAD_BLOCK_ID;
+        p.block_tables[(int64_t)s * p.max_blocks + ((len[s] + 15) >> 4) + (k - bx[s])] = id;
+    }
+
+    // ---- slots and positions, four rows at a time: a row's block is the
+    // sequence's open block (in its table) or one of those taken now ----
+    for (int64_t t0 = (int64_t)gt * 4; t0 < p.max_tokens; t0 += (int64_t)gn * 4) {
+        int64_t slot[4];
+        int32_t pos[4];
+        int s = t0 < tokens ? last_at_most(cu, S, (int)t0) : 0;
+        int64_t have = -1;   // block index whose id is in `id`, with its sequence
+        int32_t id = -1;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int64_t t = t0 + e;
+            slot[e] = -1;
+            pos[e] = 0;
+            if (t < tokens) {
+                while (cu[s + 1] <= t) {   // skips sequences without new tokens
+                    ++s;
+                    have = -1;
+                }
+                const int q = len[s] + (int)(t - cu[s]);
+                const int j = q >> 4, old = (len[s] + 15) >> 4;
+                if (have != j) {
+                    id = j < old ? p.block_tables[(int64_t)s * p.max_blocks + j]
+                                 : p.free_list[count - 1 - (bx[s] + j - old)];
+                    have = j;
+                    if (id < 0 || id >= p.num_blocks) {
+                        status |= PKV_DEV_BAD_BLOCK_ID;
+                        id = -1;
+                    }
+                }
+                pos[e] = q;
+                if (id >= 0) slot[e] = (int64_t)id * 16 + (q & 15);
+            }
+        }
+        if (p.vec && t0 + 4 <= p.max_tokens) {
+            reinterpret_cast<longlong2 *>(p.slot_mapping + t0)[0] = make_longlong2(slot[0], slot[1]);
+            reinterpret_cast<longlong2 *>(p.slot_mapping + t0)[1] = make_longlong2(slot[2], slot[3]);
+            *reinterpret_cast<int4 *>(p.token_pos + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (t0 + e < p.max_tokens) {
+                    p.slot_mapping[t0 + e] = slot[e];
+                    p.token_pos[t0 + e] = pos[e];
+                }
+        }
+    }
+    if (status) set_status(p.dev_status, status);
+}
+
+// ---------------------------------------------------------------- release
+
+struct ReleaseParams {
+    int32_t *block_tables;
+    const int32_t *seq_lens, *finished;
+    int32_t *free_list;
+    int32_t *free_count;
+    int *dev_status;
+    int S, max_blocks, free_capacity, num_blocks, window, sinks;
+};
+
+// Table entries [lo, hi) of sequence s that the call gives back.
+__device__ __forceinline__ void release_range(const ReleaseParams &p, int s, int &lo, int &hi, int &status) {
+    int64_t l = p.seq_lens[s];
+    if (l < 0 || l > (int64_t)p.max_blocks * 16) {
+        status |= PKV_DEV_BAD_CONTEXT;
+        l = l < 0 ? 0 : (int64_t)p.max_blocks * 16;
+    }
+    const int nb = (int)((l + 15) >> 4);
+    lo = hi = 0;
+    if (p.finished != nullptr && p.finished[s] != 0) {
+        hi = nb;
+    } else if (p.window > 0) {
+        // the next token sits at position l and sees positions from
+        // l - window + 1 on: a block before that whole is out of the window
+        const int64_t first = l - p.window + 1;
+        lo = (int)(((int64_t)p.sinks + 15) >> 4);
+        hi = first > 0 ? min(nb, (int)(first >> 4)) : 0;
+        if (hi < lo) hi = lo;
+    }
+}
+
+// A warp a row.  Each CTA of the cluster takes neighbouring rows: the first
+// pass counts the blocks a row gives back, the scans (of the CTA's rows, and
+// of the CTAs' totals through distributed shared memory) place them in the
+// free list in the order of the rows and of the blocks within a row, and the
+// second pass moves them.
+__global__ void __launch_bounds__(kTabThreads) release_blocks_kernel(const ReleaseParams p) {
+    extern __shared__ int rel_smem[];    // [rows of this CTA]: blocks given back, then their place
+    __shared__ Pair64 sh_scan[32];
+    __shared__ int sh_total;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x, warps = nt >> 5;
+    const int rank = (int)cluster_ctarank(), ranks = (int)cluster_nctarank();
+    pdl_wait_primary();
+    pdl_launch_dependents();
+    const int rows = (p.S + ranks - 1) / ranks;
+    const int r0 = min(p.S, rank * rows), r1 = min(p.S, r0 + rows);
+    int status = 0;
+
+    for (int s = r0 + warp; s < r1; s += warps) {
+        int lo, hi, n = 0;
+        release_range(p, s, lo, hi, status);
+        const int32_t *row = p.block_tables + (int64_t)s * p.max_blocks;
+        for (int j = lo + lane; j < hi; j += 32) {
+            const int32_t id = row[j];
+            if (id >= p.num_blocks) status |= PKV_DEV_BAD_BLOCK_ID;
+            n += id >= 0 && id < p.num_blocks;
+        }
+        n = __reduce_add_sync(0xffffffffu, n);
+        if (lane == 0) rel_smem[s - r0] = n;
+    }
+    __syncthreads();
+    const int per = (r1 - r0 + nt - 1) / nt;
+    const int i_lo = min(r1 - r0, tid * per), i_hi = min(r1 - r0, i_lo + per);
+    Pair64 sum{0, 0}, total;
+    for (int i = i_lo; i < i_hi; ++i) sum.a += rel_smem[i];
+    const Pair64 incl = cta_scan(sum, sh_scan, &total);
+    {
+        int a = (int)(incl.a - sum.a);
+        for (int i = i_lo; i < i_hi; ++i) {
+            const int n = rel_smem[i];
+            rel_smem[i] = a;
+            a += n;
+        }
+    }
+    // the CTA's total fits: a table has fewer than 2^31 entries
+    if (tid == 0) sh_total = (int)total.a;
+    const int count = p.free_count[0];
+    __syncthreads();
+    if (ranks > 1) cluster_sync();
+    int64_t before = 0, all = 0;
+    for (int r = 0; r < ranks; ++r) {
+        const int n = ranks > 1 ? ld_cluster_s32(cluster_addr(&sh_total, (uint32_t)r)) : sh_total;
+        if (r < rank) before += n;
+        all += n;
+    }
+    // every CTA has read the totals and the count: they may change now, and a
+    // CTA may leave
+    if (ranks > 1) cluster_sync();
+    const bool fail = count < 0 || count > p.free_capacity || count + all > p.free_capacity;
+    if (fail) status |= PKV_DEV_FREE_LIST;
+    if (status) set_status(p.dev_status, status);
+    if (fail) return;
+    if (rank == 0 && tid == 0) p.free_count[0] = count + (int)all;
+
+    for (int s = r0 + warp; s < r1; s += warps) {
+        int lo, hi, ignored = 0;
+        release_range(p, s, lo, hi, ignored);
+        int32_t *row = p.block_tables + (int64_t)s * p.max_blocks;
+        int64_t at = count + before + rel_smem[s - r0];
+        for (int j0 = lo; j0 < hi; j0 += 32) {
+            const int j = j0 + lane;
+            const int32_t id = j < hi ? row[j] : -1;
+            const bool give = id >= 0 && id < p.num_blocks;
+            const unsigned m = __ballot_sync(0xffffffffu, give);
+            if (give) {
+                p.free_list[at + __popc(m & ((1u << lane) - 1u))] = id;
+                row[j] = -1;
+            }
+            at += __popc(m);
+        }
+    }
+}
+
+}  // namespace pkv
+
+extern "C" int pkv_step_tables(const int32_t *seq_lens, const int32_t *new_lens, int num_seqs, int32_t *block_tables,
+                               int max_blocks_per_seq, const int32_t *free_list, int free_capacity,
+                               const int32_t *free_count, int32_t *free_count_out, int num_blocks, int block_size,
+                               int32_t *context_lens, int32_t *cu_seqlens, int64_t *slot_mapping, int32_t *token_pos,
+                               int max_tokens, int *dev_status, void *stream) {
+    pkv::NvtxRange nvtx_range("pkv_step_tables");
+    using namespace pkv;
+    if (num_seqs < 0 || max_blocks_per_seq <= 0 || free_capacity < 0 || num_blocks <= 0 || max_tokens < 0)
+        return PKV_ERR_INVALID_ARG;
+    if (block_size != 16 || num_seqs > PKV_TABLES_MAX_SEQS || max_blocks_per_seq > (1 << 26)) return PKV_ERR_UNSUPPORTED;
+    if (!free_count || !free_count_out || !cu_seqlens) return PKV_ERR_INVALID_ARG;
+    if (num_seqs > 0 && (!seq_lens || !new_lens || !block_tables || !context_lens)) return PKV_ERR_INVALID_ARG;
+    if (max_tokens > 0 && (!slot_mapping || !token_pos)) return PKV_ERR_INVALID_ARG;
+    if (free_capacity > 0 && !free_list) return PKV_ERR_INVALID_ARG;
+    if (!aligned(seq_lens, 4) || !aligned(new_lens, 4) || !aligned(block_tables, 4) || !aligned(free_list, 4) ||
+        !aligned(free_count, 4) || !aligned(free_count_out, 4) || !aligned(context_lens, 4) ||
+        !aligned(cu_seqlens, 4) || !aligned(slot_mapping, 8) || !aligned(token_pos, 4))
+        return PKV_ERR_INVALID_ARG;
+    int sms = 0;
+    int rc = current_sm_count(&sms);
+    if (rc != PKV_OK) return rc;
+    static unsigned long long attr_set = 0;
+    constexpr int kMaxSmem = (3 * PKV_TABLES_MAX_SEQS + 2) * 4;
+    if (!done_on_device(&attr_set)) {
+        cudaError_t e = cudaFuncSetAttribute(step_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+        if (e != cudaSuccess) return cuda_fail(e);
+        mark_done_on_device(&attr_set);
+    }
+    TablesParams prm;
+    prm.seq_lens = seq_lens;
+    prm.new_lens = new_lens;
+    prm.block_tables = block_tables;
+    prm.free_list = free_list;
+    prm.free_count = free_count;
+    prm.free_count_out = free_count_out;
+    prm.context_lens = context_lens;
+    prm.cu_seqlens = cu_seqlens;
+    prm.slot_mapping = slot_mapping;
+    prm.token_pos = token_pos;
+    prm.dev_status = dev_status;
+    prm.S = num_seqs;
+    prm.max_blocks = max_blocks_per_seq;
+    prm.free_capacity = free_capacity;
+    prm.num_blocks = num_blocks;
+    prm.max_tokens = max_tokens;
+    prm.vec = aligned(slot_mapping, 16) && aligned(token_pos, 16);
+    const bool small = num_seqs <= kTabThreads && max_tokens <= 4 * kTabThreads;
+    const int threads = small && num_seqs <= 256 && max_tokens <= 1024 ? 256 : kTabThreads;
+    cudaError_t e = launch_cluster(step_tables_kernel, small ? 1 : kTabCluster, small ? 1 : kTabCluster, threads,
+                                   (size_t)(3 * num_seqs + 2) * 4, static_cast<cudaStream_t>(stream), prm);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    return e == cudaSuccess ? PKV_OK : cuda_fail(e);
+}
+
+extern "C" int pkv_release_blocks(int32_t *block_tables, int max_blocks_per_seq, const int32_t *seq_lens,
+                                  const int32_t *finished, int num_seqs, int window, int num_sinks, int32_t *free_list,
+                                  int free_capacity, int32_t *free_count, int num_blocks, int block_size,
+                                  int *dev_status, void *stream) {
+    pkv::NvtxRange nvtx_range("pkv_release_blocks");
+    using namespace pkv;
+    if (num_seqs < 0 || max_blocks_per_seq <= 0 || free_capacity < 0 || num_blocks <= 0 || window < 0 || num_sinks < 0)
+        return PKV_ERR_INVALID_ARG;
+    if (block_size != 16 || num_seqs > PKV_TABLES_MAX_SEQS || max_blocks_per_seq > (1 << 26)) return PKV_ERR_UNSUPPORTED;
+    if ((int64_t)num_seqs * max_blocks_per_seq >= (int64_t)1 << 31) return PKV_ERR_UNSUPPORTED;
+    if (num_seqs == 0) return PKV_OK;
+    if (!block_tables || !seq_lens || !free_list || !free_count) return PKV_ERR_INVALID_ARG;
+    if (!aligned(block_tables, 4) || !aligned(seq_lens, 4) || !aligned(finished, 4) || !aligned(free_list, 4) ||
+        !aligned(free_count, 4))
+        return PKV_ERR_INVALID_ARG;
+    int sms = 0;
+    int rc = current_sm_count(&sms);
+    if (rc != PKV_OK) return rc;
+    static unsigned long long attr_set = 0;
+    if (!done_on_device(&attr_set)) {
+        cudaError_t e = cudaFuncSetAttribute(release_blocks_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             PKV_TABLES_MAX_SEQS * 4);
+        if (e != cudaSuccess) return cuda_fail(e);
+        mark_done_on_device(&attr_set);
+    }
+    ReleaseParams prm;
+    prm.block_tables = block_tables;
+    prm.seq_lens = seq_lens;
+    prm.finished = finished;
+    prm.free_list = free_list;
+    prm.free_count = free_count;
+    prm.dev_status = dev_status;
+    prm.S = num_seqs;
+    prm.max_blocks = max_blocks_per_seq;
+    prm.free_capacity = free_capacity;
+    prm.num_blocks = num_blocks;
+    prm.window = window;
+    prm.sinks = num_sinks;
+    const int ranks = num_seqs <= 32 ? 1 : kTabCluster;
+    const int rows = (num_seqs + ranks - 1) / ranks;
+    cudaError_t e = launch_cluster(release_blocks_kernel, ranks, ranks, kTabThreads, (size_t)rows * 4,
+                                   static_cast<cudaStream_t>(stream), prm);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    return e == cudaSuccess ? PKV_OK : cuda_fail(e);
+}
