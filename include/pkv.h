@@ -475,7 +475,9 @@ int pkv_rope_frequencies(int64_t *freqs, float *mscale, int rotary_dim, double b
  *   q_weight, k_weight  device [head_dim] of weight_dtype (dtype or F32), 16-B
  *                 aligned, or NULL: no norm of these heads
  *   eps           finite, >= 0 (read with a weight)
- * head_dim 64 or 128, rotary_dim a multiple of 16 up to head_dim.
+ * head_dim 64 or 128, rotary_dim a multiple of 16 up to head_dim.  A call's
+ * warps (at most num_tokens * (num_q_heads + 2 num_kv_heads) * head_dim / 512 + 3
+ * num_tokens) must number below 2^31, else PKV_ERR_UNSUPPORTED.
  * num_tokens == 0 is a no-op.
  */
 int pkv_qk_rope(void *q_out, int64_t q_out_stride, void *k_out, int64_t k_out_stride, const void *q, int64_t q_stride,

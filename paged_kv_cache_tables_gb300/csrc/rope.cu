@@ -18,12 +18,16 @@
 // multiplies alone.  Its top 32 bits, as a signed number of half turns, go to
 // sincospif, which needs no reduction.
 //
-// What bounds it: HBM, each row read and written once.  A CTA computes the
-// (cos, sin) of its tokens' pairs once into shared memory for all heads (a
-// thread for itself would spend more time in sincospif than its bytes take);
-// a row is head_dim / 16 lanes of two 16-byte chunks each, chosen so that
-// both ends of a pair are in one thread and no lane exchange is needed: lane
-// l < r/16 holds pairs 8l .. 8l+7, a lane behind them 16 plain dimensions.
+// What bounds it: HBM, each row read and written once, if the instructions per
+// byte stay few and enough bytes are on their way.  A row is head_dim / 16
+// lanes of two 16-byte chunks each, chosen so that both ends of a pair are in
+// one thread: lane l < r/16 holds pairs 8l .. 8l+7, a lane behind them 16
+// plain dimensions.  A warp takes up to four groups of rows of one token and one
+// kind (query, key or value heads): it issues all their loads at once, and
+// while they are under way works out what the rows share, the (cos, sin) of a
+// lane's eight pairs (the groups of lanes share the sincospi among them), the
+// weight, the slot and the addresses.  The arithmetic is on packed pairs of
+// floats.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -34,8 +38,8 @@
 
 namespace pkv {
 
-constexpr int kRopeThreads = 256;
-constexpr int kRopeMaxTokens = 16;   // tokens a CTA takes at most
+constexpr int kRopeThreads = 64;
+constexpr int kRopeSteps = 4;   // groups of rows a warp takes at most
 
 struct RopeParams {
     void *q_out, *k_out;
@@ -47,169 +51,205 @@ struct RopeParams {
     const void *q_weight, *k_weight;
     void *k_cache, *v_cache;
     int *dev_status;
-    int T, Hq, Hkv, rot, num_blocks, tokens_per_cta;
+    int T, Hq, Hkv, rot, num_blocks;
+    int q_units, k_units, units;   // warps that take a token's query heads, its key heads, and in all
+    int rows_per_unit;
     int weight_f32;
     float mscale, eps;
 };
 
+// Eight 16-bit values as four packed pairs of floats, and back.
 template <typename T>
-__device__ __forceinline__ void unpack8(const uint4 &u, float (&f)[8]) {
+__device__ __forceinline__ void unpack8(const uint4 &u, uint64_t (&f)[4]) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-            f[2 * i] = __uint_as_float(w[i] << 16);
-            f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            f[i] = f2_pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
         } else {
             const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
-            f[2 * i] = v.x;
-            f[2 * i + 1] = v.y;
+            f[i] = f2_pack(v.x, v.y);
         }
     }
 }
 
 template <typename T>
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-    return make_uint4(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]), pack2<T>(f[4], f[5]), pack2<T>(f[6], f[7]));
+__device__ __forceinline__ uint4 pack8(const uint64_t (&f)[4]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float a, b;
+        f2_unpack(f[i], a, b);
+        w[i] = pack2<T>(a, b);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
 }
 
 template <typename T>
-__device__ __forceinline__ void load_weight8(const void *w, int f32, int at, float (&f)[8]) {
+__device__ __forceinline__ void load_weight8(const void *w, int f32, int at, uint64_t (&f)[4]) {
     if (f32) {
-        const float4 a = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(w) + at));
-        const float4 b = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(w) + at) + 1);
-        f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+        const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(w) + at);
+        const float4 a = __ldg(p), b = __ldg(p + 1);
+        f[0] = f2_pack(a.x, a.y), f[1] = f2_pack(a.z, a.w), f[2] = f2_pack(b.x, b.y), f[3] = f2_pack(b.z, b.w);
     } else {
         unpack8<T>(__ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(w) + at)), f);
     }
 }
 
-// LANES = head_dim / 16 lanes hold a row; rows of a token: its query heads,
-// its key heads and (APPEND) its value heads.
+// LANES = head_dim / 16 lanes hold a row.
 template <typename T, int LANES, bool INTERLEAVED, bool APPEND>
 __global__ void __launch_bounds__(kRopeThreads) qk_rope_kernel(const RopeParams p) {
-    extern __shared__ float4 rope_smem[];   // (cos, sin) pairs, see below
-    constexpr int kRows = kRopeThreads / LANES;
+    constexpr int kGroup = 32 / LANES;   // rows a warp holds at a time
+    constexpr int kShare = 8 / kGroup;   // pairs whose sincospi a lane computes for its column of lanes
     constexpr int D = LANES * 16;
-    const int tid = threadIdx.x, l = tid % LANES;
-    const int t0 = blockIdx.x * p.tokens_per_cta, nt = min(p.tokens_per_cta, p.T - t0);
-    const int per_token = p.Hq + (APPEND ? 2 : 1) * p.Hkv;
-    const int rlanes = p.rot / 16;          // lanes of a row that rotate
-    const int items = nt * per_token;
+    const int lane = threadIdx.x & 31, l = lane % LANES, sub = lane / LANES;
+    const uint32_t unit = blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5);
+    const uint32_t token = unit / (uint32_t)p.units;
+    if (token >= (uint32_t)p.T) return;
+    const int64_t tok = token;
+    // the warp's rows: heads [first, first + rows) of one kind
+    int first = (int)(unit - token * (uint32_t)p.units);
+    const bool is_q = first < p.q_units, is_v = APPEND && first >= p.q_units + p.k_units;
+    first = (first - (is_q ? 0 : (is_v ? p.q_units + p.k_units : p.q_units))) * p.rows_per_unit;
+    const int rows = min(p.rows_per_unit, (is_q ? p.Hq : p.Hkv) - first);
     // element offsets of this lane's two chunks within a row
-    const bool turns = l < rlanes;
+    const bool turns = l < p.rot / 16;
     const int c0 = turns && !INTERLEAVED ? 8 * l : 16 * l;
     const int c1 = turns && !INTERLEAVED ? p.rot / 2 + 8 * l : 16 * l + 8;
+    const T *src = is_q   ? static_cast<const T *>(p.q) + tok * p.q_stride
+                   : is_v ? static_cast<const T *>(p.v) + tok * p.v_stride
+                          : static_cast<const T *>(p.k) + tok * p.k_stride;
+    src += (first + sub) * D;
     pdl_wait_primary();
     pdl_launch_dependents();
 
-    auto source = [&](int t, int row) -> const T * {
-        const int64_t tok = t0 + t;
-        if (row < p.Hq) return static_cast<const T *>(p.q) + tok * p.q_stride + (int64_t)row * D;
-        row -= p.Hq;
-        if (!APPEND || row < p.Hkv) return static_cast<const T *>(p.k) + tok * p.k_stride + (int64_t)row * D;
-        return static_cast<const T *>(p.v) + tok * p.v_stride + (int64_t)(row - p.Hkv) * D;
-    };
-
-    // the first row's loads are in flight while the angles are computed
-    int item = tid / LANES;
-    uint4 a = make_uint4(0, 0, 0, 0), b = a;
-    if (item < items) {
-        const T *x = source(item / per_token, item % per_token);
-        a = *reinterpret_cast<const uint4 *>(x + c0);
-        b = *reinterpret_cast<const uint4 *>(x + c1);
-    }
-    // pair 8 l + e of token t is half (e & 1) of the float4 at
-    // t * rot/4 + (e / 2) * rlanes + l: a row's lanes read neighbours
-    const int pairs = p.rot / 2;
-    for (int i = tid; i < nt * pairs; i += kRopeThreads) {
-        const int t = i / pairs, k = i % pairs;
-        const uint64_t turn = (uint64_t)(int64_t)__ldg(p.positions + t0 + t) * (uint64_t)__ldg(p.freqs + k);
-        float s, c;
-        sincospif((float)(int32_t)(turn >> 32) * 4.656612873077393e-10f, &s, &c);   // 2^-31: half turns
-        reinterpret_cast<float2 *>(rope_smem)[2 * (t * (pairs / 2) + ((k & 7) >> 1) * rlanes + (k >> 3)) + (k & 1)] =
-            make_float2(p.mscale * c, p.mscale * s);
-    }
-    __syncthreads();
-
-    for (; item < items; item += kRows) {
-        const int t = item / per_token, row = item % per_token;
-        const int64_t tok = t0 + t;
-        uint4 na = make_uint4(0, 0, 0, 0), nb = na;
-        if (item + kRows < items) {
-            const T *x = source((item + kRows) / per_token, (item + kRows) % per_token);
-            na = *reinterpret_cast<const uint4 *>(x + c0);
-            nb = *reinterpret_cast<const uint4 *>(x + c1);
+    uint4 a[kRopeSteps], b[kRopeSteps];
+#pragma unroll
+    for (int st = 0; st < kRopeSteps; ++st) {
+        if (st * kGroup + sub < rows) {
+            a[st] = *reinterpret_cast<const uint4 *>(src + st * kGroup * D + c0);
+            b[st] = *reinterpret_cast<const uint4 *>(src + st * kGroup * D + c1);
+        } else {
+            a[st] = b[st] = make_uint4(0, 0, 0, 0);
         }
-        const bool is_q = row < p.Hq, is_v = APPEND && row >= p.Hq + p.Hkv;
-        if (!is_v) {
-            float x0[8], x1[8];
-            unpack8<T>(a, x0);
-            unpack8<T>(b, x1);
-            const void *w = is_q ? p.q_weight : p.k_weight;
-            if (w != nullptr) {   // the same for all lanes of a row
-                float ss = 0.f;
+    }
+    // where the rows go: as they came, or (a token's heads 16 rows apart in a block) into the cache
+    T *dst;
+    int64_t step = D;
+    if (is_q) {
+        dst = static_cast<T *>(p.q_out) + tok * p.q_out_stride;
+    } else if constexpr (APPEND) {
+        const int64_t slot = __ldg(p.slot_mapping + tok), block = slot >> 4;
+        if (slot < 0 || block >= p.num_blocks) {
+            if (slot >= 0 && lane == 0) set_status(p.dev_status, PKV_DEV_BAD_SLOT);
+            return;
+        }
+        dst = static_cast<T *>(is_v ? p.v_cache : p.k_cache) + (block * p.Hkv * 16 + (slot & 15)) * D;
+        step = 16 * D;
+    } else {
+        dst = static_cast<T *>(p.k_out) + tok * p.k_out_stride;
+    }
+    dst += (first + sub) * step;
+
+    if (!is_v) {
+        // cos and sin (times mscale) of pairs 2i and 2i + 1 of this lane
+        uint64_t cs[4], sn[4];
+        const uint64_t pos = (uint64_t)(int64_t)__ldg(p.positions + tok);
+        float c[kShare], s[kShare];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) ss += x0[e] * x0[e] + x1[e] * x1[e];
-                const unsigned m = LANES == 8 ? 0xffu << (tid & 24) : 0xfu << (tid & 28);
+        for (int e = 0; e < kShare; ++e) {
+            const uint64_t turn = turns ? pos * (uint64_t)__ldg(p.freqs + 8 * l + kShare * sub + e) : 0ull;
+            sincospif((float)(int32_t)(turn >> 32) * 4.656612873077393e-10f, &s[e], &c[e]);   // 2^-31: half turns
+            c[e] *= p.mscale;
+            s[e] *= p.mscale;
+        }
 #pragma unroll
-                for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(m, ss, o);
-                const float inv = 1.f / sqrtf(ss * (1.f / D) + p.eps);
-                float w0[8], w1[8];
-                load_weight8<T>(w, p.weight_f32, c0, w0);
-                load_weight8<T>(w, p.weight_f32, c1, w1);
+        for (int i = 0; i < 4; ++i) {
+            float v[4];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    x0[e] = x0[e] * inv * w0[e];
-                    x1[e] = x1[e] * inv * w1[e];
+            for (int e = 0; e < 2; ++e) {
+                const int from = (2 * i + e) / kShare * LANES + l;
+                v[e] = __shfl_sync(0xffffffffu, c[(2 * i + e) % kShare], from);
+                v[2 + e] = __shfl_sync(0xffffffffu, s[(2 * i + e) % kShare], from);
+            }
+            cs[i] = f2_pack(v[0], v[1]);
+            sn[i] = f2_pack(v[2], v[3]);
+        }
+        const void *w = is_q ? p.q_weight : p.k_weight;
+        uint64_t w0[4], w1[4];
+        if (w != nullptr) {
+            load_weight8<T>(w, p.weight_f32, c0, w0);
+            load_weight8<T>(w, p.weight_f32, c1, w1);
+        }
+        constexpr uint64_t kMinus = 0x8000000080000000ull;   // the signs of a packed pair
+#pragma unroll
+        for (int st = 0; st < kRopeSteps; ++st) {
+            if (st * kGroup >= rows) break;
+            uint64_t x0[4], x1[4];
+            unpack8<T>(a[st], x0);
+            unpack8<T>(b[st], x1);
+            if (w != nullptr) {
+                uint64_t s2 = f2_mul(x0[0], x0[0]), s3 = f2_mul(x1[0], x1[0]);
+#pragma unroll
+                for (int e = 1; e < 4; ++e) {
+                    s2 = f2_fma(x0[e], x0[e], s2);
+                    s3 = f2_fma(x1[e], x1[e], s3);
+                }
+                float u, v;
+                f2_unpack(f2_add(s2, s3), u, v);
+                float ss = u + v;
+#pragma unroll
+                for (int o = LANES / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                const float inv = rsqrtf(ss * (1.f / D) + p.eps);
+                const uint64_t inv2 = f2_pack(inv, inv);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x0[e] = f2_mul(f2_mul(x0[e], inv2), w0[e]);
+                    x1[e] = f2_mul(f2_mul(x1[e], inv2), w1[e]);
                 }
             }
             if (turns) {
-                const float4 *cs = rope_smem + t * (pairs / 2) + l;
+                if constexpr (INTERLEAVED) {
+                    // (y0, y1) -> (y0, y1) c + (-y1, y0) s
+                    auto turn = [&](uint64_t y, uint64_t c2, uint64_t s2) {
+                        float y0, y1;
+                        f2_unpack(y, y0, y1);
+                        return f2_fma(f2_pack(-y1, y0), s2, f2_mul(y, c2));
+                    };
 #pragma unroll
-                for (int e2 = 0; e2 < 4; ++e2) {
-                    const float4 f = cs[e2 * rlanes];   // cos, sin of pair 2 e2, then of pair 2 e2 + 1
-                    if constexpr (INTERLEAVED) {
-                        float(&x)[8] = e2 < 2 ? x0 : x1;
-                        const int i = (e2 & 1) * 4;
-                        const float u0 = x[i], u1 = x[i + 1], u2 = x[i + 2], u3 = x[i + 3];
-                        x[i] = u0 * f.x - u1 * f.y;
-                        x[i + 1] = u0 * f.y + u1 * f.x;
-                        x[i + 2] = u2 * f.z - u3 * f.w;
-                        x[i + 3] = u2 * f.w + u3 * f.z;
-                    } else {
-                        const float u0 = x0[2 * e2], u1 = x1[2 * e2], u2 = x0[2 * e2 + 1], u3 = x1[2 * e2 + 1];
-                        x0[2 * e2] = u0 * f.x - u1 * f.y;
-                        x1[2 * e2] = u0 * f.y + u1 * f.x;
-                        x0[2 * e2 + 1] = u2 * f.z - u3 * f.w;
-                        x1[2 * e2 + 1] = u2 * f.w + u3 * f.z;
+                    for (int e = 0; e < 4; ++e) {
+                        float ca, cb, sa, sb;
+                        f2_unpack(cs[e], ca, cb);
+                        f2_unpack(sn[e], sa, sb);
+                        uint64_t *x = e < 2 ? x0 : x1;
+                        x[2 * (e & 1)] = turn(x[2 * (e & 1)], f2_pack(ca, ca), f2_pack(sa, sa));
+                        x[2 * (e & 1) + 1] = turn(x[2 * (e & 1) + 1], f2_pack(cb, cb), f2_pack(sb, sb));
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint64_t y0 = x0[e], y1 = x1[e];
+                        x0[e] = f2_fma(y1 ^ kMinus, sn[e], f2_mul(y0, cs[e]));
+                        x1[e] = f2_fma(y1, cs[e], f2_mul(y0, sn[e]));
                     }
                 }
             }
-            a = pack8<T>(x0);
-            b = pack8<T>(x1);
+            a[st] = pack8<T>(x0);
+            b[st] = pack8<T>(x1);
         }
-        T *dst = nullptr;
-        if (is_q) {
-            dst = static_cast<T *>(p.q_out) + tok * p.q_out_stride + (int64_t)row * D;
-        } else if constexpr (!APPEND) {
-            dst = static_cast<T *>(p.k_out) + tok * p.k_out_stride + (int64_t)(row - p.Hq) * D;
-        } else {
-            const int h = is_v ? row - p.Hq - p.Hkv : row - p.Hq;
-            const int64_t slot = __ldg(p.slot_mapping + tok);
-            const int64_t block = slot >> 4;
-            if (slot >= 0 && block < p.num_blocks)
-                dst = static_cast<T *>(is_v ? p.v_cache : p.k_cache) +
-                      ((block * p.Hkv + h) * 16 + (slot & 15)) * (int64_t)D;
-            else if (slot >= 0 && l == 0 && h == 0)
-                set_status(p.dev_status, PKV_DEV_BAD_SLOT);
+    }
+#pragma unroll
+    for (int st = 0; st < kRopeSteps; ++st) {
+        if (st * kGroup + sub < rows) {
+            *reinterpret_cast<uint4 *>(dst + st * kGroup * step + c0) = a[st];
+            *reinterpret_cast<uint4 *>(dst + st * kGroup * step + c1) = b[st];
         }
-        if (dst != nullptr) {
-            *reinterpret_cast<uint4 *>(dst + c0) = a;
-            *reinterpret_cast<uint4 *>(dst + c1) = b;
-        }
-        a = na;
-        b = nb;
     }
 }
 
@@ -228,9 +268,8 @@ static bool rows_meet(const void *a, int64_t sa, int64_t la, const void *b, int6
 }
 
 template <typename T, int LANES>
-static cudaError_t launch_rope_t(const RopeParams &prm, bool interleaved, bool append, int grid, size_t smem,
-                                 cudaStream_t stream) {
-    auto go = [&](auto kernel) { return launch_pdl(kernel, dim3(grid), dim3(kRopeThreads), smem, stream, prm); };
+static cudaError_t launch_rope_t(const RopeParams &prm, bool interleaved, bool append, int grid, cudaStream_t stream) {
+    auto go = [&](auto kernel) { return launch_pdl(kernel, dim3(grid), dim3(kRopeThreads), 0, stream, prm); };
     if (interleaved)
         return append ? go(qk_rope_kernel<T, LANES, true, true>) : go(qk_rope_kernel<T, LANES, true, false>);
     return append ? go(qk_rope_kernel<T, LANES, false, true>) : go(qk_rope_kernel<T, LANES, false, false>);
@@ -284,23 +323,26 @@ static int rope_launch(RopeParams &prm, int head_dim, int interleaved, int dtype
     int sms = 0;
     int rc = current_sm_count(&sms);
     if (rc != PKV_OK) return rc;
-    // tokens a CTA takes: about three rows per row of threads, but no fewer
-    // than two CTAs per SM while there are tokens for them
-    const int per_token = prm.Hq + (append ? 2 : 1) * prm.Hkv;
-    const int rows = kRopeThreads / (head_dim / 16);
-    int64_t tokens = ((int64_t)3 * rows + per_token - 1) / per_token;
-    tokens = tokens < 1 ? 1 : (tokens > kRopeMaxTokens ? kRopeMaxTokens : tokens);
-    while (tokens > 1 && (prm.T + tokens - 1) / tokens < 2 * sms) --tokens;
-    prm.tokens_per_cta = (int)tokens;
-    const int grid = (int)((prm.T + tokens - 1) / tokens);
-    const size_t smem = (size_t)tokens * prm.rot / 2 * sizeof(float2);
+    // groups of rows a warp takes: kRopeSteps, fewer while that leaves SMs
+    // with less than 16 warps
+    const int group = 32 / (head_dim / 16);
+    for (int steps = kRopeSteps;; --steps) {
+        prm.rows_per_unit = steps * group;
+        prm.q_units = (prm.Hq + prm.rows_per_unit - 1) / prm.rows_per_unit;
+        prm.k_units = (prm.Hkv + prm.rows_per_unit - 1) / prm.rows_per_unit;
+        prm.units = prm.q_units + (append ? 2 : 1) * prm.k_units;
+        if (steps == 1 || (int64_t)prm.T * prm.units >= 16 * sms) break;
+    }
+    const int64_t warps = (int64_t)prm.T * prm.units;
+    if (warps > INT32_MAX) return PKV_ERR_UNSUPPORTED;
+    const int grid = (int)((warps + kRopeThreads / 32 - 1) / (kRopeThreads / 32));
     cudaError_t e;
     if (dtype == PKV_DTYPE_BF16)
-        e = head_dim == 128 ? launch_rope_t<__nv_bfloat16, 8>(prm, interleaved, append, grid, smem, stream)
-                            : launch_rope_t<__nv_bfloat16, 4>(prm, interleaved, append, grid, smem, stream);
+        e = head_dim == 128 ? launch_rope_t<__nv_bfloat16, 8>(prm, interleaved, append, grid, stream)
+                            : launch_rope_t<__nv_bfloat16, 4>(prm, interleaved, append, grid, stream);
     else
-        e = head_dim == 128 ? launch_rope_t<__half, 8>(prm, interleaved, append, grid, smem, stream)
-                            : launch_rope_t<__half, 4>(prm, interleaved, append, grid, smem, stream);
+        e = head_dim == 128 ? launch_rope_t<__half, 8>(prm, interleaved, append, grid, stream)
+                            : launch_rope_t<__half, 4>(prm, interleaved, append, grid, stream);
     if (e == cudaSuccess) e = cudaGetLastError();
     return e == cudaSuccess ? PKV_OK : cuda_fail(e);
 }
