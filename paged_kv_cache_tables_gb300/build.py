@@ -18,7 +18,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libpkv.so")
 
 SOURCES = ["abi.cu", "append.cu", "decode.cu", "decode_static.cu", "prefill.cu", "prefill_tc.cu", "mixed.cu",
-           "tables.cu", "rope.cu", "window_decode.cu", "host_sched.cpp"]
+           "tables.cu", "rope.cu", "window_decode.cu", "window_prefill.cu", "host_sched.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -31,13 +31,6 @@
 //              16-bit (rounded value, rounding residual) pairs, which the MMA
 //              reads as its A operand straight from tensor memory.
 // While one tile's softmax runs, the tensor core works on the other tile.
-//
-// WINDOW (pkv_paged_window_prefill_attention): position p sees t <= p only if
-// t > p - window or t < sinks.  A pair of query tiles then walks the key tiles
-// of the first tokens and those from its first row's window on (tile j of the
-// walk is key tile j, or j + skip past the first tokens' tiles); a page that no
-// row of the pair sees is not read (its table entry may be anything) and
-// arrives as zeros.  Bound by the tensor pipe like the causal form.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -74,7 +67,6 @@ struct PrefillTcParams {
     int rtok, pairs_per_seq;
     float scale_log2;
     int out_dtype;
-    int window, sinks, total_q;   // WINDOW only
 };
 
 template <int D>
@@ -91,7 +83,7 @@ struct TcShape {
     static constexpr int SMEM_BYTES = 1024 + OFF_BAR + 256;
 };
 
-template <typename T, int D, bool WINDOW>
+template <typename T, int D>
 __global__ void __launch_bounds__(kTcThreads, 1)
     paged_prefill_tc_kernel(const PrefillTcParams p, const __grid_constant__ CUtensorMap tk,
                             const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tq) {
@@ -124,7 +116,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int q0 = __ldg(p.cu_seqlens + c);
     const int q_len = __ldg(p.cu_seqlens + c + 1) - q0;
     const int ctx = __ldg(p.context_lens + c);
-    if (q_len < 0 || q_len > ctx || (WINDOW && (q0 < 0 || q_len > p.total_q - q0))) {
+    if (q_len < 0 || q_len > ctx) {
         if (tid == 0 && pair == 0) set_status(p.dev_status, PKV_DEV_BAD_CHUNK);
         return;
     }
@@ -136,18 +128,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (i0 >= q_len) return;
     const int ntok = min(2 * p.rtok, q_len - i0);      // tokens of this pair (tile A first)
     const int prior = ctx - q_len;
+    const int ntiles = (prior + i0 + ntok - 1) / kTcKeys + 1;
     const int nblk = (ctx + 15) / 16;
-    // key tiles walked: all up to the last row's own, less those between the
-    // first tokens and the first row's window (its first position is wpos)
-    int ntiles = (prior + i0 + ntok - 1) / kTcKeys + 1;
-    int wpos = 0, sink_tiles = 0, skip = 0;
-    if constexpr (WINDOW) {
-        wpos = max(prior + i0 - p.window + 1, 0);
-        sink_tiles = min((p.sinks + kTcKeys - 1) / kTcKeys, ntiles);
-        skip = max(wpos / kTcKeys - sink_tiles, 0);
-        ntiles -= skip;
-    }
-    auto key_tile = [&](int j) { return WINDOW && j >= sink_tiles ? j + skip : j; };
 
     if (tid == 0) {
         mbar_init(q_full, 1);
@@ -183,13 +165,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // a slot becoming free and its copies starting
         constexpr int kPages = kTcKeys / 16;
         const int32_t *row = p.block_tables + (int64_t)c * p.max_blocks;
-        auto in_context = [&](int j) {
-            const int pg = key_tile(j) * kPages + lane;
-            bool in = lane < kPages && pg < nblk;
-            if constexpr (WINDOW) in = in && (pg * 16 + 15 >= wpos || pg * 16 < p.sinks);
-            return in;
-        };
-        auto fetch = [&](int j) { return in_context(j) ? __ldg(row + key_tile(j) * kPages + lane) : 0; };
+        auto in_context = [&](int jt) { return lane < kPages && jt * kPages + lane < nblk; };
+        auto fetch = [&](int jt) { return in_context(jt) ? __ldg(row + jt * kPages + lane) : 0; };
         int blk_next = fetch(0);
         if (lane == 0) {
             const int qrows = G * p.rtok;
@@ -325,8 +302,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int r = lane_base + lane;                 // row within the tile
         const int tok = t * p.rtok + r / G, head = r % G;
         const bool valid = r < G * p.rtok && tok < ntok;
-        // padding rows see every key (WINDOW: the last row's)
-        const int pos = valid ? prior + i0 + tok : (WINDOW ? prior + i0 + ntok - 1 : ctx - 1);
+        const int pos = valid ? prior + i0 + tok : ctx - 1;   // padding rows see every key
         const uint32_t trow = tmem + ((uint32_t)lane_base << 16) + t * 256;
         float m_used = -INFINITY, l = 0.f;
         const uint64_t scale2 = f2_pack(p.scale_log2, p.scale_log2);
@@ -338,7 +314,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 break;
             }
             tc::fence_after_sync();
-            const int key0 = key_tile(j) * kTcKeys;
+            const int key0 = j * kTcKeys;
             // one pass: the whole row of 128 scores in registers
             float v[kTcKeys];
 #pragma unroll
@@ -347,15 +323,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             tc::tmem_wait_ld();
             // causal mask, only on tiles that reach past some row's position
             const int lim = pos - key0;
-            if constexpr (WINDOW) {
-                // hidden below the row's window and behind the first tokens
-                const int low = lim - p.window + 1, sk = p.sinks - key0;
-                if (__any_sync(0xffffffffu, lim < kTcKeys - 1 || (low > 0 && sk < kTcKeys))) {
-#pragma unroll
-                    for (int e = 0; e < kTcKeys; ++e)
-                        if (e > lim || (e < low && e >= sk)) v[e] = -INFINITY;
-                }
-            } else if (__any_sync(0xffffffffu, lim < kTcKeys - 1)) {
+            if (__any_sync(0xffffffffu, lim < kTcKeys - 1)) {
 #pragma unroll
                 for (int e = 0; e < kTcKeys; ++e)
                     if (e > lim) v[e] = -INFINITY;
@@ -388,9 +356,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             // P = 2^(x - m_used) over the same columns, 32 keys at a time: 16
             // columns of rounded pairs, then 16 of residual pairs
-            // (a windowed row may have seen no key yet: nothing to subtract)
-            const float sub = WINDOW && m_used == -INFINITY ? 0.f : m_used;
-            const uint64_t negm2 = f2_pack(-sub, -sub);
+            const uint64_t negm2 = f2_pack(-m_used, -m_used);
             uint64_t sum2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
 #pragma unroll
             for (int cc = 0; cc < kTcKeys / 32; ++cc) {
@@ -418,14 +384,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             // anything: clear those V rows so 0 x garbage cannot reach O
             // (both tiles' warps write the same zeros before their product)
             const int zlo = max(ctx - key0, 0), zhi = min(kTcKeys, nblk * 16 - key0);
-            // WINDOW: and those of the keys that no row of the pair sees, in
-            // pages read for their neighbours
-            int ylo = 0, yhi = 0;
-            if constexpr (WINDOW) {
-                ylo = max(p.sinks - key0, 0);
-                yhi = min(wpos - key0, kTcKeys);
-            }
-            if (zlo < zhi || ylo < yhi) {
+            if (zlo < zhi) {
                 // V_j cannot be reloaded before this tile's P.V products,
                 // so the phase waited for here is this tile's
                 ok = mbar_wait(&v_full[j % kTcStages], (uint32_t)((j / kTcStages) & 1), kTcWaitNs);
@@ -433,7 +392,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     ok = false;
                     break;
                 }
-                if ((r >= zlo && r < zhi) || (WINDOW && r >= ylo && r < yhi)) {
+                if (r >= zlo && r < zhi) {
                     uint8_t *vrow = sm + Sh::OFF_KV + (j % kTcStages) * Sh::STAGE_BYTES + Sh::K_BYTES + r * 128;
 #pragma unroll
                     for (int hf = 0; hf < Sh::HALVES; ++hf)
@@ -501,7 +460,7 @@ static int encode_q_map(CUtensorMap *map, const void *q, int total_q, int Hq, in
     return encode_tiled_map(map, q, 3, dims, strides, box);
 }
 
-template <typename T, int D, bool WINDOW>
+template <typename T, int D>
 int launch_prefill_tc(const PrefillTcParams &prm, const CUtensorMap &tk, const CUtensorMap &tv,
                       const CUtensorMap &tq, int grid, cudaStream_t stream) {
     using Sh = TcShape<D>;
@@ -511,7 +470,7 @@ int launch_prefill_tc(const PrefillTcParams &prm, const CUtensorMap &tk, const C
     static int regs_ok = 0;   // 0 unknown, 1 as sized, -1 not
     if (regs_ok == 0) {
         cudaFuncAttributes fa;
-        cudaError_t e = cudaFuncGetAttributes(&fa, paged_prefill_tc_kernel<T, D, WINDOW>);
+        cudaError_t e = cudaFuncGetAttributes(&fa, paged_prefill_tc_kernel<T, D>);
         if (e != cudaSuccess) return cuda_fail(e);
         regs_ok = fa.numRegs == kTcLaunchRegs ? 1 : -1;
         if (regs_ok < 0) {
@@ -524,12 +483,12 @@ int launch_prefill_tc(const PrefillTcParams &prm, const CUtensorMap &tk, const C
     if (regs_ok < 0) return PKV_ERR_UNSUPPORTED;
     static unsigned long long attr_set = 0;   // per instantiation and device
     if (!done_on_device(&attr_set)) {
-        cudaError_t e = cudaFuncSetAttribute(paged_prefill_tc_kernel<T, D, WINDOW>,
+        cudaError_t e = cudaFuncSetAttribute(paged_prefill_tc_kernel<T, D>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::SMEM_BYTES);
         if (e != cudaSuccess) return cuda_fail(e);
         mark_done_on_device(&attr_set);
     }
-    cudaError_t e = launch_pdl(paged_prefill_tc_kernel<T, D, WINDOW>, dim3(grid), dim3(kTcThreads), Sh::SMEM_BYTES, stream,
+    cudaError_t e = launch_pdl(paged_prefill_tc_kernel<T, D>, dim3(grid), dim3(kTcThreads), Sh::SMEM_BYTES, stream,
                                prm, tk, tv, tq);
     if (e == cudaSuccess) e = cudaGetLastError();
     return e == cudaSuccess ? PKV_OK : cuda_fail(e);
@@ -538,7 +497,7 @@ int launch_prefill_tc(const PrefillTcParams &prm, const CUtensorMap &tk, const C
 int prefill_tc(void *out, const void *q, const int32_t *cu_seqlens, int num_seqs, int max_q_len, int total_q,
                const void *k_cache, const void *v_cache, const int32_t *block_tables, int max_blocks_per_seq,
                const int32_t *context_lens, int num_blocks, int Hq, int Hkv, int head_dim, float scale, int dtype,
-               int out_dtype, int *dev_status, cudaStream_t stream, int window, int sinks) {
+               int out_dtype, int *dev_status, cudaStream_t stream) {
     const int G = Hq / Hkv;
     const int rtok = kTcRows / G;
     const int pairs = (max_q_len + 2 * rtok - 1) / (2 * rtok);
@@ -568,22 +527,12 @@ int prefill_tc(void *out, const void *q, const int32_t *cu_seqlens, int num_seqs
     prm.pairs_per_seq = pairs;
     prm.scale_log2 = scale * 1.4426950408889634f;
     prm.out_dtype = out_dtype;
-    prm.window = window;
-    prm.sinks = sinks;
-    prm.total_q = total_q;
     const int grid = (int)grid64;
-    if (window > 0) {
-        if (dtype == PKV_DTYPE_BF16)
-            return head_dim == 128 ? launch_prefill_tc<__nv_bfloat16, 128, true>(prm, tk, tv, tq, grid, stream)
-                                   : launch_prefill_tc<__nv_bfloat16, 64, true>(prm, tk, tv, tq, grid, stream);
-        return head_dim == 128 ? launch_prefill_tc<__half, 128, true>(prm, tk, tv, tq, grid, stream)
-                               : launch_prefill_tc<__half, 64, true>(prm, tk, tv, tq, grid, stream);
-    }
     if (dtype == PKV_DTYPE_BF16)
-        return head_dim == 128 ? launch_prefill_tc<__nv_bfloat16, 128, false>(prm, tk, tv, tq, grid, stream)
-                               : launch_prefill_tc<__nv_bfloat16, 64, false>(prm, tk, tv, tq, grid, stream);
-    return head_dim == 128 ? launch_prefill_tc<__half, 128, false>(prm, tk, tv, tq, grid, stream)
-                           : launch_prefill_tc<__half, 64, false>(prm, tk, tv, tq, grid, stream);
+        return head_dim == 128 ? launch_prefill_tc<__nv_bfloat16, 128>(prm, tk, tv, tq, grid, stream)
+                               : launch_prefill_tc<__nv_bfloat16, 64>(prm, tk, tv, tq, grid, stream);
+    return head_dim == 128 ? launch_prefill_tc<__half, 128>(prm, tk, tv, tq, grid, stream)
+                           : launch_prefill_tc<__half, 64>(prm, tk, tv, tq, grid, stream);
 }
 
 }  // namespace pkv

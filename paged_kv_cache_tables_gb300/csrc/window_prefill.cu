@@ -1,0 +1,738 @@
+// Prefill attention over a sliding window and the first tokens of a paged
+// context, on the 5th-generation tensor cores (pkv_paged_window_prefill_attention).
+//
+// Mathematics.  Row i of chunk c sits at position p = ctx_c - q_len_c + i and
+// sees position t iff t <= p and (t > p - window or t < sinks).  Over key tiles
+// of 128 positions, with the running maximum m and sum l of the softmax in fp32:
+//     P = 2^(scale2 S - m),  l = l a + sum P,  O = O a + P V,  a = 2^(m_old - m),
+// where m only moves when a row's maximum grows by more than 2^8 (P and O stay
+// far inside fp32's range, and O is rarely touched).
+//
+// What is walked.  A unit of work is 2 x 128 MMA rows (two adjacent tiles A and B
+// of 128 / G tokens x the G query heads that share a KV head), against the
+// pages that one of its rows sees: those of the first tokens, then those from
+// its first row's window on, as one list of pages (page v of the list is logical
+// page v, or v + skip past the first tokens' pages) cut into key tiles of 8.
+// Positions past the first tokens' pages are kept less 16 skip throughout, so
+// that they count along the list.  Other pages are not read: their table
+// entries may be anything.
+//
+// Warps (persistent; 12 of them):
+//   0      TMA and scheduler: takes the CTA's units one after another (its own,
+//          then those of CTAs that have not been launched yet, which it cancels:
+//          clusterlaunchcontrol), publishes each unit's numbers in a ring of
+//          two, loads Q and the K / V tiles, 8 pages of 16 each, a page one box
+//   1, 2   issue the MMAs of query tile A, B: S = Q K^T (both operands in shared
+//          memory), O += P V (P in tensor memory over S), in two halves of the
+//          keys, the first while the softmax still works on the second
+//   3      clears V rows that no row of the unit sees, in pages read for their
+//          neighbours (they may hold anything, and 0 x NaN must not reach O)
+//   4-11   softmax: a warpgroup a query tile, a row per thread
+// While one tile's softmax runs, the tensor cores work on the other's products.
+// Loads, products and softmax run across the units: while a unit's outputs are
+// stored, the next one's Q, K and V arrive.
+//
+// P is rounded to 16 bits once when the output is 16 bits wide, an error of the
+// output's own kind: half a step of each weight (2^-8 sum p|v| for bf16, 2^-11
+// for fp16).  A 32-bit output gets a second product with the rounding residual.
+// PERF
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdio>
+#include <type_traits>
+
+#include "pkv.h"
+#include "pkv_device.cuh"
+#include "pkv_host.h"
+#include "pkv_tc.cuh"
+
+namespace pkv {
+
+constexpr int kWpThreads = 384;
+// registers per thread: the launch gives every thread kWpLaunchRegs; the first
+// warpgroup drops to kWpLowRegs and the two softmax warpgroups rise to
+// kWpHighRegs, which must not exceed what the drop frees
+constexpr int kWpLaunchRegs = 168;
+constexpr int kWpLowRegs = 88;
+constexpr int kWpHighRegs = 208;
+static_assert(128 * kWpLowRegs + 256 * kWpHighRegs <= kWpThreads * kWpLaunchRegs, "register split");
+constexpr int kWpRows = 128;    // MMA rows = (token, head) pairs per query tile
+constexpr int kWpKeys = 128;    // keys per K/V tile
+constexpr int kWpPages = kWpKeys / 16;
+constexpr int kWpStages = 2;
+constexpr uint64_t kWpWaitNs = 2000000000ull;
+// tensor memory: S / P of query tile t at column 256 t, O at 256 t + 128
+constexpr uint32_t kWpTmemCols = 512;
+
+struct WindowPrefillParams {
+    void *out;
+    const int32_t *cu_seqlens;
+    const int32_t *block_tables;
+    const int32_t *context_lens;
+    int *dev_status;
+    int max_blocks, num_blocks, Hq, Hkv, G;
+    int rtok, pairs_per_seq;
+    int window, sinks, total_q;
+    float scale_log2;
+    int out_dtype;
+};
+
+// One unit of work, as the scheduler publishes it (tiles == 0: no more).
+// Positions count along the list of pages.
+struct WpUnit {
+    int tiles;        // key tiles walked
+    int h, row0;      // KV head; first row of q / out
+    int tokens;       // rows of the unit (tile A first)
+    int first;        // position of the first row
+    int ctx;          // end of the context
+    int wpos;         // first position of the first row's window
+    int pad;
+};
+
+// Rows [a0, a1) and [b0, b1) of the key tile at key0 that no row of the unit
+// sees, in pages that are read: past the context, and between the first tokens
+// and the window.
+struct WpHidden {
+    int a0, a1, b0, b1;
+    __device__ __forceinline__ WpHidden(const WpUnit &u, int key0, int sinks, int keys)
+        : a0(max(u.ctx - key0, 0)), a1(min(keys, ((u.ctx + 15) & ~15) - key0)), b0(max(sinks - key0, 0)),
+          b1(min(u.wpos - key0, keys)) {}
+    __device__ __forceinline__ bool any() const { return a0 < a1 || b0 < b1; }
+    __device__ __forceinline__ bool has(int r) const { return (r >= a0 && r < a1) || (r >= b0 && r < b1); }
+};
+
+struct WpBars {
+    uint64_t unit_full[2], unit_empty[2], cancel;
+    uint64_t q_full, q_empty;
+    uint64_t k_full[kWpStages], v_full[kWpStages], k_empty[kWpStages], v_empty[kWpStages];
+    uint64_t v_clean[kWpStages];
+    uint64_t s_full[2], p_full[2][2], o_done[2];   // per query tile (and half of its keys)
+};
+
+// A K or V tile is its pages one after another; a page holds, for each group of
+// 8 rows, the 64-column halves of those rows, each an 8 x 128-byte swizzle atom.
+template <int D>
+struct WpShape {
+    static constexpr int HALVES = D / 64;
+    static constexpr int Q_HALF = kWpRows * 128;            // 128 rows x 64 columns
+    static constexpr int Q_BYTES = HALVES * Q_HALF;
+    static constexpr int GROUP = HALVES * 1024;             // 8 rows
+    static constexpr int PAGE = 2 * GROUP;
+    static constexpr int TILE = kWpPages * PAGE;
+    static constexpr int STAGE_BYTES = 2 * TILE;            // K then V
+    static constexpr int OFF_Q = 0;                         // tile A, then tile B
+    static constexpr int OFF_KV = 2 * Q_BYTES;
+    static constexpr int OFF_UNIT = OFF_KV + kWpStages * STAGE_BYTES;
+    static constexpr int OFF_CANCEL = OFF_UNIT + 2 * (int)sizeof(WpUnit);
+    static constexpr int OFF_BAR = OFF_CANCEL + 16;
+    static constexpr int SMEM_BYTES = 1024 + OFF_BAR + (int)sizeof(WpBars) + 16;
+};
+static_assert(WpShape<128>::SMEM_BYTES <= 227 * 1024, "shared memory");
+
+// One page of a cache (see encode_page_map) into shared memory.
+__device__ __forceinline__ void load_page(void *dst, const CUtensorMap *map, int group, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %2, %2, %3}], [%4];" ::"r"(smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(group), "r"(smem_addr(bar))
+        : "memory");
+}
+
+// Asks the hardware to give this CTA the place of one that has not been
+// launched; the answer (16 bytes) completes on `bar`.
+__device__ __forceinline__ void cancel_next_cta(void *answer, uint64_t *bar) {
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+            smem_addr(answer)),
+        "r"(smem_addr(bar))
+        : "memory");
+}
+
+// The place taken over (blockIdx.x), or -1: all CTAs have been launched.
+__device__ __forceinline__ int cancelled_cta(const void *answer) {
+    uint32_t ok, x;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b128 a;\n\t.reg .b32 y, z, w;\n\t"
+        "ld.shared.b128 a, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t"
+        "mov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, y, z, w}, a;\n\t}"
+        : "=r"(ok), "=r"(x)
+        : "r"(smem_addr(answer))
+        : "memory");
+    return ok ? (int)x : -1;
+}
+
+template <typename T, int D, bool RESIDUAL>
+__global__ void __launch_bounds__(kWpThreads, 1)
+    window_prefill_kernel(const WindowPrefillParams p, const __grid_constant__ CUtensorMap tk,
+                          const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tq) {
+    using Sh = WpShape<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    WpBars *bars = reinterpret_cast<WpBars *>(sm + Sh::OFF_BAR);
+    WpUnit *units = reinterpret_cast<WpUnit *>(sm + Sh::OFF_UNIT);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 1);
+    volatile int *gave_up = reinterpret_cast<volatile int *>(tmem_slot + 1);   // a wait of this CTA ran out
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars->unit_full[i], 1);
+            mbar_init(&bars->unit_empty[i], 11);   // warps 1 to 11
+            mbar_init(&bars->s_full[i], 1);
+            mbar_init(&bars->p_full[i][0], 4);
+            mbar_init(&bars->p_full[i][1], 4);
+            mbar_init(&bars->o_done[i], 1);
+        }
+        mbar_init(&bars->cancel, 1);
+        mbar_init(&bars->q_full, 1);
+        mbar_init(&bars->q_empty, 2);   // both query tiles' products
+        for (int s = 0; s < kWpStages; ++s) {
+            mbar_init(&bars->k_full[s], 1);
+            mbar_init(&bars->v_full[s], 1);
+            mbar_init(&bars->k_empty[s], 2);
+            mbar_init(&bars->v_empty[s], 2);
+            mbar_init(&bars->v_clean[s], 1);
+        }
+        *gave_up = 0;
+        fence_mbar_init();
+        prefetch_tensormap(&tq);
+        prefetch_tensormap(&tk);
+        prefetch_tensormap(&tv);
+    }
+    if (warp == 1) {
+        tc::tmem_alloc(tmem_slot, kWpTmemCols);
+        tc::tmem_relinquish();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t sbase = smem_addr(sm);
+    // inputs may come from the previous kernel on the stream (the append)
+    pdl_wait_primary();
+    pdl_launch_dependents();
+
+    // A wait that gives up after kWpWaitNs, or once another one of the CTA has.
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+        if (mbar_try_wait(bar, parity & 1u)) return true;
+        const uint64_t t0 = global_timer_ns();
+        while (!mbar_try_wait(bar, parity & 1u)) {
+            if (*gave_up) return false;
+            if (global_timer_ns() - t0 > kWpWaitNs) {
+                *gave_up = 1;
+                set_status(p.dev_status, PKV_DEV_WAIT_TIMEOUT);
+                return false;
+            }
+        }
+        return true;
+    };
+    auto wait_all = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)); };
+
+    if (warp < 4) {
+        tc::setmaxnreg_dec<kWpLowRegs>();
+        if (warp == 0) {
+            // ---------------- scheduler and TMA producer ----------------
+            int place = blockIdx.x;
+            int n = 0;              // units published
+            uint32_t g = 0;         // key tiles loaded
+            uint32_t asked = 0;     // places asked for
+            bool ok = true;
+            while (ok) {
+                // the next place is asked for while this one is worked on
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&bars->cancel, 16);
+                    cancel_next_cta(sm + Sh::OFF_CANCEL, &bars->cancel);
+                }
+                ++asked;
+                // place -> unit; chunk by chunk, the last pair of tiles first, the KV heads side by side
+                const int h = place % p.Hkv;
+                const int rest = place / p.Hkv;
+                const int pair = p.pairs_per_seq - 1 - rest % p.pairs_per_seq;
+                const int c = rest / p.pairs_per_seq;
+                const int q0 = __ldg(p.cu_seqlens + c);
+                const int q_len = __ldg(p.cu_seqlens + c + 1) - q0;
+                const int ctx = __ldg(p.context_lens + c);
+                const int i0 = pair * 2 * p.rtok;
+                int bad = 0;
+                if (q_len < 0 || q_len > ctx || q0 < 0 || q_len > p.total_q - q0)
+                    bad = PKV_DEV_BAD_CHUNK;
+                else if (ctx > p.max_blocks * 16)
+                    bad = PKV_DEV_BAD_CONTEXT;
+                if (bad && pair == 0 && lane == 0) set_status(p.dev_status, bad);
+                if (!bad && i0 < q_len) {
+                    WpUnit u = {};
+                    u.h = h;
+                    u.row0 = q0 + i0;
+                    u.tokens = min(2 * p.rtok, q_len - i0);
+                    u.first = ctx - q_len + i0;
+                    u.wpos = max(u.first - p.window + 1, 0);
+                    const int sink_pages = min((p.sinks + 15) / 16, (ctx + 15) / 16);
+                    const int skip = max(u.wpos / 16 - sink_pages, 0);
+                    u.first -= 16 * skip;
+                    u.wpos -= 16 * skip;
+                    u.ctx = ctx - 16 * skip;
+                    u.tiles = (u.first + u.tokens - 1) / kWpKeys + 1;
+                    if (n >= 2) ok = wait_all(&bars->unit_empty[n & 1], (uint32_t)(n / 2 - 1));
+                    if (!ok) break;
+                    if (lane == 0) {
+                        units[n & 1] = u;
+                        tc::mbar_arrive_cta(&bars->unit_full[n & 1]);
+                    }
+                    const int32_t *row = p.block_tables + (int64_t)c * p.max_blocks;
+                    const int pages = (u.ctx + 15) / 16;
+                    // lane i < 8 reads the block id of page i of the tile, one tile ahead
+                    auto wanted = [&](int j) { return lane < kWpPages && j * kWpPages + lane < pages; };
+                    auto fetch = [&](int j) {
+                        const int v = j * kWpPages + lane;
+                        return wanted(j) ? __ldg(row + (v < sink_pages ? v : v + skip)) : 0;
+                    };
+                    int blk_next = fetch(0);
+                    for (int j = 0; ok && j < u.tiles; ++j, ++g) {
+                        const int blk = blk_next;
+                        if (j + 1 < u.tiles) blk_next = fetch(j + 1);
+                        int y = p.num_blocks * p.Hkv * 2;      // 8-row group past the pool: zero fill
+                        if (wanted(j)) {
+                            if (blk >= 0 && blk < p.num_blocks)
+                                y = (blk * p.Hkv + h) * 2;
+                            else
+                                set_status(p.dev_status, PKV_DEV_BAD_BLOCK_ID);
+                        }
+                        int ys[kWpPages];
+#pragma unroll
+                        for (int pg = 0; pg < kWpPages; ++pg) ys[pg] = __shfl_sync(0xffffffffu, y, pg);
+                        const int st = (int)(g % kWpStages);
+                        uint8_t *kd = sm + Sh::OFF_KV + st * Sh::STAGE_BYTES, *vd = kd + Sh::TILE;
+                        if (lane == 0) {
+                            // a K slot is free once both S products of its last tile are done
+                            if (g >= kWpStages) ok = wait(&bars->k_empty[st], g / kWpStages - 1);
+                            if (ok) {
+                                mbar_arrive_expect_tx(&bars->k_full[st], Sh::TILE);
+#pragma unroll
+                                for (int pg = 0; pg < kWpPages; ++pg)
+                                    load_page(kd + pg * Sh::PAGE, &tk, ys[pg], &bars->k_full[st]);
+                            }
+                            if (ok && j == 0) {
+                                // Q is free once the unit before has no S product left
+                                if (n > 0) ok = wait(&bars->q_empty, (uint32_t)(n - 1));
+                                if (ok) {
+                                    mbar_arrive_expect_tx(&bars->q_full, (uint32_t)(2 * Sh::HALVES * p.G * p.rtok * 128));
+#pragma unroll
+                                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                                        for (int hf = 0; hf < Sh::HALVES; ++hf)
+                                            tc::tma_load_3d(sm + Sh::OFF_Q + t * Sh::Q_BYTES + hf * Sh::Q_HALF, &tq, hf * 64,
+                                                            h * p.G, u.row0 + t * p.rtok, &bars->q_full);
+                                }
+                            }
+                            // a V slot is free once both P V products of its last tile are done
+                            if (ok && g >= kWpStages) ok = wait(&bars->v_empty[st], g / kWpStages - 1);
+                            if (ok) {
+                                mbar_arrive_expect_tx(&bars->v_full[st], Sh::TILE);
+#pragma unroll
+                                for (int pg = 0; pg < kWpPages; ++pg)
+                                    load_page(vd + pg * Sh::PAGE, &tv, ys[pg], &bars->v_full[st]);
+                            }
+                        }
+                        ok = __shfl_sync(0xffffffffu, ok, 0);
+                    }
+                    ++n;
+                }
+                if (!ok) break;
+                // the place asked for
+                ok = wait_all(&bars->cancel, asked - 1);
+                if (!ok) break;
+                place = cancelled_cta(sm + Sh::OFF_CANCEL);
+                fence_proxy_async_smem();   // the answer is read before the next one is written
+                __syncwarp();
+                if (place < 0) break;
+            }
+            // no more units (after a wait that ran out the others leave by themselves)
+            if (ok && n >= 2) ok = wait_all(&bars->unit_empty[n & 1], (uint32_t)(n / 2 - 1));
+            if (ok && lane == 0) {
+                units[n & 1].tiles = 0;
+                tc::mbar_arrive_cta(&bars->unit_full[n & 1]);
+            }
+            if (!ok && lane == 0) {
+                // what is under way must land before the CTA leaves
+                mbar_wait(&bars->cancel, (asked - 1) & 1u, kWpWaitNs / 8);
+                for (int st = 0; st < kWpStages; ++st) {
+                    if (g > (uint32_t)st) {
+                        const uint32_t last = (g - 1 - st) / kWpStages;
+                        mbar_wait(&bars->k_full[st], last & 1u, kWpWaitNs / 8);
+                        mbar_wait(&bars->v_full[st], last & 1u, kWpWaitNs / 8);
+                    }
+                }
+                if (n > 0) mbar_wait(&bars->q_full, (uint32_t)(n - 1) & 1u, kWpWaitNs / 8);
+            }
+        } else if (warp < 3) {
+            // ---------------- MMA issuer of query tile t ----------------
+            // The whole warp walks the schedule, so the waits and the
+            // descriptor arithmetic are warp-uniform; one elected lane issues
+            // each MMA and commit.
+            const int t = warp - 1;
+            const bool leader = tc::elect_one();
+            constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+            constexpr uint32_t idesc_s = tc::idesc_f16(kBf16, false, false, kWpRows, kWpKeys);
+            constexpr uint32_t idesc_o = tc::idesc_f16(kBf16, false, true, kWpRows, D);
+            const uint32_t d_s = tmem + t * 256, d_o = d_s + 128;
+            const uint64_t q_desc = tc::smem_desc_sw128(sbase + Sh::OFF_Q + t * Sh::Q_BYTES, 16, 1024);
+            const uint64_t k_desc = tc::smem_desc_sw128(sbase + Sh::OFF_KV, 16, Sh::GROUP);
+            const uint64_t v_desc = tc::smem_desc_sw128(sbase + Sh::OFF_KV + Sh::TILE, 1024, Sh::GROUP);
+            uint32_t g = 0;     // key tiles done
+            auto issue_s = [&](uint32_t k, bool last) {   // S = Q K^T of key tile k, the unit's last?
+                if (!wait_all(&bars->k_full[k % kWpStages], k / kWpStages)) return false;
+                tc::fence_after_sync();
+                const uint64_t kb = k_desc + (uint64_t)(((k % kWpStages) * Sh::STAGE_BYTES) >> 4);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t qo = ((kk >> 2) * Sh::Q_HALF + (kk & 3) * 32) >> 4;
+                    const uint32_t ko = ((kk >> 2) * 1024 + (kk & 3) * 32) >> 4;
+                    if (leader) tc::mma_f16_ss(d_s, q_desc + qo, kb + ko, idesc_s, kk > 0);
+                }
+                if (leader) {
+                    tc::mma_commit(&bars->s_full[t]);
+                    tc::mma_commit(&bars->k_empty[k % kWpStages]);
+                    if (last) tc::mma_commit(&bars->q_empty);
+                }
+                return true;
+            };
+            for (int n = 0;; ++n) {
+                bool ok = wait_all(&bars->unit_full[n & 1], (uint32_t)(n / 2));
+                if (!ok) break;
+                const WpUnit u = units[n & 1];
+                const int tiles = u.tiles;
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive_cta(&bars->unit_empty[n & 1]);
+                if (tiles == 0) break;
+                // (S may be written: the product that read P over it was issued before)
+                ok = wait_all(&bars->q_full, (uint32_t)n) && issue_s(g, tiles == 1);
+                for (int j = 0; ok && j < tiles; ++j, ++g) {
+                    const uint64_t vb = v_desc + (uint64_t)(((g % kWpStages) * Sh::STAGE_BYTES) >> 4);
+                    const bool dirty = WpHidden(u, j * kWpKeys, p.sinks, kWpKeys).any();
+                    ok = wait_all(dirty ? &bars->v_clean[g % kWpStages] : &bars->v_full[g % kWpStages], g / kWpStages);
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        // P of a unit's first tile is there only after the unit before's O was read
+                        ok = ok && wait_all(&bars->p_full[t][half], g);
+                        if (!ok) break;
+                        tc::fence_after_sync();
+#pragma unroll
+                        for (int i = 0; i < kWpPages / 2; ++i) {   // O (+)= P V, a page at a time
+                            const int kk = half * (kWpPages / 2) + i;
+                            const uint32_t ph = d_s + 32 * (kk >> 1) + 8 * (kk & 1);
+                            const uint64_t vp = vb + (uint32_t)(kk * Sh::PAGE >> 4);
+                            if (leader) {
+                                tc::mma_f16_ts(d_o, ph, vp, idesc_o, j > 0 || kk > 0);
+                                if constexpr (RESIDUAL) tc::mma_f16_ts(d_o, ph + 16, vp, idesc_o, true);
+                            }
+                        }
+                    }
+                    if (!ok) break;
+                    if (leader) {
+                        tc::mma_commit(&bars->v_empty[g % kWpStages]);
+                        if (j + 1 == tiles) tc::mma_commit(&bars->o_done[t]);
+                    }
+                    if (j + 1 < tiles) ok = issue_s(g + 1, j + 2 == tiles);
+                }
+                if (!ok) break;
+            }
+        }
+        else {
+            // ---------------- cleaner of V ----------------
+            uint32_t g = 0;
+            bool ok = true;
+            for (int n = 0; ok; ++n) {
+                ok = wait_all(&bars->unit_full[n & 1], (uint32_t)(n / 2));
+                if (!ok) break;
+                const WpUnit u = units[n & 1];
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive_cta(&bars->unit_empty[n & 1]);
+                if (u.tiles == 0) break;
+                for (int j = 0; ok && j < u.tiles; ++j, ++g) {
+                    const int st = (int)(g % kWpStages);
+                    ok = wait_all(&bars->v_full[st], g / kWpStages);
+                    const WpHidden hid(u, j * kWpKeys, p.sinks, kWpKeys);
+                    if (hid.any()) {
+                        // four rows at a time, eight lanes a 128-byte row half
+                        uint8_t *v = sm + Sh::OFF_KV + st * Sh::STAGE_BYTES + Sh::TILE + (lane & 7) * 16;
+                        for (int r = lane >> 3; r < kWpKeys; r += 4)
+                            if (hid.has(r))
+#pragma unroll
+                                for (int hf = 0; hf < Sh::HALVES; ++hf)
+                                    *reinterpret_cast<uint4 *>(v + (r >> 3) * Sh::GROUP + hf * 1024 + (r & 7) * 128) =
+                                        make_uint4(0u, 0u, 0u, 0u);
+                        fence_proxy_async_smem();
+                    }
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive_cta(&bars->v_clean[st]);
+                }
+            }
+        }
+    } else {
+        tc::setmaxnreg_inc<kWpHighRegs>();
+        // ---------------- softmax: tile t, one row per thread ----------------
+        const int t = (warp - 4) >> 2;
+        const int lane_base = 32 * (warp & 3);          // tensor-memory lanes this warp may touch
+        const int r = lane_base + lane;                 // row within the tile
+        const uint32_t scol = tmem + ((uint32_t)lane_base << 16) + t * 256;   // the scores, then P
+        const uint32_t ocol = scol + 128;
+        const uint64_t scale2 = f2_pack(p.scale_log2, p.scale_log2);
+        uint32_t g = 0;                                 // key tiles taken
+        bool ok = true;
+        for (int n = 0; ok; ++n) {
+            ok = wait_all(&bars->unit_full[n & 1], (uint32_t)(n / 2));
+            if (!ok) break;
+            const WpUnit u = units[n & 1];
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive_cta(&bars->unit_empty[n & 1]);
+            if (u.tiles == 0) break;
+            const int tok = t * p.rtok + r / p.G, head = r % p.G;
+            const bool valid = r < p.G * p.rtok && tok < u.tokens;
+            const int pos = u.first + (valid ? tok : u.tokens - 1);   // padding rows see the last row's keys
+            float m_used = -INFINITY, l = 0.f;
+            for (int j = 0; j < u.tiles; ++j, ++g) {
+                ok = wait_all(&bars->s_full[t], g);
+                if (!ok) break;
+                tc::fence_after_sync();
+                const int key0 = j * kWpKeys;
+                float v[kWpKeys];
+#pragma unroll
+                for (int cc = 0; cc < kWpKeys; cc += 32) tc::tmem_ld32(scol + cc, *reinterpret_cast<float(*)[32]>(v + cc));
+                tc::tmem_wait_ld();
+                // hidden: past the row's position; below its window and behind the first tokens
+                const int lim = pos - key0, low = lim - p.window + 1, sk = p.sinks - key0;
+                if (__any_sync(0xffffffffu, lim < kWpKeys - 1 || (low > 0 && sk < kWpKeys))) {
+                    auto below = [](int n) { return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u); };
+#pragma unroll
+                    for (int cc = 0; cc < kWpKeys; cc += 32) {
+                        const uint32_t see = below(lim + 1 - cc) & (~below(low - cc) | below(sk - cc));
+                        if (__any_sync(0xffffffffu, see != 0xffffffffu)) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (!(see & (1u << e))) v[cc + e] = -INFINITY;
+                        }
+                    }
+                }
+                float mx4[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+                for (int pr = 0; pr < (kWpKeys - 4) / 2; ++pr)
+                    mx4[pr & 3] = fmax3(mx4[pr & 3], v[4 + 2 * pr], v[5 + 2 * pr]);
+                // scale_log2 > 0, so the scaled maximum is the maximum scaled
+                const float mx = fmax3(fmaxf(mx4[0], mx4[1]), mx4[2], mx4[3]) * p.scale_log2;
+                const bool first = m_used == -INFINITY;
+                const float m_new = fmaxf(m_used, mx);
+                const bool rescale = !first && m_new > m_used + 8.f;
+                const float alpha = rescale ? exp2_approx(m_used - m_new) : 1.f;
+                if (first || rescale) m_used = m_new;
+                // O was last written by the P V product before, which the tensor
+                // core finished before this tile's S (issued after it) completed
+                if (__any_sync(0xffffffffu, rescale)) {
+#pragma unroll 1
+                    for (int cc = 0; cc < D; cc += 32) {
+                        float o[32];
+                        tc::tmem_ld32(ocol + cc, o);
+                        tc::tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] *= alpha;
+                        tc::tmem_st32(ocol + cc, o);
+                    }
+                }
+                // P = 2^(x - m_used) over the same columns, 32 keys at a time: 16
+                // columns of rounded pairs, then (RESIDUAL) 16 of residual pairs.
+                // A row that has seen no key yet has nothing to subtract.
+                const float sub = m_used == -INFINITY ? 0.f : m_used;
+                const uint64_t negm2 = f2_pack(-sub, -sub);
+                uint64_t sum2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+#pragma unroll
+                for (int cc = 0; cc < kWpKeys / 32; ++cc) {
+                    uint32_t hi[16], lo[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        float a, b;
+                        f2_unpack(f2_fma(f2_pack(v[32 * cc + 2 * e], v[32 * cc + 2 * e + 1]), scale2, negm2), a, b);
+                        a = exp2_approx(a);
+                        b = exp2_approx(b);
+                        const uint64_t ab = f2_pack(a, b);
+                        sum2[e & 1] = f2_add(sum2[e & 1], ab);
+                        if constexpr (RESIDUAL)
+                            pack2_split2<T>(ab, a, b, hi[e], lo[e]);
+                        else
+                            hi[e] = pack2<T>(a, b);
+                    }
+                    tc::tmem_st16(scol + cc * 32, hi);
+                    if constexpr (RESIDUAL) tc::tmem_st16(scol + cc * 32 + 16, lo);
+                    if (cc % 2 == 1) {   // half of the keys are ready
+                        tc::tmem_wait_st();
+                        tc::fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) tc::mbar_arrive_cta(&bars->p_full[t][cc / 2]);
+                    }
+                }
+                float s0, s1, s2, s3;
+                f2_unpack(sum2[0], s0, s1);
+                f2_unpack(sum2[1], s2, s3);
+                l = l * alpha + ((s0 + s1) + (s2 + s3));
+            }
+            ok = ok && wait_all(&bars->o_done[t], (uint32_t)n);
+            if (!ok) break;
+            tc::fence_after_sync();
+            const float inv = 1.f / l;
+            const int64_t ob = ((int64_t)(u.row0 + tok) * p.Hq + (int64_t)u.h * p.G + head) * D;
+#pragma unroll 1
+            for (int cc = 0; cc < D; cc += 32) {
+                float v[32];
+                tc::tmem_ld32(ocol + cc, v);
+                tc::tmem_wait_ld();
+                if (valid) {
+                    if constexpr (RESIDUAL) {   // a 32-bit output
+                        float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(p.out) + ob + cc);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            dst[e] = make_float4(v[4 * e] * inv, v[4 * e + 1] * inv, v[4 * e + 2] * inv, v[4 * e + 3] * inv);
+                    } else {
+                        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<T *>(p.out) + ob + cc);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            dst[e] = make_uint4(pack2<T>(v[8 * e] * inv, v[8 * e + 1] * inv),
+                                                pack2<T>(v[8 * e + 2] * inv, v[8 * e + 3] * inv),
+                                                pack2<T>(v[8 * e + 4] * inv, v[8 * e + 5] * inv),
+                                                pack2<T>(v[8 * e + 6] * inv, v[8 * e + 7] * inv));
+                    }
+                }
+            }
+            // O has been read: ordered before this unit's successor's P, whose
+            // arrival lets the tensor core write O again
+            tc::fence_before_sync();
+        }
+    }
+
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == 1) {
+        tc::fence_after_sync();
+        tc::tmem_dealloc(tmem, kWpTmemCols);
+    }
+}
+
+// A cache as (64 columns, 8 rows, column halves, groups of 8 rows): a box of two
+// groups is one (block, KV head) page in the order of WpShape, in one load.
+// Groups past the pool read 0.
+static int encode_page_map(CUtensorMap *map, const void *base, int num_blocks, int num_kv_heads, int head_dim) {
+    const uint64_t row = (uint64_t)head_dim * 2;
+    const uint64_t dims[4] = {64, 8, (uint64_t)head_dim / 64, (uint64_t)num_blocks * num_kv_heads * 2};
+    const uint64_t strides[3] = {row, 128, 8 * row};
+    const uint32_t box[4] = {64, 8, (uint32_t)head_dim / 64, 2};
+    return encode_tiled_map(map, base, 4, dims, strides, box);
+}
+
+template <typename T, int D, bool RESIDUAL>
+static int launch_window_prefill(const WindowPrefillParams &prm, const CUtensorMap &tk, const CUtensorMap &tv,
+                                 const CUtensorMap &tq, int grid, cudaStream_t stream) {
+    using Sh = WpShape<D>;
+    // the register split inside the kernel waits for registers that only exist
+    // if the compiled count is the one it was sized for: check it (once; the
+    // answer does not change) and refuse to launch otherwise
+    static int regs_ok = 0;   // 0 unknown, 1 as sized, -1 not
+    if (regs_ok == 0) {
+        cudaFuncAttributes fa;
+        cudaError_t e = cudaFuncGetAttributes(&fa, window_prefill_kernel<T, D, RESIDUAL>);
+        if (e != cudaSuccess) return cuda_fail(e);
+        regs_ok = fa.numRegs == kWpLaunchRegs ? 1 : -1;
+        if (regs_ok < 0) {
+            char msg[128];
+            std::snprintf(msg, sizeof msg, "window prefill kernel compiled to %d registers per thread, its split needs %d",
+                          fa.numRegs, kWpLaunchRegs);
+            set_error_message(msg);
+        }
+    }
+    if (regs_ok < 0) return PKV_ERR_UNSUPPORTED;
+    static unsigned long long attr_set = 0;   // per instantiation and device
+    if (!done_on_device(&attr_set)) {
+        cudaError_t e = cudaFuncSetAttribute(window_prefill_kernel<T, D, RESIDUAL>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::SMEM_BYTES);
+        if (e != cudaSuccess) return cuda_fail(e);
+        mark_done_on_device(&attr_set);
+    }
+    cudaError_t e = launch_pdl(window_prefill_kernel<T, D, RESIDUAL>, dim3(grid), dim3(kWpThreads), Sh::SMEM_BYTES, stream,
+                               prm, tk, tv, tq);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    return e == cudaSuccess ? PKV_OK : cuda_fail(e);
+}
+
+}  // namespace pkv
+
+extern "C" int pkv_paged_window_prefill_attention(void *out, const void *q, const int32_t *cu_seqlens, int num_seqs,
+                                                  int max_q_len, int total_q, const void *k_cache, const void *v_cache,
+                                                  const int32_t *block_tables, int max_blocks_per_seq,
+                                                  const int32_t *context_lens, int num_blocks, int num_q_heads,
+                                                  int num_kv_heads, int head_dim, int block_size, int window,
+                                                  int num_sinks, float scale, int dtype, int out_dtype, int *dev_status,
+                                                  void *stream) {
+    pkv::NvtxRange nvtx_range("pkv_paged_window_prefill_attention");
+    using namespace pkv;
+    if (num_seqs < 0 || max_q_len < 0 || total_q < 0 || num_blocks <= 0 || num_kv_heads <= 0 || num_q_heads <= 0 ||
+        max_blocks_per_seq <= 0 || window <= 0 || num_sinks < 0)
+        return PKV_ERR_INVALID_ARG;
+    if (num_q_heads % num_kv_heads != 0) return PKV_ERR_INVALID_ARG;
+    const int G = num_q_heads / num_kv_heads;
+    if (G > 16 || block_size != 16 || (head_dim != 64 && head_dim != 128)) return PKV_ERR_UNSUPPORTED;
+    if (dtype != PKV_DTYPE_F16 && dtype != PKV_DTYPE_BF16) return PKV_ERR_UNSUPPORTED;
+    if (out_dtype != dtype && out_dtype != PKV_DTYPE_F32) return PKV_ERR_UNSUPPORTED;
+    if (!(std::isfinite(scale) && scale > 0.f)) return PKV_ERR_INVALID_ARG;
+    if ((int64_t)num_blocks * num_kv_heads * block_size >= (int64_t)1 << 31) return PKV_ERR_UNSUPPORTED;
+    if (max_blocks_per_seq > (1 << 26)) return PKV_ERR_UNSUPPORTED;
+    if (num_seqs == 0 || max_q_len == 0 || total_q == 0) return PKV_OK;
+    if (!out || !q || !cu_seqlens || !k_cache || !v_cache || !block_tables || !context_lens) return PKV_ERR_INVALID_ARG;
+    // the query tile is fetched by TMA and output rows are stored as 16-byte vectors
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+        !aligned(cu_seqlens, 4) || !aligned(block_tables, 4) || !aligned(context_lens, 4))
+        return PKV_ERR_INVALID_ARG;
+    const int rtok = kWpRows / G;
+    const int pairs = (int)(((int64_t)max_q_len + 2 * rtok - 1) / (2 * rtok));
+    const int64_t grid = (int64_t)num_seqs * pairs * num_kv_heads;
+    if (grid >= (int64_t)1 << 31) return PKV_ERR_UNSUPPORTED;
+    CUtensorMap tk, tv, tq;
+    int rc = encode_page_map(&tk, k_cache, num_blocks, num_kv_heads, head_dim);
+    if (rc != PKV_OK) return rc;
+    rc = encode_page_map(&tv, v_cache, num_blocks, num_kv_heads, head_dim);
+    if (rc != PKV_OK) return rc;
+    // q as [total_q][Hq][head_dim]: a box of 64 columns x G heads x rtok tokens; rows past total_q read 0
+    const uint64_t dims[3] = {(uint64_t)head_dim, (uint64_t)num_q_heads, (uint64_t)total_q};
+    const uint64_t strides[2] = {(uint64_t)head_dim * 2, (uint64_t)num_q_heads * head_dim * 2};
+    const uint32_t box[3] = {64, (uint32_t)G, (uint32_t)rtok};
+    rc = encode_tiled_map(&tq, q, 3, dims, strides, box);
+    if (rc != PKV_OK) return rc;
+    WindowPrefillParams prm;
+    prm.out = out;
+    prm.cu_seqlens = cu_seqlens;
+    prm.block_tables = block_tables;
+    prm.context_lens = context_lens;
+    prm.dev_status = dev_status;
+    prm.max_blocks = max_blocks_per_seq;
+    prm.num_blocks = num_blocks;
+    prm.Hq = num_q_heads;
+    prm.Hkv = num_kv_heads;
+    prm.G = G;
+    prm.rtok = rtok;
+    prm.pairs_per_seq = pairs;
+    const int64_t capacity = (int64_t)max_blocks_per_seq * 16;
+    prm.window = window < capacity ? window : (int)capacity;   // no context is longer
+    prm.sinks = num_sinks < capacity ? num_sinks : (int)capacity;
+    prm.total_q = total_q;
+    prm.scale_log2 = scale * 1.4426950408889634f;
+    prm.out_dtype = out_dtype;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    auto launch = [&](auto type, auto residual) {
+        using T = decltype(type);
+        constexpr bool R = decltype(residual)::value;
+        return head_dim == 128 ? launch_window_prefill<T, 128, R>(prm, tk, tv, tq, (int)grid, st)
+                               : launch_window_prefill<T, 64, R>(prm, tk, tv, tq, (int)grid, st);
+    };
+    if (out_dtype == PKV_DTYPE_F32)
+        return dtype == PKV_DTYPE_BF16 ? launch(__nv_bfloat16(), std::true_type()) : launch(__half(), std::true_type());
+    return dtype == PKV_DTYPE_BF16 ? launch(__nv_bfloat16(), std::false_type()) : launch(__half(), std::false_type());
+}

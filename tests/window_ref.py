@@ -11,6 +11,12 @@ value plus residual (2 half steps of 2^-8: 2^-16 for bf16, less for fp16), exp2
 of 2^-24 at most: 2^-14; an fp32 sum of n terms in a chain).  The output's own
 rounding to 16 bits is half a step, eps / 2 relative, or half the smallest
 subnormal.
+
+Prefill with a 16-bit output rounds the weights to that type once (no residual):
+2^x of scores relative to a maximum that the row's own has reached or passed, so
+the largest weight, and with it the sum, is at least 1.  A weight w then moves by
+at most eps / 2 w, or half the smallest subnormal, and the output by at most
+eps / 2 sum p |v| + TINY / 2 sum |v| (the sum is taken of the unrounded weights).
 """
 import numpy as np
 import torch
@@ -53,9 +59,12 @@ def attend(q, first, keys, values, window, sinks, scale):
     return out.reshape(R, Hq, d), spread.reshape(R, Hq, d), mass.reshape(R, Hq, 1)
 
 
-def attention_bound(out, spread, mass, d, scale, out_dtype):
+def attention_bound(out, spread, mass, d, scale, out_dtype, weights=None):
+    """weights: (type the weights are rounded to, a bound on sum |v|), or None for value and residual."""
     ds = d * 2.0 ** -23 * mass * scale
     err = (2 * ds + 2.0 ** -16 + 2.0 ** -22 + 2.0 ** -14) * spread
+    if weights is not None:
+        err = err + EPS[weights[0]] / 2 * spread + TINY[weights[0]] / 2 * weights[1]
     return err + rounding(out, err, out_dtype)
 
 
