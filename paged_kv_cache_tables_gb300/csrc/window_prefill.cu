@@ -23,7 +23,7 @@
 //          clusterlaunchcontrol), publishes each unit's numbers in a ring of
 //          two, loads Q and the K / V tiles, 8 pages of 16 each, a page one box
 //   1, 2   issue the MMAs of query tile A, B: S = Q K^T (both operands in shared
-//          memory), O += P V (P in tensor memory over S), in two halves of the
+//          memory), O += P V (P in tensor memory over S), in two parts of the
 //          keys, the first while the softmax still works on the second
 //   3      clears V rows that no row of the unit sees, in pages read for their
 //          neighbours (they may hold anything, and 0 x NaN must not reach O)
@@ -107,7 +107,7 @@ struct WpBars {
     uint64_t q_full, q_empty;
     uint64_t k_full[kWpStages], v_full[kWpStages], k_empty[kWpStages], v_empty[kWpStages];
     uint64_t v_clean[kWpStages];
-    uint64_t s_full[2], p_full[2][2], o_done[2];   // per query tile (and half of its keys)
+    uint64_t s_full[2], p_full[2][2], o_done[2];   // per query tile (and part of its keys)
 };
 
 // A K or V tile is its pages one after another; a page holds, for each group of
@@ -121,6 +121,11 @@ struct WpShape {
     static constexpr int PAGE = 2 * GROUP;
     static constexpr int TILE = kWpPages * PAGE;
     static constexpr int STAGE_BYTES = 2 * TILE;            // K then V
+    // 32-key groups of P after which the first part of P V starts.  Three
+    // chunks of 3,500-4,100 rows, window 4,096: 614 us after one group, 571
+    // after two, 515 after three, 677 after all four (head_dim 128); 440, 414,
+    // 431 and 504 us (head_dim 64).
+    static constexpr int FIRST_PART = D == 128 ? 3 : 2;
     static constexpr int OFF_Q = 0;                         // tile A, then tile B
     static constexpr int OFF_KV = 2 * Q_BYTES;
     static constexpr int OFF_UNIT = OFF_KV + kWpStages * STAGE_BYTES;
@@ -415,14 +420,14 @@ __global__ void __launch_bounds__(kWpThreads, 1)
                     const bool dirty = WpHidden(u, j * kWpKeys, p.sinks, kWpKeys).any();
                     ok = wait_all(dirty ? &bars->v_clean[g % kWpStages] : &bars->v_full[g % kWpStages], g / kWpStages);
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
+                    for (int part = 0; part < 2; ++part) {
                         // P of a unit's first tile is there only after the unit before's O was read
-                        ok = ok && wait_all(&bars->p_full[t][half], g);
+                        ok = ok && wait_all(&bars->p_full[t][part], g);
                         if (!ok) break;
                         tc::fence_after_sync();
 #pragma unroll
-                        for (int i = 0; i < kWpPages / 2; ++i) {   // O (+)= P V, a page at a time
-                            const int kk = half * (kWpPages / 2) + i;
+                        for (int kk = part ? 2 * Sh::FIRST_PART : 0; kk < (part ? kWpPages : 2 * Sh::FIRST_PART); ++kk) {
+                            // O (+)= P V, a page at a time
                             const uint32_t ph = d_s + 32 * (kk >> 1) + 8 * (kk & 1);
                             const uint64_t vp = vb + (uint32_t)(kk * Sh::PAGE >> 4);
                             if (leader) {
@@ -565,11 +570,11 @@ __global__ void __launch_bounds__(kWpThreads, 1)
                     }
                     tc::tmem_st16(scol + cc * 32, hi);
                     if constexpr (RESIDUAL) tc::tmem_st16(scol + cc * 32 + 16, lo);
-                    if (cc % 2 == 1) {   // half of the keys are ready
+                    if (cc == Sh::FIRST_PART - 1 || cc == 3) {   // a part of P is ready
                         tc::tmem_wait_st();
                         tc::fence_before_sync();
                         __syncwarp();
-                        if (lane == 0) tc::mbar_arrive_cta(&bars->p_full[t][cc / 2]);
+                        if (lane == 0) tc::mbar_arrive_cta(&bars->p_full[t][cc == 3]);
                     }
                 }
                 float s0, s1, s2, s3;
