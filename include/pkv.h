@@ -556,10 +556,16 @@ int pkv_step_tables(const int32_t *seq_lens, const int32_t *new_lens, int num_se
  * a length outside [0, max_blocks_per_seq * 16] is clamped and sets
  * PKV_DEV_BAD_CONTEXT; where the list has no room for all of them
  * (PKV_DEV_FREE_LIST), nothing is moved.
+ *   workspace     device, 4-B aligned, >= pkv_release_workspace_size(num_seqs)
+ *                 bytes (0 for up to 256 sequences: may be NULL); contents on
+ *                 entry ignored; not to be used by another call that may run
+ *                 concurrently
  */
+size_t pkv_release_workspace_size(int num_seqs);
 int pkv_release_blocks(int32_t *block_tables, int max_blocks_per_seq, const int32_t *seq_lens, const int32_t *finished,
                        int num_seqs, int window, int num_sinks, int32_t *free_list, int free_capacity,
-                       int32_t *free_count, int num_blocks, int block_size, int *dev_status, void *stream);
+                       int32_t *free_count, int num_blocks, int block_size, void *workspace, size_t workspace_bytes,
+                       int *dev_status, void *stream);
 
 /* ---- host block pool ----------------------------------------------------------
  * A preallocated set of physical block ids with a free list used as a stack

@@ -100,7 +100,8 @@ def lib():
         "pkv_qk_rope_append": ([P, I64, P, I64, P, I64, P, I64, P, P, P, I, I, F, P, P, I, F, I, P, P, I, I, I, I, I,
                                 I, P, P], I),
         "pkv_step_tables": ([P, P, I, P, I, P, I, P, P, I, I, P, P, P, P, I, P, P], I),
-        "pkv_release_blocks": ([P, I, P, P, I, I, I, P, I, P, I, I, P, P], I),
+        "pkv_release_workspace_size": ([I], SZ),
+        "pkv_release_blocks": ([P, I, P, P, I, I, I, P, I, P, I, I, P, SZ, P, P], I),
         "pkv_copy_blocks": ([P, I64, P, I64, P, I, I64, P, P], I),
         "pkv_pool_create": ([I, P], P),
         "pkv_pool_destroy": ([P], None),
@@ -577,25 +578,38 @@ def step_tables(seq_lens, new_lens, block_tables, free_list, free_count, num_blo
         raise PkvError("pkv_step_tables", st)
 
 
+def release_workspace_size(num_seqs):
+    return int(lib().pkv_release_workspace_size(num_seqs))
+
+
 def release_blocks(block_tables, seq_lens, free_list, free_count, num_blocks, finished=None, window=0, num_sinks=0,
-                   dev_status=None, stream=None):
+                   workspace=None, dev_status=None, stream=None):
     """pkv_release_blocks: blocks of finished sequences (finished int32 [S], non-
     zero), and with window > 0 those no later token can see, go back to
     free_list int32 [capacity] / free_count int32 [1]; their entries in
-    block_tables int32 [S, max_blocks] become -1."""
+    block_tables int32 [S, max_blocks] become -1.  workspace: uint8 CUDA tensor
+    (allocated here if None)."""
     dev = _device_of("block_tables", block_tables)
     if dev != _current_device():
         return _elsewhere(dev, release_blocks, block_tables, seq_lens, free_list, free_count, num_blocks, finished, window,
-                          num_sinks, dev_status, stream)
+                          num_sinks, workspace, dev_status, stream)
     tables = block_tables.shape
     S, MB = tables
+    nwork = 0 if workspace is None else workspace.numel()
+    if workspace is None and S > 256:
+        nwork = release_workspace_size(S)
+        if stream is None:
+            workspace = _torch.empty(nwork, dtype=_torch.uint8, device=block_tables.device)
+        else:   # memory of the stream that the call runs on
+            with _torch.cuda.stream(stream):
+                workspace = _torch.empty(nwork, dtype=_torch.uint8, device=block_tables.device)
     capacity = free_list.numel()
     st = _fn["pkv_release_blocks"](
         _ptr("block_tables", block_tables, _I32, tables, dev), MB, _ptr("seq_lens", seq_lens, _I32, (S,), dev),
         None if finished is None else _ptr("finished", finished, _I32, (S,), dev), S, window, num_sinks,
         _ptr("free_list", free_list, _I32, (capacity,), dev), capacity, _ptr("free_count", free_count, _I32, (1,), dev),
-        num_blocks, 16, None if dev_status is None else _ptr("dev_status", dev_status, _I32, (1,), dev),
-        _stream_on(dev, stream))
+        num_blocks, 16, None if workspace is None else _ptr("workspace", workspace, _torch.uint8, (nwork,), dev), nwork,
+        None if dev_status is None else _ptr("dev_status", dev_status, _I32, (1,), dev), _stream_on(dev, stream))
     if st != PKV_OK:
         raise PkvError("pkv_release_blocks", st)
 

@@ -29,7 +29,7 @@
 namespace pkv {
 
 constexpr int kTabThreads = 1024;
-constexpr int kTabCluster = 8;
+constexpr int kTabCluster = 16;   // more than the portable 8: opted into at the first launch
 
 struct TablesParams {
     const int32_t *seq_lens, *new_lens;
@@ -233,6 +233,7 @@ struct ReleaseParams {
     const int32_t *seq_lens, *finished;
     int32_t *free_list;
     int32_t *free_count;
+    int32_t *counts;     // workspace: [S] blocks each row gives back, then the list's count before the call
     int *dev_status;
     int S, max_blocks, free_capacity, num_blocks, window, sinks;
 };
@@ -240,13 +241,14 @@ struct ReleaseParams {
 // Table entries [lo, hi) of sequence s that the call gives back.
 __device__ __forceinline__ void release_range(const ReleaseParams &p, int s, int &lo, int &hi, int &status) {
     int64_t l = p.seq_lens[s];
+    const bool finished = p.finished != nullptr && p.finished[s] != 0;
     if (l < 0 || l > (int64_t)p.max_blocks * 16) {
         status |= PKV_DEV_BAD_CONTEXT;
         l = l < 0 ? 0 : (int64_t)p.max_blocks * 16;
     }
     const int nb = (int)((l + 15) >> 4);
     lo = hi = 0;
-    if (p.finished != nullptr && p.finished[s] != 0) {
+    if (finished) {
         hi = nb;
     } else if (p.window > 0) {
         // the next token sits at position l and sees positions from
@@ -258,86 +260,155 @@ __device__ __forceinline__ void release_range(const ReleaseParams &p, int s, int
     }
 }
 
-// A warp a row.  Each CTA of the cluster takes neighbouring rows: the first
-// pass counts the blocks a row gives back, the scans (of the CTA's rows, and
-// of the CTAs' totals through distributed shared memory) place them in the
-// free list in the order of the rows and of the blocks within a row, and the
-// second pass moves them.
-__global__ void __launch_bounds__(kTabThreads) release_blocks_kernel(const ReleaseParams p) {
-    extern __shared__ int rel_smem[];    // [rows of this CTA]: blocks given back, then their place
-    __shared__ Pair64 sh_scan[32];
-    __shared__ int sh_total;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x, warps = nt >> 5;
-    const int rank = (int)cluster_ctarank(), ranks = (int)cluster_nctarank();
-    pdl_wait_primary();
-    pdl_launch_dependents();
-    const int rows = (p.S + ranks - 1) / ranks;
-    const int r0 = min(p.S, rank * rows), r1 = min(p.S, r0 + rows);
-    int status = 0;
+// A warp a row, kRelLoads entries of it under way in each lane; the blocks go
+// on the list in the order of the rows and of the blocks within a row.  Two
+// forms.  Up to kRelSmallRows rows are one launch: a cluster of CTAs counts its
+// rows' blocks, exchanges the CTAs' totals through distributed shared memory
+// and moves the blocks.  More rows are two launches over the whole GPU: one
+// counts into the workspace, the other sums the counts of the rows before its
+// own (each CTA reads them all, out of L2) and moves.  4,000 rows of up to
+// 2,048 blocks take # us so, and 45 us in one cluster of 16 CTAs of 1,024
+// threads; 256 rows of up to 512 take # us in one launch and # us in two, which
+// cost the host another 7 us.
+constexpr int kRelThreads = 256;
+constexpr int kRelLoads = 8;
+constexpr int kRelSmallWarps = 16;
+constexpr int kRelSmallRows = kTabCluster * kRelSmallWarps;
 
-    for (int s = r0 + warp; s < r1; s += warps) {
-        int lo, hi, n = 0;
-        release_range(p, s, lo, hi, status);
-        const int32_t *row = p.block_tables + (int64_t)s * p.max_blocks;
-        for (int j = lo + lane; j < hi; j += 32) {
-            const int32_t id = row[j];
-            if (id >= p.num_blocks) status |= PKV_DEV_BAD_BLOCK_ID;
-            n += id >= 0 && id < p.num_blocks;
+// visit(j0, ids): the entries j0 + 32 u + lane, u < kRelLoads, of row s that
+// are given back (others -1), in order
+template <typename F>
+__device__ __forceinline__ void walk_row(const ReleaseParams &p, int s, int lane, int &status, F visit) {
+    int lo, hi;
+    release_range(p, s, lo, hi, status);
+    const int32_t *row = p.block_tables + (int64_t)s * p.max_blocks;
+    for (int j0 = lo; j0 < hi; j0 += 32 * kRelLoads) {
+        int32_t id[kRelLoads];
+#pragma unroll
+        for (int u = 0; u < kRelLoads; ++u) {
+            const int j = j0 + 32 * u + lane;
+            id[u] = j < hi ? row[j] : -1;
         }
-        n = __reduce_add_sync(0xffffffffu, n);
-        if (lane == 0) rel_smem[s - r0] = n;
+#pragma unroll
+        for (int u = 0; u < kRelLoads; ++u)
+            if (id[u] >= p.num_blocks) {
+                status |= PKV_DEV_BAD_BLOCK_ID;
+                id[u] = -1;
+            }
+        visit(j0, id);
     }
-    __syncthreads();
-    const int per = (r1 - r0 + nt - 1) / nt;
-    const int i_lo = min(r1 - r0, tid * per), i_hi = min(r1 - r0, i_lo + per);
-    Pair64 sum{0, 0}, total;
-    for (int i = i_lo; i < i_hi; ++i) sum.a += rel_smem[i];
-    const Pair64 incl = cta_scan(sum, sh_scan, &total);
-    {
-        int a = (int)(incl.a - sum.a);
-        for (int i = i_lo; i < i_hi; ++i) {
-            const int n = rel_smem[i];
-            rel_smem[i] = a;
-            a += n;
-        }
-    }
-    // the CTA's total fits: a table has fewer than 2^31 entries
-    if (tid == 0) sh_total = (int)total.a;
-    const int count = p.free_count[0];
-    __syncthreads();
-    if (ranks > 1) cluster_sync();
-    int64_t before = 0, all = 0;
-    for (int r = 0; r < ranks; ++r) {
-        const int n = ranks > 1 ? ld_cluster_s32(cluster_addr(&sh_total, (uint32_t)r)) : sh_total;
-        if (r < rank) before += n;
-        all += n;
-    }
-    // every CTA has read the totals and the count: they may change now, and a
-    // CTA may leave
-    if (ranks > 1) cluster_sync();
-    const bool fail = count < 0 || count > p.free_capacity || count + all > p.free_capacity;
-    if (fail) status |= PKV_DEV_FREE_LIST;
+}
+
+// Blocks of row s given back (all lanes get the count).
+__device__ __forceinline__ int count_row(const ReleaseParams &p, int s, int lane) {
+    int status = 0, n = 0;
+    walk_row(p, s, lane, status, [&](int, const int32_t(&id)[kRelLoads]) {
+#pragma unroll
+        for (int u = 0; u < kRelLoads; ++u) n += id[u] >= 0;
+    });
     if (status) set_status(p.dev_status, status);
-    if (fail) return;
-    if (rank == 0 && tid == 0) p.free_count[0] = count + (int)all;
+    return __reduce_add_sync(0xffffffffu, n);
+}
 
-    for (int s = r0 + warp; s < r1; s += warps) {
-        int lo, hi, ignored = 0;
-        release_range(p, s, lo, hi, ignored);
-        int32_t *row = p.block_tables + (int64_t)s * p.max_blocks;
-        int64_t at = count + before + rel_smem[s - r0];
-        for (int j0 = lo; j0 < hi; j0 += 32) {
-            const int j = j0 + lane;
-            const int32_t id = j < hi ? row[j] : -1;
-            const bool give = id >= 0 && id < p.num_blocks;
-            const unsigned m = __ballot_sync(0xffffffffu, give);
-            if (give) {
-                p.free_list[at + __popc(m & ((1u << lane) - 1u))] = id;
-                row[j] = -1;
+// Moves row s's blocks to free_list[at..].
+__device__ __forceinline__ void move_row(const ReleaseParams &p, int s, int lane, int64_t at) {
+    int ignored = 0;
+    int32_t *row = p.block_tables + (int64_t)s * p.max_blocks;
+    walk_row(p, s, lane, ignored, [&](int j0, const int32_t(&id)[kRelLoads]) {
+#pragma unroll
+        for (int u = 0; u < kRelLoads; ++u) {
+            const unsigned m = __ballot_sync(0xffffffffu, id[u] >= 0);
+            if (id[u] >= 0) {
+                p.free_list[at + __popc(m & ((1u << lane) - 1u))] = id[u];
+                row[j0 + 32 * u + lane] = -1;
             }
             at += __popc(m);
         }
+    });
+}
+
+__global__ void __launch_bounds__(kRelSmallWarps * 32) release_small_kernel(const ReleaseParams p) {
+    __shared__ int sh_count[kRelSmallWarps];
+    __shared__ int sh_total;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int rank = (int)cluster_ctarank(), ranks = (int)cluster_nctarank();
+    const int s = rank * kRelSmallWarps + warp;
+    pdl_wait_primary();
+    pdl_launch_dependents();
+    const int count = p.free_count[0];
+    const int n = s < p.S ? count_row(p, s, lane) : 0;
+    if (lane == 0) sh_count[warp] = n;
+    __syncthreads();
+    int64_t at = 0, all = 0;
+    int mine = 0;
+#pragma unroll
+    for (int w = 0; w < kRelSmallWarps; ++w) {
+        if (w < warp) at += sh_count[w];
+        mine += sh_count[w];   // (a table has fewer than 2^31 entries)
     }
+    if (threadIdx.x == 0) sh_total = mine;
+    cluster_sync();
+    for (int r = 0; r < ranks; ++r) {
+        const int t = ld_cluster_s32(cluster_addr(&sh_total, (uint32_t)r));
+        if (r < rank) at += t;
+        all += t;
+    }
+    // every CTA has read the totals and the count: they may change now, and a
+    // CTA may leave
+    cluster_sync();
+    if (count < 0 || count > p.free_capacity || count + all > p.free_capacity) {
+        if (rank == 0 && threadIdx.x == 0) set_status(p.dev_status, PKV_DEV_FREE_LIST);
+        return;
+    }
+    if (rank == 0 && threadIdx.x == 0) p.free_count[0] = count + (int)all;
+    if (n > 0) move_row(p, s, lane, count + at);
+}
+
+__global__ void __launch_bounds__(kRelThreads) release_count_kernel(const ReleaseParams p) {
+    const int lane = threadIdx.x & 31, s = blockIdx.x * (kRelThreads / 32) + (threadIdx.x >> 5);
+    pdl_wait_primary();
+    pdl_launch_dependents();
+    if (blockIdx.x == 0 && threadIdx.x == 0) p.counts[p.S] = p.free_count[0];
+    if (s >= p.S) return;
+    const int n = count_row(p, s, lane);
+    if (lane == 0) p.counts[s] = n;
+}
+
+__global__ void __launch_bounds__(kRelThreads) release_move_kernel(const ReleaseParams p) {
+    __shared__ Pair64 sh_sum[kRelThreads / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int first = blockIdx.x * (kRelThreads / 32), s = first + warp;
+    pdl_wait_primary();
+    pdl_launch_dependents();
+    // blocks given back by the rows before this CTA's, and by all
+    Pair64 sum{0, 0};
+    for (int i = tid; i < p.S; i += kRelThreads) {
+        const int n = p.counts[i];
+        sum.b += n;
+        if (i < first) sum.a += n;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        sum.a += __shfl_xor_sync(0xffffffffu, sum.a, o);
+        sum.b += __shfl_xor_sync(0xffffffffu, sum.b, o);
+    }
+    if (lane == 0) sh_sum[warp] = sum;
+    __syncthreads();
+    int64_t at = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kRelThreads / 32; ++w) {
+        at += sh_sum[w].a;
+        all += sh_sum[w].b;
+    }
+    const int count = p.counts[p.S];
+    if (count < 0 || count > p.free_capacity || count + all > p.free_capacity) {
+        if (blockIdx.x == 0 && tid == 0) set_status(p.dev_status, PKV_DEV_FREE_LIST);
+        return;
+    }
+    if (blockIdx.x == 0 && tid == 0) p.free_count[0] = count + (int)all;
+    if (s >= p.S || p.counts[s] == 0) return;
+    for (int i = first; i < s; ++i) at += p.counts[i];
+    move_row(p, s, lane, count + at);
 }
 
 }  // namespace pkv
@@ -367,6 +438,8 @@ extern "C" int pkv_step_tables(const int32_t *seq_lens, const int32_t *new_lens,
     constexpr int kMaxSmem = (3 * PKV_TABLES_MAX_SEQS + 2) * 4;
     if (!done_on_device(&attr_set)) {
         cudaError_t e = cudaFuncSetAttribute(step_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(step_tables_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return cuda_fail(e);
         mark_done_on_device(&attr_set);
     }
@@ -396,10 +469,14 @@ extern "C" int pkv_step_tables(const int32_t *seq_lens, const int32_t *new_lens,
     return e == cudaSuccess ? PKV_OK : cuda_fail(e);
 }
 
+extern "C" size_t pkv_release_workspace_size(int num_seqs) {
+    return num_seqs <= pkv::kRelSmallRows ? 0 : ((size_t)num_seqs + 1) * sizeof(int32_t);
+}
+
 extern "C" int pkv_release_blocks(int32_t *block_tables, int max_blocks_per_seq, const int32_t *seq_lens,
                                   const int32_t *finished, int num_seqs, int window, int num_sinks, int32_t *free_list,
                                   int free_capacity, int32_t *free_count, int num_blocks, int block_size,
-                                  int *dev_status, void *stream) {
+                                  void *workspace, size_t workspace_bytes, int *dev_status, void *stream) {
     pkv::NvtxRange nvtx_range("pkv_release_blocks");
     using namespace pkv;
     if (num_seqs < 0 || max_blocks_per_seq <= 0 || free_capacity < 0 || num_blocks <= 0 || window < 0 || num_sinks < 0)
@@ -411,22 +488,16 @@ extern "C" int pkv_release_blocks(int32_t *block_tables, int max_blocks_per_seq,
     if (!aligned(block_tables, 4) || !aligned(seq_lens, 4) || !aligned(finished, 4) || !aligned(free_list, 4) ||
         !aligned(free_count, 4))
         return PKV_ERR_INVALID_ARG;
-    int sms = 0;
-    int rc = current_sm_count(&sms);
-    if (rc != PKV_OK) return rc;
-    static unsigned long long attr_set = 0;
-    if (!done_on_device(&attr_set)) {
-        cudaError_t e = cudaFuncSetAttribute(release_blocks_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             PKV_TABLES_MAX_SEQS * 4);
-        if (e != cudaSuccess) return cuda_fail(e);
-        mark_done_on_device(&attr_set);
-    }
+    const bool small = num_seqs <= kRelSmallRows;
+    if (!small && (!workspace || !aligned(workspace, 4) || workspace_bytes < pkv_release_workspace_size(num_seqs)))
+        return PKV_ERR_WORKSPACE;
     ReleaseParams prm;
     prm.block_tables = block_tables;
     prm.seq_lens = seq_lens;
     prm.finished = finished;
     prm.free_list = free_list;
     prm.free_count = free_count;
+    prm.counts = static_cast<int32_t *>(workspace);
     prm.dev_status = dev_status;
     prm.S = num_seqs;
     prm.max_blocks = max_blocks_per_seq;
@@ -434,10 +505,23 @@ extern "C" int pkv_release_blocks(int32_t *block_tables, int max_blocks_per_seq,
     prm.num_blocks = num_blocks;
     prm.window = window;
     prm.sinks = num_sinks;
-    const int ranks = num_seqs <= 32 ? 1 : kTabCluster;
-    const int rows = (num_seqs + ranks - 1) / ranks;
-    cudaError_t e = launch_cluster(release_blocks_kernel, ranks, ranks, kTabThreads, (size_t)rows * 4,
-                                   static_cast<cudaStream_t>(stream), prm);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (small) {
+        static unsigned long long attr_set = 0;
+        if (!done_on_device(&attr_set)) {
+            e = cudaFuncSetAttribute(release_small_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            if (e != cudaSuccess) return cuda_fail(e);
+            mark_done_on_device(&attr_set);
+        }
+        int ranks = 1;
+        while (ranks * kRelSmallWarps < num_seqs) ranks *= 2;
+        e = launch_cluster(release_small_kernel, ranks, ranks, kRelSmallWarps * 32, 0, st, prm);
+    } else {
+        const int grid = (num_seqs + kRelThreads / 32 - 1) / (kRelThreads / 32);
+        e = launch_pdl(release_count_kernel, dim3(grid), dim3(kRelThreads), 0, st, prm);
+        if (e == cudaSuccess) e = launch_pdl(release_move_kernel, dim3(grid), dim3(kRelThreads), 0, st, prm);
+    }
     if (e == cudaSuccess) e = cudaGetLastError();
     return e == cudaSuccess ? PKV_OK : cuda_fail(e);
 }

@@ -189,7 +189,7 @@ def test_release_blocks(cuda_lib, window, sinks, share):
     assert status == 0
 
 
-@pytest.mark.parametrize("S", [1, 32, 33, 257, 3001, B.TABLES_MAX_SEQS])
+@pytest.mark.parametrize("S", [1, 16, 17, 32, 33, 100, 255, 256, 257, 3001, B.TABLES_MAX_SEQS])
 def test_release_blocks_many_sequences(cuda_lib, S):
     rng = random.Random(S)
     lens = [rng.randint(0, 128) for _ in range(S)]
@@ -199,6 +199,58 @@ def test_release_blocks_many_sequences(cuda_lib, S):
     got, status = run_release(pool, 8, fin, 40, 4)
     assert got == tuple(ref.release(pool.table, lens, fin, 40, 4, pool.free, pool.count, pool.num_blocks))
     assert status == 0
+
+
+@pytest.mark.parametrize("S", [3, 300])
+def test_release_long_rows(cuda_lib, S):
+    """Tables of many entries a row, with holes; a workspace of the caller's."""
+    rng = random.Random(S)
+    mb = 1000
+    lens = [rng.randint(0, mb * 16) for _ in range(S)]
+    pool = Pool(lens, mb, 3, seed=S)
+    for r in pool.table:
+        for j in rng.sample(range(mb), 300):
+            r[j] = -1
+    pool.free += [-7] * (S * mb)
+    fin = [rng.randint(0, 1) for _ in lens]
+    lens_d, table, free, count = pool.device(mb)
+    work = torch.full((4 * S + 4,), 255, dtype=torch.uint8, device="cuda")
+    status = i32([0])
+    release_blocks(table, lens_d, free, count, pool.num_blocks, finished=i32(fin), window=5000, num_sinks=100,
+                   workspace=work, dev_status=status)
+    want = ref.release(pool.table, lens, fin, 5000, 100, pool.free, pool.count, pool.num_blocks)
+    assert (table.tolist(), free.tolist(), count.item()) == tuple(want) and status.item() == 0
+
+
+@pytest.mark.parametrize("S", [40, 400])
+def test_release_captured_and_replayed(cuda_lib, S):
+    """A loop step of two calls in a graph: grow by 16, give back what left a window of 40."""
+    pool = Pool([5] * S, 40, S * 8)
+    pool.free = pool.free[:pool.count] + [-7] * (S * 40)
+    seq, table, free, count = pool.device(40)
+    new, cu, status, none = i32([16] * S), i32([0] * (S + 1)), i32([0]), i32([0] * S)
+    slots = torch.empty(S * 16, dtype=torch.int64, device="cuda")
+    pos = torch.empty(S * 16, dtype=torch.int32, device="cuda")
+
+    def call():
+        step_tables(seq, new, table, free, count, pool.num_blocks, seq, cu, slots, pos, dev_status=status)
+        release_blocks(table, seq, free, count, pool.num_blocks, finished=none, window=40, num_sinks=3, dev_status=status)
+
+    call()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        call()
+    torch.cuda.current_stream().wait_stream(side)
+    for _ in range(20):
+        g.replay()
+    tab, fr, n, lens = pool.table, pool.free, pool.count, pool.lens
+    for _ in range(21):
+        tab, n, lens, _, sl, _ = ref.step_tables(lens, [16] * S, tab, fr, n, S * 16)
+        tab, fr, n = ref.release(tab, lens, None, 40, 3, fr, n, pool.num_blocks)
+    assert status.item() == 0 and count.item() == n and table.tolist() == tab and slots.tolist() == sl
+    assert free.tolist()[:n] == fr[:n]
 
 
 def test_release_without_finished_and_without_window_is_a_no_op(cuda_lib):

@@ -126,7 +126,7 @@ def test_step_tables(change, rc):
 
 
 RELEASE = dict(tables=FAKE, max_blocks=8, seq_lens=FAKE, finished=FAKE, num_seqs=4, window=0, sinks=0, free_list=FAKE,
-               capacity=16, count=FAKE, num_blocks=16, bs=16, status=None, stream=None)
+               capacity=16, count=FAKE, num_blocks=16, bs=16, workspace=FAKE, workspace_bytes=20, status=None, stream=None)
 
 
 @pytest.mark.parametrize("change,rc", [
@@ -134,9 +134,16 @@ RELEASE = dict(tables=FAKE, max_blocks=8, seq_lens=FAKE, finished=FAKE, num_seqs
     (dict(window=-1), INVALID), (dict(sinks=-1), INVALID), (dict(capacity=-1), INVALID), (dict(num_blocks=0), INVALID),
     (dict(bs=8), UNSUPPORTED), (dict(tables=None), INVALID), (dict(seq_lens=None), INVALID), (dict(free_list=None), INVALID),
     (dict(count=None), INVALID), (dict(finished=FAKE + 2), INVALID), (dict(num_seqs=16384, max_blocks=1 << 17), UNSUPPORTED),
-    (dict(num_seqs=0, tables=None, seq_lens=None, free_list=None, count=None), 0)])
+    (dict(num_seqs=257, workspace=None, workspace_bytes=2000), -3), (dict(num_seqs=257, workspace_bytes=1031), -3),
+    (dict(num_seqs=257, workspace=FAKE + 2, workspace_bytes=2000), -3),
+    (dict(num_seqs=0, tables=None, seq_lens=None, free_list=None, count=None, workspace=None, workspace_bytes=0), 0)])
 def test_release_blocks(change, rc):
     assert call("pkv_release_blocks", RELEASE, **change) == rc
+
+
+def test_release_workspace_size():
+    assert [pkv.release_workspace_size(n) for n in (-1, 0, 256, 257, B.TABLES_MAX_SEQS)] == \
+        [0, 0, 0, 1032, 4 * B.TABLES_MAX_SEQS + 4]
 
 
 def test_bindings_refuse_cpu_tensors():
