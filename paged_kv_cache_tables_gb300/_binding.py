@@ -15,6 +15,7 @@ import numpy as np
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libpkv.so")
+CALLS_PATH = os.path.join(_HERE, "_torch_calls.so")
 
 PKV_OK = 0
 DTYPE_F16, DTYPE_BF16, DTYPE_F32 = 0, 1, 2
@@ -336,92 +337,23 @@ def copy_blocks(dst, src, pairs, dev_status=None, stream=None):
     _check("pkv_copy_blocks", st)
 
 
-# The calls below check shapes against one another and take tensors of any one
-# device: the call runs with that device current, on its current stream unless
-# one is given.  They are made once per layer or step, and a decode step's
-# kernels take a few microseconds, so what they cost on the host counts: plain
-# integers go to ctypes, and what does not change is looked up once (_setup).
+# The calls below are made once per layer or step, beside kernels of a few
+# microseconds: csrc/torch_calls.cpp checks their tensors (of any one device,
+# which the call runs on, on its current stream unless one is given) and calls
+# the C entry points.
 
-_torch = None
-_fn = {}
+_calls = None
 
 
-def _setup():
-    global _torch, _I32, _I64, _codes, _raw_stream, _current_device
-    import torch
+def _load_calls():
+    global _calls
+    import torch  # noqa: F401  (its libraries are what the module links to)
     lib()
-    _I32, _I64 = torch.int32, torch.int64
-    _codes = {torch.float16: DTYPE_F16, torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32}
-    _raw_stream = torch._C._cuda_getCurrentRawStream
-    _current_device = torch.cuda.current_device
-    for name in ("pkv_paged_window_decode_attention", "pkv_paged_window_prefill_attention", "pkv_qk_rope",
-                 "pkv_qk_rope_append", "pkv_step_tables", "pkv_release_blocks"):
-        _fn[name] = getattr(_lib, name)
-    _torch = torch
-
-
-def _device_of(name, t):
-    """Index of the CUDA device that the tensor `name`, and so the call, is on."""
-    if _torch is None:
-        _setup()
-    if not isinstance(t, _torch.Tensor) or not t.is_cuda:
-        raise TypeError("%s must be a CUDA tensor" % name)
-    return t.get_device()
-
-
-def _elsewhere(device, call, *args):
-    """`call` with the tensors' device made current."""
-    with _torch.cuda.device(device):
-        return call(*args)
-
-
-def _stream_on(device, stream):
-    if stream is None:
-        return _raw_stream(device)
-    if stream.device_index != device:
-        raise ValueError("the stream belongs to another device than the tensors")
-    return stream.cuda_stream
-
-
-def _code(name, t):
-    code = _codes.get(t.dtype)
-    if code is None:
-        raise TypeError("%s must be float16, bfloat16 or float32, got %s" % (name, t.dtype))
-    return code
-
-
-def _mismatch(name, t, dtype, shape, device):
-    if not isinstance(t, _torch.Tensor):
-        raise TypeError("%s must be a CUDA tensor" % name)
-    if t.dtype is not dtype:
-        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.shape != shape:
-        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    if t.get_device() != device:
-        raise ValueError("%s must be a CUDA tensor on the device of the others" % name)
-    raise ValueError("%s must be contiguous" % name)
-
-
-def _ptr(name, t, dtype, shape, device):
-    """Address of a contiguous tensor of this dtype, shape and device (index)."""
-    try:
-        if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
-            return t.data_ptr()
-    except AttributeError:
-        pass
-    return _mismatch(name, t, dtype, shape, device)
-
-
-def _row_stride(name, t, dtype, shape, device):
-    """Elements between tokens of [T, heads, d] rows whose heads are contiguous
-    within a token (a slice of a fused projection's rows will do)."""
-    T, H, d = shape
-    if not isinstance(t, _torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.get_device() != device:
-        _mismatch(name, t, dtype, shape, device)
-    a, b, c = t.stride()
-    if T and (c != 1 or (b != d and H > 1)):
-        raise ValueError("%s must hold each token's heads contiguously" % name)
-    return a if T > 1 else H * d
+    if not os.path.exists(CALLS_PATH):
+        raise RuntimeError("_torch_calls.so is not built (%s); run paged_kv_cache_tables_gb300.build.build()" % CALLS_PATH)
+    from . import _torch_calls
+    _calls = _torch_calls
+    return _calls
 
 
 def paged_window_decode_attention(out, q, k_cache, v_cache, block_tables, context_lens, window, num_sinks=0, scale=None,
@@ -429,23 +361,9 @@ def paged_window_decode_attention(out, q, k_cache, v_cache, block_tables, contex
     """pkv_paged_window_decode_attention: q/out [S, Hq, d]; block_tables int32
     [S, max_blocks]; context_lens int32 [S].  Each query sees the last `window`
     positions of its context and the first num_sinks."""
-    dev = _device_of("q", q)
-    if dev != _current_device():
-        return _elsewhere(dev, paged_window_decode_attention, out, q, k_cache, v_cache, block_tables, context_lens, window,
-                          num_sinks, scale, dev_status, stream)
-    rows, dtype, cache = q.shape, q.dtype, k_cache.shape
-    S, Hq, d = rows
-    NB, Hkv, bs, dk = cache
-    MB = block_tables.shape[1]
-    if dk != d:
-        raise ValueError("q and the caches must have one head_dim")
-    st = _fn["pkv_paged_window_decode_attention"](
-        _ptr("out", out, out.dtype, rows, dev), _ptr("q", q, dtype, rows, dev), _ptr("k_cache", k_cache, dtype, cache, dev),
-        _ptr("v_cache", v_cache, dtype, cache, dev), _ptr("block_tables", block_tables, _I32, (S, MB), dev), MB,
-        _ptr("context_lens", context_lens, _I32, (S,), dev), S, NB, Hq, Hkv, d, bs, window, num_sinks,
-        1.0 / math.sqrt(d) if scale is None else scale, _code("q", q), _code("out", out),
-        None if dev_status is None else _ptr("dev_status", dev_status, _I32, (1,), dev), _stream_on(dev, stream))
-    if st != PKV_OK:
+    st = (_calls or _load_calls()).window_decode(out, q, k_cache, v_cache, block_tables, context_lens, window, num_sinks,
+                                                 scale, dev_status, stream)
+    if st:
         raise PkvError("pkv_paged_window_decode_attention", st)
 
 
@@ -454,24 +372,9 @@ def paged_window_prefill_attention(out, q, cu_seqlens, max_q_len, k_cache, v_cac
     """pkv_paged_window_prefill_attention: q/out [total_q, Hq, d]; cu_seqlens
     int32 [S + 1].  Each row sees the last `window` positions up to its own and
     the first num_sinks."""
-    dev = _device_of("q", q)
-    if dev != _current_device():
-        return _elsewhere(dev, paged_window_prefill_attention, out, q, cu_seqlens, max_q_len, k_cache, v_cache,
-                          block_tables, context_lens, window, num_sinks, scale, dev_status, stream)
-    rows, dtype, cache = q.shape, q.dtype, k_cache.shape
-    T, Hq, d = rows
-    NB, Hkv, bs, dk = cache
-    S, MB = block_tables.shape
-    if dk != d:
-        raise ValueError("q and the caches must have one head_dim")
-    st = _fn["pkv_paged_window_prefill_attention"](
-        _ptr("out", out, out.dtype, rows, dev), _ptr("q", q, dtype, rows, dev),
-        _ptr("cu_seqlens", cu_seqlens, _I32, (S + 1,), dev), S, max_q_len, T, _ptr("k_cache", k_cache, dtype, cache, dev),
-        _ptr("v_cache", v_cache, dtype, cache, dev), _ptr("block_tables", block_tables, _I32, (S, MB), dev), MB,
-        _ptr("context_lens", context_lens, _I32, (S,), dev), NB, Hq, Hkv, d, bs, window, num_sinks,
-        1.0 / math.sqrt(d) if scale is None else scale, _code("q", q), _code("out", out),
-        None if dev_status is None else _ptr("dev_status", dev_status, _I32, (1,), dev), _stream_on(dev, stream))
-    if st != PKV_OK:
+    st = (_calls or _load_calls()).window_prefill(out, q, cu_seqlens, max_q_len, k_cache, v_cache, block_tables,
+                                                  context_lens, window, num_sinks, scale, dev_status, stream)
+    if st:
         raise PkvError("pkv_paged_window_prefill_attention", st)
 
 
@@ -488,37 +391,14 @@ def rope_frequencies(rotary_dim, base=10000.0, scaling=ROPE_PLAIN, factor=1.0, o
     return torch.from_numpy(host).to(device), m.value
 
 
-def _rope_weights(q, d, q_weight, k_weight, device):
-    """(q_weight, k_weight, weight_dtype) as the entry points take them."""
-    if q_weight is None and k_weight is None:
-        return None, None, DTYPE_F32
-    one = k_weight if q_weight is None else q_weight
-    dtype = one.dtype
-    return (None if q_weight is None else _ptr("q_weight", q_weight, dtype, (d,), device),
-            None if k_weight is None else _ptr("k_weight", k_weight, dtype, (d,), device), _code("the weights", one))
-
-
 def qk_rope(q_out, k_out, q, k, positions, freqs, interleaved=False, mscale=1.0, q_weight=None, k_weight=None, eps=1e-6,
             stream=None):
     """pkv_qk_rope: q, q_out [T, Hq, d] and k, k_out [T, Hkv, d], each token's
     heads contiguous; positions int32 [T]; freqs and mscale from
     rope_frequencies.  q_out may be q, and k_out k."""
-    dev = _device_of("q", q)
-    if dev != _current_device():
-        return _elsewhere(dev, qk_rope, q_out, k_out, q, k, positions, freqs, interleaved, mscale, q_weight, k_weight, eps,
-                          stream)
-    qs, dtype = q.shape, q.dtype
-    T, Hq, d = qs
-    ks = (T, k.shape[1], d)
-    pairs = freqs.numel()
-    wq, wk, wt = _rope_weights(q, d, q_weight, k_weight, dev)
-    qos, kos = _row_stride("q_out", q_out, dtype, qs, dev), _row_stride("k_out", k_out, dtype, ks, dev)
-    qis, kis = _row_stride("q", q, dtype, qs, dev), _row_stride("k", k, dtype, ks, dev)
-    st = _fn["pkv_qk_rope"](
-        q_out.data_ptr(), qos, k_out.data_ptr(), kos, q.data_ptr(), qis, k.data_ptr(), kis,
-        _ptr("positions", positions, _I32, (T,), dev), _ptr("freqs", freqs, _I64, (pairs,), dev), 2 * pairs,
-        1 if interleaved else 0, mscale, wq, wk, wt, eps, T, Hq, ks[1], d, _code("q", q), _stream_on(dev, stream))
-    if st != PKV_OK:
+    st = (_calls or _load_calls()).qk_rope(q_out, k_out, q, k, positions, freqs, interleaved, mscale, q_weight, k_weight,
+                                           eps, stream)
+    if st:
         raise PkvError("pkv_qk_rope", st)
 
 
@@ -526,28 +406,9 @@ def qk_rope_append(q_out, q, k, v, positions, slot_mapping, freqs, k_cache, v_ca
                    q_weight=None, k_weight=None, eps=1e-6, dev_status=None, stream=None):
     """pkv_qk_rope_append: as qk_rope, the keys (rotated) and values [T, Hkv, d]
     going to the caches [NB, Hkv, 16, d] by slot_mapping, int64 [T]."""
-    dev = _device_of("q", q)
-    if dev != _current_device():
-        return _elsewhere(dev, qk_rope_append, q_out, q, k, v, positions, slot_mapping, freqs, k_cache, v_cache,
-                          interleaved, mscale, q_weight, k_weight, eps, dev_status, stream)
-    qs, dtype, cache = q.shape, q.dtype, k_cache.shape
-    T, Hq, d = qs
-    NB, Hkv, bs, dk = cache
-    if dk != d:
-        raise ValueError("q and the caches must have one head_dim")
-    ks = (T, Hkv, d)
-    pairs = freqs.numel()
-    wq, wk, wt = _rope_weights(q, d, q_weight, k_weight, dev)
-    qos, qis = _row_stride("q_out", q_out, dtype, qs, dev), _row_stride("q", q, dtype, qs, dev)
-    kis, vis = _row_stride("k", k, dtype, ks, dev), _row_stride("v", v, dtype, ks, dev)
-    st = _fn["pkv_qk_rope_append"](
-        q_out.data_ptr(), qos, q.data_ptr(), qis, k.data_ptr(), kis, v.data_ptr(), vis,
-        _ptr("positions", positions, _I32, (T,), dev), _ptr("slot_mapping", slot_mapping, _I64, (T,), dev),
-        _ptr("freqs", freqs, _I64, (pairs,), dev), 2 * pairs, 1 if interleaved else 0, mscale, wq, wk, wt, eps, T,
-        _ptr("k_cache", k_cache, dtype, cache, dev), _ptr("v_cache", v_cache, dtype, cache, dev), NB, bs, Hq, Hkv, d,
-        _code("q", q), None if dev_status is None else _ptr("dev_status", dev_status, _I32, (1,), dev),
-        _stream_on(dev, stream))
-    if st != PKV_OK:
+    st = (_calls or _load_calls()).qk_rope_append(q_out, q, k, v, positions, slot_mapping, freqs, k_cache, v_cache,
+                                                  interleaved, mscale, q_weight, k_weight, eps, dev_status, stream)
+    if st:
         raise PkvError("pkv_qk_rope_append", st)
 
 
@@ -558,23 +419,10 @@ def step_tables(seq_lens, new_lens, block_tables, free_list, free_count, num_blo
     (updated in place unless free_count_out is given); cu_seqlens int32 [S + 1];
     slot_mapping int64 and token_pos int32 [max_tokens].  context_lens may be
     seq_lens."""
-    dev = _device_of("seq_lens", seq_lens)
-    if dev != _current_device():
-        return _elsewhere(dev, step_tables, seq_lens, new_lens, block_tables, free_list, free_count, num_blocks,
-                          context_lens, cu_seqlens, slot_mapping, token_pos, free_count_out, dev_status, stream)
-    tables = block_tables.shape
-    S, MB = tables
-    ss = (S,)
-    T, capacity = slot_mapping.numel(), free_list.numel()
-    count = _ptr("free_count", free_count, _I32, (1,), dev)
-    st = _fn["pkv_step_tables"](
-        _ptr("seq_lens", seq_lens, _I32, ss, dev), _ptr("new_lens", new_lens, _I32, ss, dev), S,
-        _ptr("block_tables", block_tables, _I32, tables, dev), MB, _ptr("free_list", free_list, _I32, (capacity,), dev),
-        capacity, count, count if free_count_out is None else _ptr("free_count_out", free_count_out, _I32, (1,), dev),
-        num_blocks, 16, _ptr("context_lens", context_lens, _I32, ss, dev), _ptr("cu_seqlens", cu_seqlens, _I32, (S + 1,), dev),
-        _ptr("slot_mapping", slot_mapping, _I64, (T,), dev), _ptr("token_pos", token_pos, _I32, (T,), dev), T,
-        None if dev_status is None else _ptr("dev_status", dev_status, _I32, (1,), dev), _stream_on(dev, stream))
-    if st != PKV_OK:
+    st = (_calls or _load_calls()).step_tables(seq_lens, new_lens, block_tables, free_list, free_count, num_blocks,
+                                               context_lens, cu_seqlens, slot_mapping, token_pos, free_count_out,
+                                               dev_status, stream)
+    if st:
         raise PkvError("pkv_step_tables", st)
 
 
@@ -588,29 +436,19 @@ def release_blocks(block_tables, seq_lens, free_list, free_count, num_blocks, fi
     zero), and with window > 0 those no later token can see, go back to
     free_list int32 [capacity] / free_count int32 [1]; their entries in
     block_tables int32 [S, max_blocks] become -1.  workspace: uint8 CUDA tensor
-    (allocated here if None)."""
-    dev = _device_of("block_tables", block_tables)
-    if dev != _current_device():
-        return _elsewhere(dev, release_blocks, block_tables, seq_lens, free_list, free_count, num_blocks, finished, window,
-                          num_sinks, workspace, dev_status, stream)
-    tables = block_tables.shape
-    S, MB = tables
-    nwork = 0 if workspace is None else workspace.numel()
-    if workspace is None and S > 256:
-        nwork = release_workspace_size(S)
+    (allocated here if None and needed)."""
+    calls = _calls or _load_calls()
+    if workspace is None and len(block_tables) > 256:
+        import torch
+        n = release_workspace_size(len(block_tables))
         if stream is None:
-            workspace = _torch.empty(nwork, dtype=_torch.uint8, device=block_tables.device)
+            workspace = torch.empty(n, dtype=torch.uint8, device=block_tables.device)
         else:   # memory of the stream that the call runs on
-            with _torch.cuda.stream(stream):
-                workspace = _torch.empty(nwork, dtype=_torch.uint8, device=block_tables.device)
-    capacity = free_list.numel()
-    st = _fn["pkv_release_blocks"](
-        _ptr("block_tables", block_tables, _I32, tables, dev), MB, _ptr("seq_lens", seq_lens, _I32, (S,), dev),
-        None if finished is None else _ptr("finished", finished, _I32, (S,), dev), S, window, num_sinks,
-        _ptr("free_list", free_list, _I32, (capacity,), dev), capacity, _ptr("free_count", free_count, _I32, (1,), dev),
-        num_blocks, 16, None if workspace is None else _ptr("workspace", workspace, _torch.uint8, (nwork,), dev), nwork,
-        None if dev_status is None else _ptr("dev_status", dev_status, _I32, (1,), dev), _stream_on(dev, stream))
-    if st != PKV_OK:
+            with torch.cuda.stream(stream):
+                workspace = torch.empty(n, dtype=torch.uint8, device=block_tables.device)
+    st = calls.release_blocks(block_tables, seq_lens, free_list, free_count, num_blocks, finished, window, num_sinks,
+                              workspace, dev_status, stream)
+    if st:
         raise PkvError("pkv_release_blocks", st)
 
 

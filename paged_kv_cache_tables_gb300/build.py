@@ -1,14 +1,17 @@
-"""Build libpkv.so in-tree with nvcc for sm_103a.
+"""Build libpkv.so in-tree with nvcc for sm_103a, and _torch_calls.so with g++.
 
-Each translation unit compiles in its own nvcc process (in parallel), then
-nvcc links the shared library.  The CUDA runtime is linked statically; the
+Each translation unit compiles in its own process (in parallel), then nvcc
+links the shared library and g++ the Python module that calls it with torch
+tensors (against the installed torch's headers and libraries).  The CUDA runtime is linked statically; the
 driver's tensor-map encoder is looked up at run time, so the library loads
 on a machine without a GPU (the host scheduler works there).
 """
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -16,6 +19,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libpkv.so")
+CALLS = os.path.join(HERE, "_torch_calls.so")
 
 SOURCES = ["abi.cu", "append.cu", "decode.cu", "decode_static.cu", "prefill.cu", "prefill_tc.cu", "mixed.cu",
            "tables.cu", "rope.cu", "window_decode.cu", "window_prefill.cu", "host_sched.cpp"]
@@ -52,19 +56,52 @@ def _compile(src: str, verbose_ptxas: bool) -> str:
     return obj
 
 
+def _torch_dir() -> str:
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        raise RuntimeError("torch not found")
+    return list(spec.submodule_search_locations)[0]
+
+
+def _run(what: str, cmd) -> None:
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("%s failed:\n%s\n%s" % (what, " ".join(cmd), res.stderr))
+
+
+def _compile_calls() -> str:
+    torch, obj = _torch_dir(), os.path.join(BUILD, "torch_calls.o")
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    _run("g++", ["g++", "-O2", "-std=c++17", "-fPIC", "-I", INCLUDE, "-I", os.path.join(torch, "include"), "-I",
+                 os.path.join(torch, "include", "torch", "csrc", "api", "include"), "-I",
+                 sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"), "-c",
+                 os.path.join(CSRC, "torch_calls.cpp"), "-o", obj])
+    return obj
+
+
+def _link_calls(obj: str) -> None:
+    tmp = CALLS + ".tmp.%d" % os.getpid()
+    _run("link", ["g++", "-shared", "-o", tmp, obj, "-L", HERE, "-l:libpkv.so", "-Wl,-rpath,$ORIGIN", "-L",
+                  os.path.join(_torch_dir(), "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"])
+    os.replace(tmp, CALLS)
+
+
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _inputs_mtime():
+    if not force and all(os.path.exists(p) and os.path.getmtime(p) >= _inputs_mtime() for p in (LIB, CALLS)):
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     srcs = [s for s in SOURCES if os.path.exists(os.path.join(CSRC, s))]
-    with cf.ThreadPoolExecutor(max_workers=len(srcs)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(srcs) + 1) as ex:
+        calls = ex.submit(_compile_calls)
         objs = list(ex.map(lambda s: _compile(s, verbose_ptxas), srcs))
+        calls_obj = calls.result()
     tmp = LIB + ".tmp.%d" % os.getpid()
     cmd = [nvcc()] + ARCH + ["-shared", "-o", tmp] + objs + ["-lcudart_static", "-lrt", "-ldl", "-lpthread"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError("link failed:\n%s\n%s" % (" ".join(cmd), res.stderr))
     os.replace(tmp, LIB)
+    _link_calls(calls_obj)
     return LIB
 
 
