@@ -388,10 +388,10 @@ int pkv_paged_decode_attention_static(void *out, const void *q, const void *k_ca
 /*
  * pkv_paged_window_decode_attention -- pkv_paged_decode_attention over a
  * window: the query of sequence s sits at position context_lens[s] - 1.
- * Arguments as there, without a workspace, and scale must be positive.  One
- * launch; a range's parts meet through distributed shared memory of a
- * thread-block cluster, in an order fixed by the context lengths, so equal
- * inputs give equal bits.  Hidden positions of a block that is read may hold
+ * Arguments as there, without a workspace; scale must be positive, out and q
+ * 16-B aligned.  One launch; a range's parts meet in shared memory (of a
+ * thread-block cluster where a range has several CTAs), in an order fixed by
+ * the context lengths, so equal inputs give equal bits.  Hidden positions of a block that is read may hold
  * anything (NaN, infinity) in K and V.  context_lens is read after the wait
  * for the work enqueued before the call.  Further limits: num_seqs *
  * num_kv_heads * 16 and num_seqs * max_blocks_per_seq below 2^31,

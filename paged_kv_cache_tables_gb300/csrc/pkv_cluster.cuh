@@ -1,5 +1,6 @@
 // Thread-block clusters: rank, barrier, reads of another CTA's shared memory,
-// and a launch with a cluster dimension.  Inline PTX, written for this library.
+// taking the place of a CTA not yet launched, and a launch with a cluster
+// dimension.  Inline PTX, written for this library.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -44,6 +45,32 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
     float v;
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
     return v;
+}
+
+// Asks the hardware to give this CTA the place of one that has not been
+// launched; the answer (16 bytes) completes on `bar`.
+__device__ __forceinline__ void cancel_next_cta(void *answer, uint64_t *bar) {
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+            smem_addr(answer)),
+        "r"(smem_addr(bar))
+        : "memory");
+}
+
+// The place taken over (blockIdx.x), or -1: all CTAs have been launched.
+__device__ __forceinline__ int cancelled_cta(const void *answer) {
+    uint32_t ok, x;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b128 a;\n\t.reg .b32 y, z, w;\n\t"
+        "ld.shared.b128 a, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t"
+        "mov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, y, z, w}, a;\n\t}"
+        : "=r"(ok), "=r"(x)
+        : "r"(smem_addr(answer))
+        : "memory");
+    return ok ? (int)x : -1;
 }
 
 // launch_pdl with the grid cut into clusters of `ranks` CTAs.

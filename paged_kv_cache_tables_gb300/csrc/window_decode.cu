@@ -52,25 +52,278 @@ struct WindowDecodeParams {
     int out_dtype;
 };
 
-template <int D>
+// Two forms.  FEW, for ranges that all fit on the GPU at once (split over
+// clusters): long rings, two blocks a step, since a warp's time for a block is
+// a chain of latencies that two share.  MANY, for more ranges: three CTAs an SM
+// with shorter rings and one block a step, so that CTAs that start and end
+// hide behind one that streams.  us, FEW / MANY: 256 sequences x 8 heads of up
+// to 65 blocks 94.0 / 91.4, of up to 9 blocks 39.7 / 33.1; 200 x 2 of up to 20
+// 14.8 / 11.8; one wave: 7 x 8 of 505 blocks 37.8 / 42.6, 32 x 8 of 33 14.4 / 15.3.
+template <int D, bool MANY>
 struct WindowShape {
     static constexpr int HALVES = D / 64;               // 64-element (128-byte) column halves
     static constexpr int HALF_BYTES = 64 * 16 * 2;
     static constexpr int TILE_BYTES = HALVES * HALF_BYTES;
     static constexpr int STAGE_BYTES = 2 * TILE_BYTES;  // K then V
-    static constexpr int STAGES = D == 128 ? 3 : 6;
+    static constexpr int STAGES = D == 128 ? (MANY ? 2 : 3) : 4;
+    static constexpr int STEP = MANY ? 1 : 2;           // blocks a warp takes at a time
+    static constexpr int PER_SM = D == 128 && !MANY ? 2 : 3;
     static constexpr int RING_BYTES = kWinWarps * STAGES * STAGE_BYTES;
     // behind the ring: barriers, then (m, l) of each warp and of the CTA
     static constexpr int OFF_ML = RING_BYTES + kWinWarps * STAGES * 8;
     static constexpr int SMEM_BYTES = 1024 + OFF_ML + (kWinWarps + 1) * 32 * 4;
 };
 
-template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kWinWarps * 32, 2)
+// The blocks of a context that hold a position its last token sees.
+struct Visible {
+    int ctx, w0;            // clamped context; the window's first position
+    int sink_blocks, skip;  // entry v of the list is logical block v, or v + skip from sink_blocks on
+    int count;
+    bool bad;
+    __device__ __forceinline__ Visible(const WindowDecodeParams &p, int context) {
+        bad = context < 0 || context > p.max_blocks * 16;
+        ctx = min(max(context, 0), p.max_blocks * 16);
+        const int nblk = (ctx + 15) >> 4;
+        w0 = max(ctx - p.window, 0);
+        sink_blocks = min((p.sinks + 15) >> 4, nblk);
+        skip = max((w0 >> 4) - sink_blocks, 0);
+        count = nblk - skip;
+    }
+    __device__ __forceinline__ int logical(int v) const { return v < sink_blocks ? v : v + skip; }
+    // the visible positions of logical block j, one bit each (never none):
+    // before ctx, and in the window or among the first tokens
+    __device__ __forceinline__ uint32_t bits(int j, int sinks) const {
+        const int t0 = j * 16;
+        const int lim = min(ctx - t0, 16), first = min(max(w0 - t0, 0), 16), sk = min(max(sinks - t0, 0), 16);
+        return ((1u << lim) - 1u) & ((0xffffu << first) | ((1u << sk) - 1u)) & 0xffffu;
+    }
+};
+
+// Issues the TMA loads of block `blk`'s K and V tiles of KV head h into a ring
+// slot (one lane).
+template <int D, bool MANY>
+__device__ __forceinline__ void issue_block(const WindowDecodeParams &p, const CUtensorMap *tk, const CUtensorMap *tv,
+                                            uint8_t *slot, uint64_t *bar, int blk, int h, uint64_t policy) {
+    using Sh = WindowShape<D, MANY>;
+    const bool bad_blk = blk < 0 || blk >= p.num_blocks;
+    if (bad_blk) set_status(p.dev_status, PKV_DEV_BAD_BLOCK_ID);
+    // past the end for a bad block id: the load fills zeros
+    const int y = bad_blk ? p.num_blocks * p.Hkv * 16 : (blk * p.Hkv + h) * 16;
+    mbar_arrive_expect_tx(bar, Sh::STAGE_BYTES);
+#pragma unroll
+    for (int hf = 0; hf < Sh::HALVES; ++hf) {
+        tma_load_2d(slot + hf * Sh::HALF_BYTES, tk, hf * 64, y, bar, policy);
+        tma_load_2d(slot + Sh::TILE_BYTES + hf * Sh::HALF_BYTES, tv, hf * 64, y, bar, policy);
+    }
+}
+
+// A warp's part of a range: query fragments (rows = heads of the group, padded
+// to 16), accumulator, running maximum and sum.
+template <typename T, int D, int NT, bool MANY>
+struct WarpPart {
+    using Sh = WindowShape<D, MANY>;
+    static constexpr int STEP = Sh::STEP;
+    uint32_t qa[D / 16][4];
+    float acc[D / 16][NT][4];
+    float m_run[NT], l_run[NT];
+
+    // q: G rows of D elements
+    __device__ __forceinline__ void start(const uint32_t *q, int G, int lane) {
+        const int g = lane >> 2, t4 = lane & 3;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+            const int c0 = (kk * 16 + 2 * t4) >> 1;
+            qa[kk][0] = g < G ? q[g * (D / 2) + c0] : 0u;
+            qa[kk][2] = g < G ? q[g * (D / 2) + c0 + 4] : 0u;
+            if constexpr (NT == 1) {   // group of at most 8 heads: rows 8..15 are padding
+                qa[kk][1] = 0u;
+                qa[kk][3] = 0u;
+            } else {
+                qa[kk][1] = g + 8 < G ? q[(g + 8) * (D / 2) + c0] : 0u;
+                qa[kk][3] = g + 8 < G ? q[(g + 8) * (D / 2) + c0 + 4] : 0u;
+            }
+        }
+#pragma unroll
+        for (int mt = 0; mt < D / 16; ++mt)
+#pragma unroll
+            for (int pn = 0; pn < NT; ++pn)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[mt][pn][e] = 0.f;
+#pragma unroll
+        for (int pn = 0; pn < NT; ++pn) {
+            m_run[pn] = -INFINITY;
+            l_run[pn] = 0.f;
+        }
+    }
+
+    // STEP blocks of 16 tokens in ring slots at `slot`, bit t of `bits` set
+    // where token t of them is seen (some token of the first block is).
+    // `release` runs once the slots have been read.
+    template <typename F>
+    __device__ __forceinline__ void attend(const uint32_t (&slot)[STEP], uint32_t bits, float scale_log2, int lane,
+                                           F release) {
+        const int t4 = lane & 3, mi = lane >> 3;
+        const int row = ((mi >> 1) << 3) + (lane & 7);   // token row this lane addresses
+        const int sw = row & 7;                           // 128-byte swizzle phase of that row
+        auto at = [&](int kk) {
+            const int chunk = ((kk & 3) << 1) + (mi & 1);
+            return (uint32_t)((kk >> 2) * Sh::HALF_BYTES + row * 128 + ((chunk ^ sw) << 4));
+        };
+        // S = Q K^T, two chains per 8-token tile
+        float s0[2 * STEP][4], s1[2 * STEP][4];
+#pragma unroll
+        for (int nt = 0; nt < 2 * STEP; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s0[nt][e] = s1[nt][e] = 0.f;
+#pragma unroll
+        for (int b = 0; b < STEP; ++b) {
+            uint32_t kf[D / 16][4];
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) ldsm_x4(slot[b] + at(kk), kf[kk][0], kf[kk][1], kf[kk][2], kf[kk][3]);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; kk += 2) {
+                mma_16816<T>(s0[2 * b], qa[kk], kf[kk][0], kf[kk][1]);
+                mma_16816<T>(s0[2 * b + 1], qa[kk], kf[kk][2], kf[kk][3]);
+                mma_16816<T>(s1[2 * b], qa[kk + 1], kf[kk + 1][0], kf[kk + 1][1]);
+                mma_16816<T>(s1[2 * b + 1], qa[kk + 1], kf[kk + 1][2], kf[kk + 1][3]);
+            }
+        }
+        uint32_t vf[STEP][D / 16][4];
+#pragma unroll
+        for (int b = 0; b < STEP; ++b)
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+                ldsm_x4_t(slot[b] + Sh::TILE_BYTES + at(kk), vf[b][kk][0], vf[b][kk][1], vf[b][kk][2], vf[b][kk][3]);
+        release();
+
+        float pr[2 * STEP][2 * NT];
+        float alpha[NT];
+        bool moved = false;
+#pragma unroll
+        for (int pn = 0; pn < NT; ++pn) {
+            float x[2 * STEP][2];
+            float mx = -INFINITY;
+#pragma unroll
+            for (int nt = 0; nt < 2 * STEP; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float v = (s0[nt][pn * 2 + e] + s1[nt][pn * 2 + e]) * scale_log2;
+                    x[nt][e] = (bits >> (nt * 8 + 2 * t4 + e)) & 1u ? v : -INFINITY;
+                    mx = fmaxf(mx, x[nt][e]);
+                }
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            // the maximum is only moved when it grows by more than 2^8
+            const bool move = m_run[pn] == -INFINITY || mx > m_run[pn] + 8.f;
+            const float m_new = move ? fmaxf(m_run[pn], mx) : m_run[pn];
+            // no finite score so far (keys of infinities): nothing to subtract
+            const float sub = m_new == -INFINITY ? 0.f : m_new;
+            alpha[pn] = move ? exp2_approx(m_run[pn] - sub) : 1.f;
+            moved |= move;
+            m_run[pn] = m_new;
+            float rs = 0.f;
+#pragma unroll
+            for (int nt = 0; nt < 2 * STEP; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    pr[nt][pn * 2 + e] = exp2_approx(x[nt][e] - sub);
+                    rs += pr[nt][pn * 2 + e];
+                }
+            l_run[pn] = l_run[pn] * alpha[pn] + rs;
+        }
+        // hidden positions may hold anything (even NaN): clear their V values
+        // in the fragments, so that 0 x garbage cannot reach the accumulator.
+        // Registers 0/1 hold tokens 2 t4 (low half) and 2 t4 + 1, 2/3 the same
+        // tokens + 8.
+        if (bits != (uint32_t)((1ull << (16 * STEP)) - 1u)) {
+#pragma unroll
+            for (int b = 0; b < STEP; ++b) {
+                const uint32_t w = bits >> (16 * b + 2 * t4);
+                const uint32_t m01 = (w & 1u ? 0x0000ffffu : 0u) | (w & 2u ? 0xffff0000u : 0u);
+                const uint32_t m23 = (w & 0x100u ? 0x0000ffffu : 0u) | (w & 0x200u ? 0xffff0000u : 0u);
+#pragma unroll
+                for (int mt = 0; mt < D / 16; ++mt) {
+                    vf[b][mt][0] &= m01;
+                    vf[b][mt][1] &= m01;
+                    vf[b][mt][2] &= m23;
+                    vf[b][mt][3] &= m23;
+                }
+            }
+        }
+        if (__any_sync(0xffffffffu, moved))
+#pragma unroll
+            for (int pn = 0; pn < NT; ++pn) {
+                const float a_lo = __shfl_sync(0xffffffffu, alpha[pn], 8 * t4);
+                const float a_hi = __shfl_sync(0xffffffffu, alpha[pn], 8 * t4 + 4);
+#pragma unroll
+                for (int mt = 0; mt < D / 16; ++mt) {
+                    acc[mt][pn][0] *= a_lo;
+                    acc[mt][pn][1] *= a_hi;
+                    acc[mt][pn][2] *= a_lo;
+                    acc[mt][pn][3] *= a_hi;
+                }
+            }
+        // O^T += V^T P^T, P as a rounded 16-bit value and its rounding
+        // residual: the weights keep about 16 significant bits
+#pragma unroll
+        for (int b = 0; b < STEP; ++b) {
+            uint32_t pb0[NT][2], pb1[NT][2];
+#pragma unroll
+            for (int pn = 0; pn < NT; ++pn) {
+                pack2_split<T>(pr[2 * b][pn * 2], pr[2 * b][pn * 2 + 1], pb0[pn][0], pb0[pn][1]);
+                pack2_split<T>(pr[2 * b + 1][pn * 2], pr[2 * b + 1][pn * 2 + 1], pb1[pn][0], pb1[pn][1]);
+            }
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int mt = 0; mt < D / 16; ++mt)
+#pragma unroll
+                    for (int pn = 0; pn < NT; ++pn) mma_16816<T>(acc[mt][pn], vf[b][mt], pb0[pn][r], pb1[pn][r]);
+        }
+    }
+
+    // The rows' sums over their lanes; lane t4 == 0 of row g then holds row
+    // 8 pn + g's in l_run[pn].
+    __device__ __forceinline__ void finish() {
+#pragma unroll
+        for (int pn = 0; pn < NT; ++pn) {
+            l_run[pn] += __shfl_xor_sync(0xffffffffu, l_run[pn], 1);
+            l_run[pn] += __shfl_xor_sync(0xffffffffu, l_run[pn], 2);
+        }
+    }
+
+    // (m, l) of the heads at ml[head], ml[16 + head]; accumulators at part[head * D + d].
+    __device__ __forceinline__ void store(float *ml, float *part, int G, int lane) const {
+        const int g = lane >> 2, t4 = lane & 3;
+#pragma unroll
+        for (int pn = 0; pn < NT; ++pn) {
+            if (t4 == 0) {
+                ml[pn * 8 + g] = m_run[pn];
+                ml[16 + pn * 8 + g] = l_run[pn];
+            }
+            const int ha = pn * 8 + 2 * t4, hb = ha + 1;
+#pragma unroll
+            for (int mt = 0; mt < D / 16; ++mt) {
+                const int d0 = mt * 16 + g;
+                if (ha < G) {
+                    part[ha * D + d0] = acc[mt][pn][0];
+                    part[ha * D + d0 + 8] = acc[mt][pn][2];
+                }
+                if (hb < G) {
+                    part[hb * D + d0] = acc[mt][pn][1];
+                    part[hb * D + d0 + 8] = acc[mt][pn][3];
+                }
+            }
+        }
+    }
+};
+
+template <typename T, int D, int NT, bool MANY>
+__global__ void __launch_bounds__(kWinWarps * 32, NT == 1 ? WindowShape<D, MANY>::PER_SM : 2)
     window_decode_kernel(const WindowDecodeParams p, const __grid_constant__ CUtensorMap tk,
                          const __grid_constant__ CUtensorMap tv) {
-    using Sh = WindowShape<D>;
-    constexpr int STAGES = Sh::STAGES;
+    using Sh = WindowShape<D, MANY>;
+    constexpr int STAGES = Sh::STAGES, STEP = Sh::STEP;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Sh::RING_BYTES);
@@ -95,244 +348,67 @@ __global__ void __launch_bounds__(kWinWarps * 32, 2)
     pdl_launch_dependents();
 
     // ---- the range's visible blocks, and this warp's share ----
-    int ctx = __ldg(p.context_lens + s);
-    if (ctx < 0 || ctx > p.max_blocks * 16) {
-        if (tid == 0 && rank == 0 && h == 0) set_status(p.dev_status, PKV_DEV_BAD_CONTEXT);
-        ctx = ctx < 0 ? 0 : p.max_blocks * 16;
-    }
-    const int nblk = (ctx + 15) >> 4;
-    const int w0 = max(ctx - p.window, 0);                   // the window's first position
-    const int sink_blocks = min((p.sinks + 15) >> 4, nblk);
-    const int skip = max((w0 >> 4) - sink_blocks, 0);
-    const int visible = nblk - skip;
-    const int v_lo = (int)((int64_t)visible * rank / ranks), v_hi = (int)((int64_t)visible * (rank + 1) / ranks);
+    const Visible vis(p, __ldg(p.context_lens + s));
+    if (vis.bad && tid == 0 && rank == 0 && h == 0) set_status(p.dev_status, PKV_DEV_BAD_CONTEXT);
+    const int v_lo = (int)((int64_t)vis.count * rank / ranks), v_hi = (int)((int64_t)vis.count * (rank + 1) / ranks);
     const int n = max(0, (v_hi - v_lo - warp + kWinWarps - 1) / kWinWarps);
-    auto logical = [&](int i) {
-        const int v = v_lo + warp + kWinWarps * i;
-        return v < sink_blocks ? v : v + skip;
-    };
+    auto logical = [&](int i) { return vis.logical(v_lo + warp + kWinWarps * i); };
     const int32_t *row = p.block_tables + (int64_t)s * p.max_blocks;
     int ids = lane < n ? __ldg(row + logical(lane)) : 0;     // lane i: the id of this warp's block 32 k + i
     const uint64_t policy = l2_policy_evict_first();
     auto issue = [&](int i) {
         const int blk = __shfl_sync(0xffffffffu, ids, i & 31);
-        if (lane == 0) {
-            const bool bad_blk = blk < 0 || blk >= p.num_blocks;
-            if (bad_blk) set_status(p.dev_status, PKV_DEV_BAD_BLOCK_ID);
-            // past the end for a bad block id: the load fills zeros
-            const int y = bad_blk ? p.num_blocks * p.Hkv * 16 : (blk * p.Hkv + h) * 16;
-            uint64_t *bar = &wbar[i % STAGES];
-            mbar_arrive_expect_tx(bar, Sh::STAGE_BYTES);
-            uint8_t *kdst = wring + (i % STAGES) * Sh::STAGE_BYTES;
-#pragma unroll
-            for (int hf = 0; hf < Sh::HALVES; ++hf) {
-                tma_load_2d(kdst + hf * Sh::HALF_BYTES, &tk, hf * 64, y, bar, policy);
-                tma_load_2d(kdst + Sh::TILE_BYTES + hf * Sh::HALF_BYTES, &tv, hf * 64, y, bar, policy);
-            }
-        }
+        if (lane == 0)
+            issue_block<D, MANY>(p, &tk, &tv, wring + (i % STAGES) * Sh::STAGE_BYTES, &wbar[i % STAGES], blk, h, policy);
     };
     int issued = 0;
     for (; issued < min(n, STAGES); ++issued) issue(issued);
 
-    // ---- query fragments: rows = heads of the group, padded to 16 ----
-    const int g = lane >> 2, t4 = lane & 3;
-    uint32_t qa[D / 16][4];
-    {
-        const uint32_t *qbase =
-            reinterpret_cast<const uint32_t *>(static_cast<const T *>(p.q) + ((int64_t)s * p.Hq + (int64_t)h * G) * D);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-            const int c0 = (kk * 16 + 2 * t4) >> 1;
-            qa[kk][0] = g < G ? __ldg(qbase + g * (D / 2) + c0) : 0u;
-            qa[kk][2] = g < G ? __ldg(qbase + g * (D / 2) + c0 + 4) : 0u;
-            if constexpr (NT == 1) {   // group of at most 8 heads: rows 8..15 are padding
-                qa[kk][1] = 0u;
-                qa[kk][3] = 0u;
-            } else {
-                qa[kk][1] = g + 8 < G ? __ldg(qbase + (g + 8) * (D / 2) + c0) : 0u;
-                qa[kk][3] = g + 8 < G ? __ldg(qbase + (g + 8) * (D / 2) + c0 + 4) : 0u;
-            }
-        }
-    }
-    float acc[D / 16][NT][4];
-    float m_run[NT], l_run[NT];
-#pragma unroll
-    for (int mt = 0; mt < D / 16; ++mt)
-#pragma unroll
-        for (int pn = 0; pn < NT; ++pn)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[mt][pn][e] = 0.f;
-#pragma unroll
-    for (int pn = 0; pn < NT; ++pn) {
-        m_run[pn] = -INFINITY;
-        l_run[pn] = 0.f;
-    }
-    const int mi = lane >> 3;
-    const int ld_row = ((mi >> 1) << 3) + (lane & 7);   // token row this lane addresses
-    const int ld_sw = ld_row & 7;                        // 128-byte swizzle phase of that row
+    WarpPart<T, D, NT, MANY> part_w;
+    part_w.start(reinterpret_cast<const uint32_t *>(static_cast<const T *>(p.q) + ((int64_t)s * p.Hq + (int64_t)h * G) * D),
+                 G, lane);
     const uint32_t ring_addr = smem_addr(wring);
 
     bool timed_out = false;
-    int i = 0;
-    for (; i < n; ++i) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&wbar[i % STAGES], (uint32_t)(i / STAGES) & 1u, kWinWaitNs))) {
+    int i = 0;   // blocks taken
+    while (i < n) {
+        // an odd block out is taken with itself, the second time all hidden
+        const int k = min(STEP, n - i);
+        uint32_t slot[STEP], bits = 0;
+        bool ok = true;
+#pragma unroll
+        for (int b = 0; b < STEP; ++b) {
+            const int x = i + min(b, k - 1);
+            ok = ok && mbar_wait(&wbar[x % STAGES], (uint32_t)(x / STAGES) & 1u, kWinWaitNs);
+            slot[b] = ring_addr + (x % STAGES) * Sh::STAGE_BYTES;
+            if (b < k) bits |= vis.bits(logical(x), p.sinks) << (16 * b);
+        }
+        if (!__all_sync(0xffffffffu, ok)) {
             timed_out = true;
             break;
         }
-        const uint32_t kbase = ring_addr + (i % STAGES) * Sh::STAGE_BYTES;
-        const uint32_t vbase = kbase + Sh::TILE_BYTES;
-        // the block's fragments into registers, then its slot back to the TMA engine
-        uint32_t kf[D / 16][4], vf[D / 16][4];
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-            const int chunk = ((kk & 3) << 1) + (mi & 1);
-            const uint32_t off = (kk >> 2) * Sh::HALF_BYTES + ld_row * 128 + ((chunk ^ ld_sw) << 4);
-            ldsm_x4(kbase + off, kf[kk][0], kf[kk][1], kf[kk][2], kf[kk][3]);
-            ldsm_x4_t(vbase + off, vf[kk][0], vf[kk][1], vf[kk][2], vf[kk][3]);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (issued < n) {
-            if ((issued & 31) == 0) ids = issued + lane < n ? __ldg(row + logical(issued + lane)) : 0;
-            issue(issued);
-            ++issued;
-        }
-
-        // S = Q K^T over the block's 16 tokens, two chains per 8-token tile
-        float sacc[2][4], sacc2[2][4];
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sacc[nt][e] = sacc2[nt][e] = 0.f;
-#pragma unroll
-        for (int kk = 0; kk < D / 16; kk += 2) {
-            mma_16816<T>(sacc[0], qa[kk], kf[kk][0], kf[kk][1]);
-            mma_16816<T>(sacc[1], qa[kk], kf[kk][2], kf[kk][3]);
-            mma_16816<T>(sacc2[0], qa[kk + 1], kf[kk + 1][0], kf[kk + 1][1]);
-            mma_16816<T>(sacc2[1], qa[kk + 1], kf[kk + 1][2], kf[kk + 1][3]);
-        }
-
-        // the block's visible tokens, one bit each (never none): before ctx,
-        // and in the window or among the first tokens
-        const int t0 = logical(i) * 16;
-        const int lim = min(ctx - t0, 16), first = min(max(w0 - t0, 0), 16), sk = min(max(p.sinks - t0, 0), 16);
-        const uint32_t bits = ((1u << lim) - 1u) & ((0xffffu << first) | ((1u << sk) - 1u)) & 0xffffu;
-        float pr[2][4];
-        float alpha[NT];
-#pragma unroll
-        for (int pn = 0; pn < NT; ++pn) {
-            float x[2][2];
-            float mx = -INFINITY;
-#pragma unroll
-            for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int tok = nt * 8 + 2 * t4 + e;
-                    const float v = (sacc[nt][pn * 2 + e] + sacc2[nt][pn * 2 + e]) * p.scale_log2;
-                    x[nt][e] = (bits >> tok) & 1u ? v : -INFINITY;
-                    mx = fmaxf(mx, x[nt][e]);
-                }
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            const float m_new = fmaxf(m_run[pn], mx);
-            // no finite score so far (keys of infinities): nothing to subtract
-            const float sub = m_new == -INFINITY ? 0.f : m_new;
-            alpha[pn] = exp2_approx(m_run[pn] - sub);
-            m_run[pn] = m_new;
-            float rs = 0.f;
-#pragma unroll
-            for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    pr[nt][pn * 2 + e] = exp2_approx(x[nt][e] - sub);
-                    rs += pr[nt][pn * 2 + e];
-                }
-            l_run[pn] = l_run[pn] * alpha[pn] + rs;
-        }
-        // hidden positions may hold anything (even NaN): clear their V values
-        // in the fragments, so that 0 x garbage cannot reach the accumulator.
-        // Registers 0/1 hold tokens 2 t4 (low half) and 2 t4 + 1, 2/3 the same
-        // tokens + 8.
-        if (bits != 0xffffu) {
-            const uint32_t b = bits >> (2 * t4);
-            const uint32_t m01 = (b & 1u ? 0x0000ffffu : 0u) | (b & 2u ? 0xffff0000u : 0u);
-            const uint32_t m23 = (b & 0x100u ? 0x0000ffffu : 0u) | (b & 0x200u ? 0xffff0000u : 0u);
-#pragma unroll
-            for (int mt = 0; mt < D / 16; ++mt) {
-                vf[mt][0] &= m01;
-                vf[mt][1] &= m01;
-                vf[mt][2] &= m23;
-                vf[mt][3] &= m23;
+        i += k;
+        part_w.attend(slot, bits, p.scale_log2, lane, [&] {
+            fence_proxy_async_smem();
+            __syncwarp();
+            for (int u = 0; u < k && issued < n; ++u, ++issued) {
+                if ((issued & 31) == 0) ids = issued + lane < n ? __ldg(row + logical(issued + lane)) : 0;
+                issue(issued);
             }
-        }
-        // rescale the accumulator (only when a row's maximum moved), O^T += V^T P^T
-        bool moved = false;
-#pragma unroll
-        for (int pn = 0; pn < NT; ++pn) moved |= alpha[pn] != 1.f;
-        if (__any_sync(0xffffffffu, moved))
-#pragma unroll
-            for (int pn = 0; pn < NT; ++pn) {
-                const float a_lo = __shfl_sync(0xffffffffu, alpha[pn], 8 * t4);
-                const float a_hi = __shfl_sync(0xffffffffu, alpha[pn], 8 * t4 + 4);
-#pragma unroll
-                for (int mt = 0; mt < D / 16; ++mt) {
-                    acc[mt][pn][0] *= a_lo;
-                    acc[mt][pn][1] *= a_hi;
-                    acc[mt][pn][2] *= a_lo;
-                    acc[mt][pn][3] *= a_hi;
-                }
-            }
-        // P as a rounded 16-bit value and its rounding residual: the weights
-        // keep about 16 significant bits
-        uint32_t pb0[NT][2], pb1[NT][2];
-#pragma unroll
-        for (int pn = 0; pn < NT; ++pn) {
-            pack2_split<T>(pr[0][pn * 2], pr[0][pn * 2 + 1], pb0[pn][0], pb0[pn][1]);
-            pack2_split<T>(pr[1][pn * 2], pr[1][pn * 2 + 1], pb1[pn][0], pb1[pn][1]);
-        }
-#pragma unroll
-        for (int mt = 0; mt < D / 16; ++mt) {
-#pragma unroll
-            for (int pn = 0; pn < NT; ++pn) {
-                mma_16816<T>(acc[mt][pn], vf[mt], pb0[pn][0], pb1[pn][0]);
-                mma_16816<T>(acc[mt][pn], vf[mt], pb0[pn][1], pb1[pn][1]);
-            }
-        }
+        });
     }
     if (timed_out) {
         if (lane == 0) set_status(p.dev_status, PKV_DEV_WAIT_TIMEOUT);
         // what is still in flight must land before the ring is used again
-        for (int k = i + 1; k < issued; ++k) mbar_wait(&wbar[k % STAGES], (uint32_t)(k / STAGES) & 1u, kWinWaitNs / 8);
+        for (int k = i; k < issued; ++k) mbar_wait(&wbar[k % STAGES], (uint32_t)(k / STAGES) & 1u, kWinWaitNs / 8);
     }
 
     // ---- the warps' parts: (m, l) per head, accumulators [warp][head][d] over the ring ----
     __syncthreads();   // every warp is done with its slots
     float *part = reinterpret_cast<float *>(smem);
     const int GD = G * D;
-#pragma unroll
-    for (int pn = 0; pn < NT; ++pn) {
-        float l = l_run[pn];
-        l += __shfl_xor_sync(0xffffffffu, l, 1);
-        l += __shfl_xor_sync(0xffffffffu, l, 2);
-        if (t4 == 0) {
-            ml[warp * 32 + pn * 8 + g] = m_run[pn];
-            ml[warp * 32 + 16 + pn * 8 + g] = l;
-        }
-        const int ha = pn * 8 + 2 * t4, hb = ha + 1;
-        float *wp = part + warp * GD;
-#pragma unroll
-        for (int mt = 0; mt < D / 16; ++mt) {
-            const int d0 = mt * 16 + g;
-            if (ha < G) {
-                wp[ha * D + d0] = acc[mt][pn][0];
-                wp[ha * D + d0 + 8] = acc[mt][pn][2];
-            }
-            if (hb < G) {
-                wp[hb * D + d0] = acc[mt][pn][1];
-                wp[hb * D + d0 + 8] = acc[mt][pn][3];
-            }
-        }
-    }
+    part_w.finish();
+    part_w.store(ml + warp * 32, part + warp * GD, G, lane);
     __syncthreads();
     float *comb = part + kWinWarps * GD;   // the CTA's accumulators, unnormalised
     float *cml = ml + kWinWarps * 32;
@@ -351,7 +427,7 @@ __global__ void __launch_bounds__(kWinWarps * 32, 2)
             L += f * ml[w * 32 + 16 + hh];
         }
         if (ranks == 1) {
-            store_out<T>(p.out, p.out_dtype, ob + e, visible > 0 ? o / L : 0.f);
+            store_out<T>(p.out, p.out_dtype, ob + e, vis.count > 0 ? o / L : 0.f);
         } else {
             comb[e] = o;
             if (e % D == 0) {
@@ -393,27 +469,53 @@ __global__ void __launch_bounds__(kWinWarps * 32, 2)
             }
             M = Mn;
         }
-        store_out<T>(p.out, p.out_dtype, ob + e, visible > 0 ? o / L : 0.f);
+        store_out<T>(p.out, p.out_dtype, ob + e, vis.count > 0 ? o / L : 0.f);
     }
     cluster_sync();   // a CTA's shared memory outlives its readers
 }
 
-template <typename T, int D, int NT>
+template <typename T, int D, int NT, bool MANY>
 static int launch_window_decode(const WindowDecodeParams &prm, const CUtensorMap &tk, const CUtensorMap &tv, int grid,
                                 int ranks, cudaStream_t stream) {
+    constexpr int kSmem = WindowShape<D, MANY>::SMEM_BYTES;
     static unsigned long long attr_set = 0;   // per instantiation and device
     if (!done_on_device(&attr_set)) {
-        cudaError_t e = cudaFuncSetAttribute(window_decode_kernel<T, D, NT>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, WindowShape<D>::SMEM_BYTES);
+        cudaError_t e = cudaFuncSetAttribute(window_decode_kernel<T, D, NT, MANY>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
         if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(window_decode_kernel<T, D, NT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            e = cudaFuncSetAttribute(window_decode_kernel<T, D, NT, MANY>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return cuda_fail(e);
         mark_done_on_device(&attr_set);
     }
-    cudaError_t e = launch_cluster(window_decode_kernel<T, D, NT>, grid, ranks, kWinWarps * 32,
-                                   WindowShape<D>::SMEM_BYTES, stream, prm, tk, tv);
+    cudaError_t e = launch_cluster(window_decode_kernel<T, D, NT, MANY>, grid, ranks, kWinWarps * 32, kSmem, stream, prm, tk,
+                                   tv);
     if (e == cudaSuccess) e = cudaGetLastError();
     return e == cudaSuccess ? PKV_OK : cuda_fail(e);
+}
+
+// The form and the CTAs per range, from the number of ranges, the blocks that
+// one can have, and whether MANY is built for the group size.
+template <typename T, int D>
+static int window_decode(const WindowDecodeParams &prm, const CUtensorMap &tk, const CUtensorMap &tv, int64_t ranges,
+                         int64_t blocks, int sms, cudaStream_t stream) {
+    constexpr int kFew = WindowShape<D, false>::PER_SM, kMany = WindowShape<D, true>::PER_SM;
+    // CTAs per range: as many as all fit on the GPU at once, each with at least
+    // two blocks a warp.  A second wave of clusters costs more than it evens
+    // out: 16 sequences x 8 heads x 65 blocks take 14.9 us in 256 CTAs and 19.1
+    // us in 512; 4 x 8 x 257 14.2 us in 256 and 24.3 us in 512.
+    int ranks = (int)std::min<int64_t>({kWinMaxCluster, 2 * sms / ranges, blocks / (2 * kWinWarps)});
+    if (ranks > 8 && ranks < kWinMaxCluster) ranks = 8;
+    if (ranks < 1) ranks = 1;
+    const int grid = (int)(ranges * ranks);
+    if (prm.G > 8) return launch_window_decode<T, D, 2, false>(prm, tk, tv, grid, ranks, stream);
+    // ranges of equal length pay for the last wave: its CTAs at half or a third
+    // of an SM's rate each (64 x 8 ranges of 65 blocks: 45.2 us in 1.7 waves of
+    // two, 50.8 us in 1.1 waves of three).  Of many waves, or of short ranges,
+    // MANY is the better one all the same.
+    auto waves = [&](int per_sm) { return (ranges + per_sm * sms - 1) / (per_sm * sms) * per_sm; };
+    if (ranges > 2 * sms && (ranges >= 6 * sms || blocks <= 32 || waves(kMany) <= waves(kFew)))
+        return launch_window_decode<T, D, 1, true>(prm, tk, tv, grid, ranks, stream);
+    return launch_window_decode<T, D, 1, false>(prm, tk, tv, grid, ranks, stream);
 }
 
 }  // namespace pkv
@@ -441,7 +543,7 @@ extern "C" int pkv_paged_window_decode_attention(void *out, const void *q, const
     if ((int64_t)num_seqs * num_kv_heads * kWinMaxCluster >= (int64_t)1 << 31) return PKV_ERR_UNSUPPORTED;
     if (num_seqs == 0) return PKV_OK;
     if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens) return PKV_ERR_INVALID_ARG;
-    if (!aligned(q, 4) || !aligned(out, 4) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
         !aligned(block_tables, 4) || !aligned(context_lens, 4))
         return PKV_ERR_INVALID_ARG;
     int sms = 0;
@@ -468,29 +570,13 @@ extern "C" int pkv_paged_window_decode_attention(void *out, const void *q, const
     prm.sinks = num_sinks < capacity ? num_sinks : (int)capacity;
     prm.scale_log2 = scale * 1.4426950408889634f;
     prm.out_dtype = out_dtype;
-    // CTAs per range: as many as all fit on the GPU at once (two per SM), each
-    // with at least two blocks a warp.  A second wave of clusters costs more
-    // than it evens out: 16 sequences x 8 heads x 65 blocks take 14.9 us in 256
-    // CTAs and 19.1 us in 512; 4 x 8 x 257 14.2 us in 256 and 24.3 us in 512.
-    const int64_t ranges = (int64_t)num_seqs * num_kv_heads;
     const int64_t most = ((int64_t)prm.sinks + 15) / 16 + ((int64_t)window + 14) / 16 + 1;
-    const int64_t blocks = most < max_blocks_per_seq ? most : max_blocks_per_seq;
-    int ranks = (int)std::min<int64_t>({kWinMaxCluster, 2 * sms / ranges, blocks / (2 * kWinWarps)});
-    if (ranks > 8 && ranks < kWinMaxCluster) ranks = 8;
-    if (ranks < 1) ranks = 1;
-    const int grid = (int)(ranges * ranks);
+    const int64_t blocks = std::min<int64_t>(most, max_blocks_per_seq);
+    const int64_t ranges = (int64_t)num_seqs * num_kv_heads;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const bool wide = G > 8;
-    if (dtype == PKV_DTYPE_BF16) {
-        if (head_dim == 128)
-            return wide ? launch_window_decode<__nv_bfloat16, 128, 2>(prm, tk, tv, grid, ranks, st)
-                        : launch_window_decode<__nv_bfloat16, 128, 1>(prm, tk, tv, grid, ranks, st);
-        return wide ? launch_window_decode<__nv_bfloat16, 64, 2>(prm, tk, tv, grid, ranks, st)
-                    : launch_window_decode<__nv_bfloat16, 64, 1>(prm, tk, tv, grid, ranks, st);
-    }
-    if (head_dim == 128)
-        return wide ? launch_window_decode<__half, 128, 2>(prm, tk, tv, grid, ranks, st)
-                    : launch_window_decode<__half, 128, 1>(prm, tk, tv, grid, ranks, st);
-    return wide ? launch_window_decode<__half, 64, 2>(prm, tk, tv, grid, ranks, st)
-                : launch_window_decode<__half, 64, 1>(prm, tk, tv, grid, ranks, st);
+    if (dtype == PKV_DTYPE_BF16)
+        return head_dim == 128 ? window_decode<__nv_bfloat16, 128>(prm, tk, tv, ranges, blocks, sms, st)
+                               : window_decode<__nv_bfloat16, 64>(prm, tk, tv, ranges, blocks, sms, st);
+    return head_dim == 128 ? window_decode<__half, 128>(prm, tk, tv, ranges, blocks, sms, st)
+                           : window_decode<__half, 64>(prm, tk, tv, ranges, blocks, sms, st);
 }

@@ -43,6 +43,7 @@
 #include <type_traits>
 
 #include "pkv.h"
+#include "pkv_cluster.cuh"
 #include "pkv_device.cuh"
 #include "pkv_host.h"
 #include "pkv_tc.cuh"
@@ -144,32 +145,6 @@ __device__ __forceinline__ void load_page(void *dst, const CUtensorMap *map, int
         : "memory");
 }
 
-// Asks the hardware to give this CTA the place of one that has not been
-// launched; the answer (16 bytes) completes on `bar`.
-__device__ __forceinline__ void cancel_next_cta(void *answer, uint64_t *bar) {
-    asm volatile(
-        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
-            smem_addr(answer)),
-        "r"(smem_addr(bar))
-        : "memory");
-}
-
-// The place taken over (blockIdx.x), or -1: all CTAs have been launched.
-__device__ __forceinline__ int cancelled_cta(const void *answer) {
-    uint32_t ok, x;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b128 a;\n\t.reg .b32 y, z, w;\n\t"
-        "ld.shared.b128 a, [%2];\n\t"
-        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t"
-        "mov.u32 %1, 0;\n\t"
-        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, y, z, w}, a;\n\t}"
-        : "=r"(ok), "=r"(x)
-        : "r"(smem_addr(answer))
-        : "memory");
-    return ok ? (int)x : -1;
-}
-
 template <typename T, int D, bool RESIDUAL>
 __global__ void __launch_bounds__(kWpThreads, 1)
     window_prefill_kernel(const WindowPrefillParams p, const __grid_constant__ CUtensorMap tk,
@@ -246,13 +221,16 @@ __global__ void __launch_bounds__(kWpThreads, 1)
             uint32_t g = 0;         // key tiles loaded
             uint32_t asked = 0;     // places asked for
             bool ok = true;
-            while (ok) {
-                // the next place is asked for while this one is worked on
-                if (lane == 0) {
+            bool asking = false;
+            auto ask = [&]() {
+                if (!asking && lane == 0) {
                     mbar_arrive_expect_tx(&bars->cancel, 16);
                     cancel_next_cta(sm + Sh::OFF_CANCEL, &bars->cancel);
                 }
-                ++asked;
+                asked += !asking;
+                asking = true;
+            };
+            while (ok) {
                 // place -> unit; chunk by chunk, the last pair of tiles first, the KV heads side by side
                 const int h = place % p.Hkv;
                 const int rest = place / p.Hkv;
@@ -297,6 +275,10 @@ __global__ void __launch_bounds__(kWpThreads, 1)
                     };
                     int blk_next = fetch(0);
                     for (int j = 0; ok && j < u.tiles; ++j, ++g) {
+                        // the next place is asked for near the unit's end: a
+                        // CTA that takes one sooner holds it back from others
+                        // (8 x 512 rows: 73.9 us when asked for at its start)
+                        if (j + 2 >= u.tiles) ask();
                         const int blk = blk_next;
                         if (j + 1 < u.tiles) blk_next = fetch(j + 1);
                         int y = p.num_blocks * p.Hkv * 2;      // 8-row group past the pool: zero fill
@@ -347,9 +329,10 @@ __global__ void __launch_bounds__(kWpThreads, 1)
                     ++n;
                 }
                 if (!ok) break;
-                // the place asked for
+                ask();
                 ok = wait_all(&bars->cancel, asked - 1);
                 if (!ok) break;
+                asking = false;
                 place = cancelled_cta(sm + Sh::OFF_CANCEL);
                 fence_proxy_async_smem();   // the answer is read before the next one is written
                 __syncwarp();
@@ -363,7 +346,7 @@ __global__ void __launch_bounds__(kWpThreads, 1)
             }
             if (!ok && lane == 0) {
                 // what is under way must land before the CTA leaves
-                mbar_wait(&bars->cancel, (asked - 1) & 1u, kWpWaitNs / 8);
+                if (asking) mbar_wait(&bars->cancel, (asked - 1) & 1u, kWpWaitNs / 8);
                 for (int st = 0; st < kWpStages; ++st) {
                     if (g > (uint32_t)st) {
                         const uint32_t last = (g - 1 - st) / kWpStages;

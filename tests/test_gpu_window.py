@@ -122,6 +122,37 @@ def test_decode_every_split(cuda_lib, S, hi, window):
         assert torch.equal(st.decode(F32), got)
 
 
+@pytest.mark.parametrize("window,sinks", [(1, 0), (16, 0), (33, 17), (200, 100), (700, 1), (100000, 0)])
+@pytest.mark.parametrize("Hq,Hkv,d,dtype,out_dtype", [(4, 4, 64, F16, F32), (32, 4, 128, BF16, F32), (12, 4, 128, F16, F16),
+                                                      (20, 4, 64, BF16, BF16)])
+def test_decode_many_ranges(cuda_lib, window, sinks, Hq, Hkv, d, dtype, out_dtype):
+    """More ranges than SMs: contexts from none to a few hundred tokens beside long ones, in one batch."""
+    ctx = [CONTEXTS[i % len(CONTEXTS)] if i % 3 else (i * 37) % 400 for i in range(100)]
+    st = Step(ctx, [1] * len(ctx), Hq, Hkv, d, dtype, window, sinks, seed=window % 83)
+    got = st.decode(out_dtype)
+    want, bound = st.reference(out_dtype)
+    ref.assert_within(got, want, bound, "window %d, sinks %d" % (window, sinks))
+    assert st.status.item() == 0
+    for _ in range(2):
+        assert torch.equal(st.decode(out_dtype), got)
+
+
+def test_decode_many_ranges_reports_bad_entries(cuda_lib):
+    ctx = [40 + i for i in range(200)]
+    st = Step(ctx, [1] * 200, 8, 2, 64, F16, 64, 4, poison=False)
+    st.table[60, 4] = 10 ** 6     # context 100, positions 64 to 79: visible, reads zeros
+    st.dev["table"] = st.table.cuda()
+    want, bound = st.reference(F32)
+    ref.assert_within(st.decode(F32), want, bound)
+    assert st.status.item() == 1
+    st.status.zero_()
+    st.dev["ctx"][3], st.dev["ctx"][5] = -7, 10 ** 8
+    got = st.decode(F32)
+    assert st.status.item() == 3 and (got[3] == 0).all() and torch.isfinite(got).all()
+    keep = [i for i in range(200) if i not in (3, 5)]
+    ref.assert_within(got[keep], want[keep], bound[keep])
+
+
 @pytest.mark.parametrize("window,sinks", WINDOWS)
 @pytest.mark.parametrize("Hq,Hkv,d,dtype,out_dtype", [(8, 2, 64, F16, F32), (4, 1, 128, BF16, F32), (8, 2, 128, BF16, BF16)])
 def test_prefill(cuda_lib, window, sinks, Hq, Hkv, d, dtype, out_dtype):
@@ -240,6 +271,13 @@ def test_captured_and_on_side_streams(cuda_lib):
         gp.replay()
         ref.assert_within(od, *st.reference(F32))
         ref.assert_within(op, *pf.reference(F32))
+    many = Step([50 + i for i in range(200)], [1] * 200, 8, 2, 64, F16, 40, 4, poison=False)
+    gm = torch.cuda.CUDAGraph()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(gm, stream=side):
+        om = many.decode(F32)
+    gm.replay()
+    ref.assert_within(om, *many.reference(F32))
     streams = [torch.cuda.Stream() for _ in range(2)]
     torch.cuda.synchronize()
     outs = []

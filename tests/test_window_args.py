@@ -37,6 +37,7 @@ ATTENTION = [
     (dict(out=None), INVALID), (dict(q=None), INVALID), (dict(k_cache=None), INVALID), (dict(v_cache=None), INVALID),
     (dict(block_tables=None), INVALID), (dict(context_lens=None), INVALID), (dict(k_cache=FAKE + 8), INVALID),
     (dict(v_cache=FAKE + 2), INVALID), (dict(q=FAKE + 2), INVALID), (dict(out=FAKE + 2), INVALID),
+    (dict(q=FAKE + 8), INVALID), (dict(out=FAKE + 8), INVALID),
     (dict(block_tables=FAKE + 1), INVALID), (dict(context_lens=FAKE + 2), INVALID),
     (dict(num_seqs=0, out=None, q=None, k_cache=None, v_cache=None, block_tables=None, context_lens=None), 0)]
 
