@@ -9,7 +9,8 @@
 // far inside fp32's range, and O is rarely touched).
 //
 // What is walked.  A unit of work is 2 x 128 MMA rows (two adjacent tiles A and B
-// of 128 / G tokens x the G query heads that share a KV head), against the
+// of 128 / G tokens x the G query heads that share a KV head; or tile A alone,
+// where that fills the GPU better), against the
 // pages that one of its rows sees: those of the first tokens, then those from
 // its first row's window on, as one list of pages (page v of the list is logical
 // page v, or v + skip past the first tokens' pages) cut into key tiles of 8.
@@ -73,7 +74,7 @@ struct WindowPrefillParams {
     const int32_t *context_lens;
     int *dev_status;
     int max_blocks, num_blocks, Hq, Hkv, G;
-    int rtok, pairs_per_seq;
+    int rtok, units_per_seq;
     int window, sinks, total_q;
     float scale_log2;
     int out_dtype;
@@ -145,7 +146,8 @@ __device__ __forceinline__ void load_page(void *dst, const CUtensorMap *map, int
         : "memory");
 }
 
-template <typename T, int D, bool RESIDUAL>
+// TILES: query tiles of a unit, 2, or 1 (A alone)
+template <typename T, int D, bool RESIDUAL, int TILES>
 __global__ void __launch_bounds__(kWpThreads, 1)
     window_prefill_kernel(const WindowPrefillParams p, const __grid_constant__ CUtensorMap tk,
                           const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tq) {
@@ -161,7 +163,7 @@ __global__ void __launch_bounds__(kWpThreads, 1)
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars->unit_full[i], 1);
-            mbar_init(&bars->unit_empty[i], 11);   // warps 1 to 11
+            mbar_init(&bars->unit_empty[i], TILES == 2 ? 11 : 6);   // warps 1 to 11, or those of tile A and the cleaner
             mbar_init(&bars->s_full[i], 1);
             mbar_init(&bars->p_full[i][0], 4);
             mbar_init(&bars->p_full[i][1], 4);
@@ -169,12 +171,12 @@ __global__ void __launch_bounds__(kWpThreads, 1)
         }
         mbar_init(&bars->cancel, 1);
         mbar_init(&bars->q_full, 1);
-        mbar_init(&bars->q_empty, 2);   // both query tiles' products
+        mbar_init(&bars->q_empty, TILES);   // each query tile's products
         for (int s = 0; s < kWpStages; ++s) {
             mbar_init(&bars->k_full[s], 1);
             mbar_init(&bars->v_full[s], 1);
-            mbar_init(&bars->k_empty[s], 2);
-            mbar_init(&bars->v_empty[s], 2);
+            mbar_init(&bars->k_empty[s], TILES);
+            mbar_init(&bars->v_empty[s], TILES);
             mbar_init(&bars->v_clean[s], 1);
         }
         *gave_up = 0;
@@ -234,23 +236,23 @@ __global__ void __launch_bounds__(kWpThreads, 1)
                 // place -> unit; chunk by chunk, the last pair of tiles first, the KV heads side by side
                 const int h = place % p.Hkv;
                 const int rest = place / p.Hkv;
-                const int pair = p.pairs_per_seq - 1 - rest % p.pairs_per_seq;
-                const int c = rest / p.pairs_per_seq;
+                const int unit = p.units_per_seq - 1 - rest % p.units_per_seq;
+                const int c = rest / p.units_per_seq;
                 const int q0 = __ldg(p.cu_seqlens + c);
                 const int q_len = __ldg(p.cu_seqlens + c + 1) - q0;
                 const int ctx = __ldg(p.context_lens + c);
-                const int i0 = pair * 2 * p.rtok;
+                const int i0 = unit * TILES * p.rtok;
                 int bad = 0;
                 if (q_len < 0 || q_len > ctx || q0 < 0 || q_len > p.total_q - q0)
                     bad = PKV_DEV_BAD_CHUNK;
                 else if (ctx > p.max_blocks * 16)
                     bad = PKV_DEV_BAD_CONTEXT;
-                if (bad && pair == 0 && lane == 0) set_status(p.dev_status, bad);
+                if (bad && unit == 0 && lane == 0) set_status(p.dev_status, bad);
                 if (!bad && i0 < q_len) {
                     WpUnit u = {};
                     u.h = h;
                     u.row0 = q0 + i0;
-                    u.tokens = min(2 * p.rtok, q_len - i0);
+                    u.tokens = min(TILES * p.rtok, q_len - i0);
                     u.first = ctx - q_len + i0;
                     u.wpos = max(u.first - p.window + 1, 0);
                     const int sink_pages = min((p.sinks + 15) / 16, (ctx + 15) / 16);
@@ -306,9 +308,9 @@ __global__ void __launch_bounds__(kWpThreads, 1)
                                 // Q is free once the unit before has no S product left
                                 if (n > 0) ok = wait(&bars->q_empty, (uint32_t)(n - 1));
                                 if (ok) {
-                                    mbar_arrive_expect_tx(&bars->q_full, (uint32_t)(2 * Sh::HALVES * p.G * p.rtok * 128));
+                                    mbar_arrive_expect_tx(&bars->q_full, (uint32_t)(TILES * Sh::HALVES * p.G * p.rtok * 128));
 #pragma unroll
-                                    for (int t = 0; t < 2; ++t)
+                                    for (int t = 0; t < TILES; ++t)
 #pragma unroll
                                         for (int hf = 0; hf < Sh::HALVES; ++hf)
                                             tc::tma_load_3d(sm + Sh::OFF_Q + t * Sh::Q_BYTES + hf * Sh::Q_HALF, &tq, hf * 64,
@@ -388,7 +390,7 @@ __global__ void __launch_bounds__(kWpThreads, 1)
                 }
                 return true;
             };
-            for (int n = 0;; ++n) {
+            for (int n = 0; t < TILES; ++n) {
                 bool ok = wait_all(&bars->unit_full[n & 1], (uint32_t)(n / 2));
                 if (!ok) break;
                 const WpUnit u = units[n & 1];
@@ -470,7 +472,7 @@ __global__ void __launch_bounds__(kWpThreads, 1)
         const uint32_t ocol = scol + 128;
         const uint64_t scale2 = f2_pack(p.scale_log2, p.scale_log2);
         uint32_t g = 0;                                 // key tiles taken
-        bool ok = true;
+        bool ok = t < TILES;
         for (int n = 0; ok; ++n) {
             ok = wait_all(&bars->unit_full[n & 1], (uint32_t)(n / 2));
             if (!ok) break;
@@ -617,7 +619,7 @@ static int encode_page_map(CUtensorMap *map, const void *base, int num_blocks, i
     return encode_tiled_map(map, base, 4, dims, strides, box);
 }
 
-template <typename T, int D, bool RESIDUAL>
+template <typename T, int D, bool RESIDUAL, int TILES>
 static int launch_window_prefill(const WindowPrefillParams &prm, const CUtensorMap &tk, const CUtensorMap &tv,
                                  const CUtensorMap &tq, int grid, cudaStream_t stream) {
     using Sh = WpShape<D>;
@@ -627,7 +629,7 @@ static int launch_window_prefill(const WindowPrefillParams &prm, const CUtensorM
     static int regs_ok = 0;   // 0 unknown, 1 as sized, -1 not
     if (regs_ok == 0) {
         cudaFuncAttributes fa;
-        cudaError_t e = cudaFuncGetAttributes(&fa, window_prefill_kernel<T, D, RESIDUAL>);
+        cudaError_t e = cudaFuncGetAttributes(&fa, window_prefill_kernel<T, D, RESIDUAL, TILES>);
         if (e != cudaSuccess) return cuda_fail(e);
         regs_ok = fa.numRegs == kWpLaunchRegs ? 1 : -1;
         if (regs_ok < 0) {
@@ -640,12 +642,12 @@ static int launch_window_prefill(const WindowPrefillParams &prm, const CUtensorM
     if (regs_ok < 0) return PKV_ERR_UNSUPPORTED;
     static unsigned long long attr_set = 0;   // per instantiation and device
     if (!done_on_device(&attr_set)) {
-        cudaError_t e = cudaFuncSetAttribute(window_prefill_kernel<T, D, RESIDUAL>,
+        cudaError_t e = cudaFuncSetAttribute(window_prefill_kernel<T, D, RESIDUAL, TILES>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::SMEM_BYTES);
         if (e != cudaSuccess) return cuda_fail(e);
         mark_done_on_device(&attr_set);
     }
-    cudaError_t e = launch_pdl(window_prefill_kernel<T, D, RESIDUAL>, dim3(grid), dim3(kWpThreads), Sh::SMEM_BYTES, stream,
+    cudaError_t e = launch_pdl(window_prefill_kernel<T, D, RESIDUAL, TILES>, dim3(grid), dim3(kWpThreads), Sh::SMEM_BYTES, stream,
                                prm, tk, tv, tq);
     if (e == cudaSuccess) e = cudaGetLastError();
     return e == cudaSuccess ? PKV_OK : cuda_fail(e);
@@ -679,12 +681,23 @@ extern "C" int pkv_paged_window_prefill_attention(void *out, const void *q, cons
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
         !aligned(cu_seqlens, 4) || !aligned(block_tables, 4) || !aligned(context_lens, 4))
         return PKV_ERR_INVALID_ARG;
+    int sms = 0;
+    int rc = current_sm_count(&sms);
+    if (rc != PKV_OK) return rc;
     const int rtok = kWpRows / G;
-    const int pairs = (int)(((int64_t)max_q_len + 2 * rtok - 1) / (2 * rtok));
-    const int64_t grid = (int64_t)num_seqs * pairs * num_kv_heads;
+    // query tiles of a unit: two, which share every K and V tile; or one, when
+    // all units then run at once: a step of 128 keys takes # us with two tiles on
+    // an SM and # us with one (512 rows behind 4,096, window 1,024: 24.1 and 17.2
+    // us; three chunks of 3,500-4,100, which fill the GPU either way, 509 and 789).
+    // A 32-bit output always takes two.
+    auto units_of = [&](int tiles) { return ((int64_t)max_q_len + tiles * rtok - 1) / (tiles * rtok); };
+    const bool one = out_dtype != PKV_DTYPE_F32 && num_seqs * units_of(1) * num_kv_heads <= sms;
+    const int qtiles = one ? 1 : 2;
+    const int64_t grid = (int64_t)num_seqs * units_of(qtiles) * num_kv_heads;
     if (grid >= (int64_t)1 << 31) return PKV_ERR_UNSUPPORTED;
+    const int units = (int)units_of(qtiles);
     CUtensorMap tk, tv, tq;
-    int rc = encode_page_map(&tk, k_cache, num_blocks, num_kv_heads, head_dim);
+    rc = encode_page_map(&tk, k_cache, num_blocks, num_kv_heads, head_dim);
     if (rc != PKV_OK) return rc;
     rc = encode_page_map(&tv, v_cache, num_blocks, num_kv_heads, head_dim);
     if (rc != PKV_OK) return rc;
@@ -706,7 +719,8 @@ extern "C" int pkv_paged_window_prefill_attention(void *out, const void *q, cons
     prm.Hkv = num_kv_heads;
     prm.G = G;
     prm.rtok = rtok;
-    prm.pairs_per_seq = pairs;
+    prm.units_per_seq = units;
+
     const int64_t capacity = (int64_t)max_blocks_per_seq * 16;
     prm.window = window < capacity ? window : (int)capacity;   // no context is longer
     prm.sinks = num_sinks < capacity ? num_sinks : (int)capacity;
@@ -714,13 +728,20 @@ extern "C" int pkv_paged_window_prefill_attention(void *out, const void *q, cons
     prm.scale_log2 = scale * 1.4426950408889634f;
     prm.out_dtype = out_dtype;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    auto launch = [&](auto type, auto residual) {
+    auto launch = [&](auto type, auto residual, auto tiles) {
         using T = decltype(type);
         constexpr bool R = decltype(residual)::value;
-        return head_dim == 128 ? launch_window_prefill<T, 128, R>(prm, tk, tv, tq, (int)grid, st)
-                               : launch_window_prefill<T, 64, R>(prm, tk, tv, tq, (int)grid, st);
+        constexpr int N = decltype(tiles)::value;
+        return head_dim == 128 ? launch_window_prefill<T, 128, R, N>(prm, tk, tv, tq, (int)grid, st)
+                               : launch_window_prefill<T, 64, R, N>(prm, tk, tv, tq, (int)grid, st);
     };
+    using Yes = std::true_type;
+    using No = std::false_type;
+    std::integral_constant<int, 1> tile;
+    std::integral_constant<int, 2> tiles;
+    const bool bf16 = dtype == PKV_DTYPE_BF16;
     if (out_dtype == PKV_DTYPE_F32)
-        return dtype == PKV_DTYPE_BF16 ? launch(__nv_bfloat16(), std::true_type()) : launch(__half(), std::true_type());
-    return dtype == PKV_DTYPE_BF16 ? launch(__nv_bfloat16(), std::false_type()) : launch(__half(), std::false_type());
+        return bf16 ? launch(__nv_bfloat16(), Yes(), tiles) : launch(__half(), Yes(), tiles);
+    if (one) return bf16 ? launch(__nv_bfloat16(), No(), tile) : launch(__half(), No(), tile);
+    return bf16 ? launch(__nv_bfloat16(), No(), tiles) : launch(__half(), No(), tiles);
 }
