@@ -29,6 +29,7 @@
 namespace pkv {
 
 constexpr int kTabThreads = 1024;
+constexpr int kTabBatch = 4;     // sequences whose lengths a thread has under way
 constexpr int kTabCluster = 16;   // more than the portable 8: opted into at the first launch
 
 struct TablesParams {
@@ -97,7 +98,7 @@ __device__ __forceinline__ int last_at_most(const int *prefix, int n, int x) {
     return lo;
 }
 
-__global__ void __launch_bounds__(kTabThreads) step_tables_kernel(const TablesParams p) {
+__global__ void __launch_bounds__(kTabThreads, 1) step_tables_kernel(const TablesParams p) {
     extern __shared__ int tab_smem[];
     __shared__ Pair64 sh_scan[32];
     __shared__ int sh_bad;
@@ -117,30 +118,41 @@ __global__ void __launch_bounds__(kTabThreads) step_tables_kernel(const TablesPa
     const int per = (S + nt - 1) / nt;
     const int s_lo = min(S, tid * per), s_hi = min(S, s_lo + per);
     const int64_t limit = (int64_t)p.max_blocks * 16;
+    const int count = p.free_count[0];
     int bad = 0;
     Pair64 sum{0, 0};
-    for (int s = s_lo; s < s_hi; ++s) {
-        const int l = p.seq_lens[s], n = p.new_lens[s];
-        len[s] = l;
-        if (l < 0 || (int64_t)l + max(n, 0) > limit) {
-            bad |= PKV_DEV_BAD_CONTEXT;
-        } else if (n < 0 || n > p.max_tokens) {
-            bad |= PKV_DEV_BAD_CHUNK;
-        } else {
-            sum.a += n;
-            sum.b += (int)(((int64_t)l + n + 15) >> 4) - (int)(((int64_t)l + 15) >> 4);
+    for (int s0 = s_lo; s0 < s_hi; s0 += kTabBatch) {
+        int ls[kTabBatch], ns[kTabBatch];   // on their way together
+#pragma unroll
+        for (int i = 0; i < kTabBatch; ++i) {
+            ls[i] = s0 + i < s_hi ? p.seq_lens[s0 + i] : 0;
+            ns[i] = s0 + i < s_hi ? p.new_lens[s0 + i] : 0;
+        }
+#pragma unroll
+        for (int i = 0; i < kTabBatch; ++i) {
+            if (s0 + i >= s_hi) break;
+            const int l = ls[i], n = ns[i];
+            len[s0 + i] = l;
+            cu[s0 + i] = n;
+            if (l < 0 || (int64_t)l + max(n, 0) > limit) {
+                bad |= PKV_DEV_BAD_CONTEXT;
+            } else if (n < 0 || n > p.max_tokens) {
+                bad |= PKV_DEV_BAD_CHUNK;
+            } else {
+                sum.a += n;
+                sum.b += (int)(((int64_t)l + n + 15) >> 4) - (int)(((int64_t)l + 15) >> 4);
+            }
         }
     }
     Pair64 total;
     const Pair64 incl = cta_scan(sum, sh_scan, &total);
-    const int count = p.free_count[0];
     if (total.a > p.max_tokens) bad |= PKV_DEV_BAD_CHUNK;
     if (count < 0 || count > p.free_capacity || total.b > count) bad |= PKV_DEV_FREE_LIST;
     if (bad) atomicOr(&sh_bad, bad);
     {
         int64_t a = incl.a - sum.a, b = incl.b - sum.b;
         for (int s = s_lo; s < s_hi; ++s) {
-            const int l = len[s], n = p.new_lens[s];
+            const int l = len[s], n = cu[s];
             cu[s] = (int)a;
             bx[s] = (int)b;
             a += n;
@@ -167,48 +179,37 @@ __global__ void __launch_bounds__(kTabThreads) step_tables_kernel(const TablesPa
     }
     if (gt == 0) p.free_count_out[0] = fail ? count : count - bx[S];
 
-    // ---- the blocks taken ----
+    // ---- the blocks taken (a thread's first id is on its way while the tokens
+    // are laid out) ----
     const int taken = fail ? 0 : bx[S], tokens = fail ? 0 : cu[S];
+    const int32_t *top = p.free_list + count - 1;   // the k-th block taken is top[-k]
+    const int32_t first_id = gt < taken ? top[-gt] : 0;
     int status = 0;
-    for (int k = gt; k < taken; k += gn) {
-        const int s = last_at_most(bx, S, k);
-        const int32_t id = p.free_list[count - 1 - k];
-        if (id < 0 || id >= p.num_blocks) status |= PKV_DEV_BAD_BLOCK_ID;
-        p.block_tables[(int64_t)s * p.max_blocks + ((len[s] + 15) >> 4) + (k - bx[s])] = id;
-    }
 
     // ---- slots and positions, four rows at a time: a row's block is the
     // sequence's open block (in its table) or one of those taken now ----
     for (int64_t t0 = (int64_t)gt * 4; t0 < p.max_tokens; t0 += (int64_t)gn * 4) {
         int64_t slot[4];
-        int32_t pos[4];
+        int32_t pos[4], id[4];
         int s = t0 < tokens ? last_at_most(cu, S, (int)t0) : 0;
-        int64_t have = -1;   // block index whose id is in `id`, with its sequence
-        int32_t id = -1;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int64_t t = t0 + e;
-            slot[e] = -1;
+            id[e] = -1;
             pos[e] = 0;
             if (t < tokens) {
-                while (cu[s + 1] <= t) {   // skips sequences without new tokens
-                    ++s;
-                    have = -1;
-                }
+                while (cu[s + 1] <= t) ++s;   // skips sequences without new tokens
                 const int q = len[s] + (int)(t - cu[s]);
                 const int j = q >> 4, old = (len[s] + 15) >> 4;
-                if (have != j) {
-                    id = j < old ? p.block_tables[(int64_t)s * p.max_blocks + j]
-                                 : p.free_list[count - 1 - (bx[s] + j - old)];
-                    have = j;
-                    if (id < 0 || id >= p.num_blocks) {
-                        status |= PKV_DEV_BAD_BLOCK_ID;
-                        id = -1;
-                    }
-                }
                 pos[e] = q;
-                if (id >= 0) slot[e] = (int64_t)id * 16 + (q & 15);
+                id[e] = *(j < old ? p.block_tables + (int64_t)s * p.max_blocks + j : top - (bx[s] + j - old));
             }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const bool held = id[e] >= 0 && id[e] < p.num_blocks;
+            if (!held && t0 + e < tokens) status |= PKV_DEV_BAD_BLOCK_ID;
+            slot[e] = held ? (int64_t)id[e] * 16 + (pos[e] & 15) : -1;
         }
         if (p.vec && t0 + 4 <= p.max_tokens) {
             reinterpret_cast<longlong2 *>(p.slot_mapping + t0)[0] = make_longlong2(slot[0], slot[1]);
@@ -222,6 +223,12 @@ __global__ void __launch_bounds__(kTabThreads) step_tables_kernel(const TablesPa
                     p.token_pos[t0 + e] = pos[e];
                 }
         }
+    }
+    for (int k = gt; k < taken; k += gn) {
+        const int s = last_at_most(bx, S, k);
+        const int32_t id = k == gt ? first_id : top[-k];
+        if (id < 0 || id >= p.num_blocks) status |= PKV_DEV_BAD_BLOCK_ID;
+        p.block_tables[(int64_t)s * p.max_blocks + ((len[s] + 15) >> 4) + (k - bx[s])] = id;
     }
     if (status) set_status(p.dev_status, status);
 }
