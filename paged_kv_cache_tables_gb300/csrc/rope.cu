@@ -27,7 +27,12 @@
 // while they are under way works out what the rows share, the (cos, sin) of a
 // lane's eight pairs (the groups of lanes share the sincospi among them), the
 // weight, the slot and the addresses.  The arithmetic is on packed pairs of
-// floats.
+// floats.  16,383 tokens x 32 heads of 128 (268 MB in and out): 40.0 us, 99 % of
+// the measured copy rate; 4,344 tokens normed, rotated and appended (107 MB): 20.5
+// us, 77 %; 64 tokens: 1.6 us.  Before the loads were issued together: 50.2, 24.8
+// and 1.9 us.  Measured and left: CTAs of one warp (20.0 us, but calls of many
+// small rows are then bound by the launch of CTAs, about 3 a ns), key and value
+// heads in one warp (21.1 us).
 #include <cuda_runtime.h>
 
 #include <cmath>

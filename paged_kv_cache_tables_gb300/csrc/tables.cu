@@ -12,7 +12,8 @@
 //
 // What bounds it: latency.  The step of 4,020 sequences and 127,780 rows
 // writes 1.6 MB, 0.24 us at the measured copy rate; the launch, the reads of
-// the lengths and the scan are a chain of round trips several times as long.
+// the lengths, the scan and the reads of ids are a chain of round trips, 3.5 us
+// for 256 sequences and 9.4 us for those 4,020 (in 8 CTAs 11.6 us).
 // So everything is one launch without a workspace: a small step is one CTA;
 // a larger one is one cluster of CTAs, each of which scans all lengths itself
 // (at most 16,384 of them, out of L2) and fills its share of the outputs, its
@@ -274,9 +275,9 @@ __device__ __forceinline__ void release_range(const ReleaseParams &p, int s, int
 // and moves the blocks.  More rows are two launches over the whole GPU: one
 // counts into the workspace, the other sums the counts of the rows before its
 // own (each CTA reads them all, out of L2) and moves.  4,000 rows of up to
-// 2,048 blocks take # us so, and 45 us in one cluster of 16 CTAs of 1,024
-// threads; 256 rows of up to 512 take # us in one launch and # us in two, which
-// cost the host another 7 us.
+// 2,048 blocks take 13 us so, and 49 us in one cluster of 16 CTAs of 1,024
+// threads; 256 rows of up to 512 take 5.8 us in one launch and 5.2 us in two,
+// which cost the host another 7 us (a launch, and the workspace).
 constexpr int kRelThreads = 256;
 constexpr int kRelLoads = 8;
 constexpr int kRelSmallWarps = 16;

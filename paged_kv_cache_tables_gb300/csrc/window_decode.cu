@@ -4,9 +4,10 @@
 // Mathematics.  The query of sequence s sits at position p = ctx_s - 1 and
 // sees position t iff t <= p and (t > p - window or t < sinks):
 //     out = sum_t softmax_t(scale * q . K_t) V_t  over those t,
-// taken block by block with the running maximum m and sum l of the softmax in
-// fp32: a block's scores x give m' = max(m, x), weights 2^(x - m'), and l and
-// the accumulator are scaled by 2^(m - m').  Parts of a range combine the same
+// taken a few blocks at a time with the running maximum m and sum l of the
+// softmax in fp32: their scores x give m' = max(m, x), weights 2^(x - m'), and
+// l and the accumulator are scaled by 2^(m - m') (m is left alone until it
+// grows by more than 2^8).  Parts of a range combine the same
 // way: with M = max m_i, out = sum acc_i 2^(m_i - M) / sum l_i 2^(m_i - M).
 //
 // What is read.  Only blocks that hold a visible position: the blocks of the
@@ -24,6 +25,16 @@
 // parts meet in shared memory, the CTAs' parts through distributed shared
 // memory, so there is no workspace, no second launch, and the order of every
 // sum is fixed by the lengths alone.
+//
+// What bounds it: HBM.  256 sequences x 8 KV heads, window 1,024 (597 MB of
+// visible K and V): 90.6 us, 97 % of the measured copy rate; 16 x 8, window
+// 8,000: 78.7 us, 98 %; 7 x 8 of it 37.4 us, 91 % (5 CTAs a range fill 280 of
+// 304 places).  Small calls are a chain of latencies (launch, length, table
+// entry, tile, products, cluster): 3 to 5 us.  Measured and left: persistent
+// CTAs of 8 warps that stream from range to range, ranges taken by cluster
+// launch control: 122 us for the 256 sequences, since what a CTA holds ahead it
+// holds back from idle SMs at the end, and what it does not hold ahead it waits
+// for.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -505,6 +516,9 @@ static int window_decode(const WindowDecodeParams &prm, const CUtensorMap &tk, c
     // us in 512; 4 x 8 x 257 14.2 us in 256 and 24.3 us in 512.
     int ranks = (int)std::min<int64_t>({kWinMaxCluster, 2 * sms / ranges, blocks / (2 * kWinWarps)});
     if (ranks > 8 && ranks < kWinMaxCluster) ranks = 8;
+    // a call of few CTAs is bound by a warp's chain of latencies: one block a
+    // warp, up to a CTA per SM (8 ranges of 17 blocks: 5.6 -> 4.2 us)
+    ranks = std::max(ranks, (int)std::min<int64_t>({8, sms / ranges, blocks / kWinWarps}));
     if (ranks < 1) ranks = 1;
     const int grid = (int)(ranges * ranks);
     if (prm.G > 8) return launch_window_decode<T, D, 2, false>(prm, tk, tv, grid, ranks, stream);

@@ -36,7 +36,19 @@
 // P is rounded to 16 bits once when the output is 16 bits wide, an error of the
 // output's own kind: half a step of each weight (2^-8 sum p|v| for bf16, 2^-11
 // for fp16).  A 32-bit output gets a second product with the rounding residual.
-// PERF
+// Three chunks of 3,500 to 4,100 rows x 32 heads, window 4,096, head_dim 128: 510
+// us, 1,450 TFLOP/s of the rows' own products (76 % of the measured cuBLAS burst);
+// 8 chunks of 512, window 1,024: 72 us.  The causal kernel's design with a window
+// took 764 and 122 us: residual products 1.25x, pages loaded as two boxes of 2 KB
+// (1.45 us for 64 KB an SM, these 0.92), V cleared by the softmax warps, the first
+// tokens' pages a tile of their own, one unit a CTA.
+// What bounds it now is the chain S -> softmax -> P V -> S of a tile, 1.4 us a key
+// tile with the other tile's chain beside it: loads alone take 0.9 us, products
+// alone 1.2 us.  Measured and left: 64-key tiles with two score buffers each (S
+// then runs ahead, but an N = 64 product costs as much as N = 128, since reading
+// Q out of shared memory bounds both: 633 us); two warpgroups a tile (677 us); a
+// polynomial for every eighth exp2 (550 us); four parts of P instead of two
+// (616 us).
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -686,8 +698,8 @@ extern "C" int pkv_paged_window_prefill_attention(void *out, const void *q, cons
     if (rc != PKV_OK) return rc;
     const int rtok = kWpRows / G;
     // query tiles of a unit: two, which share every K and V tile; or one, when
-    // all units then run at once: a step of 128 keys takes # us with two tiles on
-    // an SM and # us with one (512 rows behind 4,096, window 1,024: 24.1 and 17.2
+    // all units then run at once: a step of 128 keys takes 1.40 us with two tiles on
+    // an SM and 0.95 us with one (512 rows behind 4,096, window 1,024: 24.1 and 17.2
     // us; three chunks of 3,500-4,100, which fill the GPU either way, 509 and 789).
     // A 32-bit output always takes two.
     auto units_of = [&](int tiles) { return ((int64_t)max_q_len + tiles * rtok - 1) / (tiles * rtok); };

@@ -148,8 +148,8 @@ def test_in_place_on_slices_of_fused_rows(cuda_lib):
                                                          (333, 20, 4, 128, 64, True, True), (1500, 8, 1, 128, 128, False, True)])
 def test_append(cuda_lib, T, Hq, Hkv, d, rot, inter, normed, dtype):
     g = torch.Generator().manual_seed(T)
-    fused = torch.randn(T, (Hq + 2 * Hkv) * d, generator=g).to(dtype).cuda()
-    q, k, v = (x.view(T, -1, d) for x in fused.split([Hq * d, Hkv * d, Hkv * d], dim=1))
+    fused = torch.randn(T, (Hq + 2 * Hkv) * d + 64, generator=g).to(dtype).cuda()
+    q, k, v = (x.view(T, -1, d) for x in fused.split([Hq * d, Hkv * d, Hkv * d, 64], dim=1)[:3])
     pos = torch.randint(0, 1 << 20, (T,), generator=g, dtype=torch.int32).cuda()
     NB = T // 16 + 3
     slots = torch.randperm(NB * 16, generator=g)[:T]
