@@ -48,7 +48,7 @@
 // then runs ahead, but an N = 64 product costs as much as N = 128, since reading
 // Q out of shared memory bounds both: 633 us); two warpgroups a tile (677 us); a
 // polynomial for every eighth exp2 (550 us); four parts of P instead of two
-// (616 us).
+// (616 us); P by the maximum so far, the tile's own taken beside it (565 us).
 #include <cuda_runtime.h>
 
 #include <cmath>
