@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kWpThreads, 1)
             mbar_init(&bars->k_full[s], 1);
             mbar_init(&bars->v_full[s], 1);
             mbar_init(&bars->k_empty[s], TILES);
-            mbar_init(&bars->v_empty[s], TILES);
+            mbar_init(&bars->v_empty[s], TILES + 1);   // and the cleaner, which must not fall a phase behind
             mbar_init(&bars->v_clean[s], 1);
         }
         *gave_up = 0;
@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(kWpThreads, 1)
                                                             h * p.G, u.row0 + t * p.rtok, &bars->q_full);
                                 }
                             }
-                            // a V slot is free once both P V products of its last tile are done
+                            // a V slot is free once both P V products of its last tile (and its cleaning) are done
                             if (ok && g >= kWpStages) ok = wait(&bars->v_empty[st], g / kWpStages - 1);
                             if (ok) {
                                 mbar_arrive_expect_tx(&bars->v_full[st], Sh::TILE);
@@ -470,7 +470,10 @@ __global__ void __launch_bounds__(kWpThreads, 1)
                         fence_proxy_async_smem();
                     }
                     __syncwarp();
-                    if (lane == 0) tc::mbar_arrive_cta(&bars->v_clean[st]);
+                    if (lane == 0) {
+                        tc::mbar_arrive_cta(&bars->v_clean[st]);
+                        tc::mbar_arrive_cta(&bars->v_empty[st]);
+                    }
                 }
             }
         }
