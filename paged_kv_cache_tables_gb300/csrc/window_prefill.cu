@@ -29,26 +29,30 @@
 //   3      clears V rows that no row of the unit sees, in pages read for their
 //          neighbours (they may hold anything, and 0 x NaN must not reach O)
 //   4-11   softmax: a warpgroup a query tile, a row per thread
-// While one tile's softmax runs, the tensor cores work on the other's products.
+// While one tile's softmax runs, the tensor cores work on the other's products:
+// the two issuers take turns, P V of a key tile and S of the next one turn.  Left
+// to themselves the tiles fall into step, both softmaxes at once and then both
+// products: 3,500 to 3,750 cycles a key tile for the two, in turns 2,650 to 2,900.
 // Loads, products and softmax run across the units: while a unit's outputs are
 // stored, the next one's Q, K and V arrive.
 //
 // P is rounded to 16 bits once when the output is 16 bits wide, an error of the
 // output's own kind: half a step of each weight (2^-8 sum p|v| for bf16, 2^-11
 // for fp16).  A 32-bit output gets a second product with the rounding residual.
-// Three chunks of 3,500 to 4,100 rows x 32 heads, window 4,096, head_dim 128: 510
-// us, 1,450 TFLOP/s of the rows' own products (76 % of the measured cuBLAS burst);
-// 8 chunks of 512, window 1,024: 72 us.  The causal kernel's design with a window
+// Three chunks of 3,500 to 4,100 rows x 32 heads, window 4,096, head_dim 128: 457
+// us, 1,620 TFLOP/s of the rows' own products (85 % of the measured cuBLAS burst;
+// without turns 509 us); 8 chunks of 512, window 1,024: 64 us (72).  The causal kernel's design with a window
 // took 764 and 122 us: residual products 1.25x, pages loaded as two boxes of 2 KB
 // (1.45 us for 64 KB an SM, these 0.92), V cleared by the softmax warps, the first
 // tokens' pages a tile of their own, one unit a CTA.
-// What bounds it now is the chain S -> softmax -> P V -> S of a tile, 1.4 us a key
-// tile with the other tile's chain beside it: loads alone take 0.9 us, products
-// alone 1.2 us.  Measured and left: 64-key tiles with two score buffers each (S
-// then runs ahead, but an N = 64 product costs as much as N = 128, since reading
-// Q out of shared memory bounds both: 633 us); two warpgroups a tile (677 us); a
-// polynomial for every eighth exp2 (550 us); four parts of P instead of two
-// (616 us); P by the maximum so far, the tile's own taken beside it (565 us).
+// What bounds it now: the tensor cores' turns, 1.35 us a key tile of both query
+// tiles (products alone 1.2 us, loads alone 0.9), and between units the wait for
+// the next Q.  Measured and left, each before the tiles took turns (then 509 to
+// 515 us): 64-key tiles with two score buffers each (S then runs ahead, but an
+// N = 64 product costs as much as N = 128, since reading Q out of shared memory
+// bounds both: 633 us); two warpgroups a tile (677 us); a polynomial for every
+// eighth exp2 (550 us); four parts of P instead of two (616 us); P by the maximum
+// so far, the tile's own taken beside it (565 us).
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -122,6 +126,7 @@ struct WpBars {
     uint64_t k_full[kWpStages], v_full[kWpStages], k_empty[kWpStages], v_empty[kWpStages];
     uint64_t v_clean[kWpStages];
     uint64_t s_full[2], p_full[2][2], o_done[2];   // per query tile (and part of its keys)
+    uint64_t turn[2];                              // a query tile's turn at the tensor cores
 };
 
 // A K or V tile is its pages one after another; a page holds, for each group of
@@ -135,10 +140,10 @@ struct WpShape {
     static constexpr int PAGE = 2 * GROUP;
     static constexpr int TILE = kWpPages * PAGE;
     static constexpr int STAGE_BYTES = 2 * TILE;            // K then V
-    // 32-key groups of P after which the first part of P V starts.  Three
-    // chunks of 3,500-4,100 rows, window 4,096: 614 us after one group, 571
-    // after two, 515 after three, 677 after all four (head_dim 128); 440, 414,
-    // 431 and 504 us (head_dim 64).
+    // 32-key groups of P after which the first part of P V may start.  Three
+    // chunks of 3,500-4,100 rows, window 4,096: 459 us after two groups, 453
+    // after three (head_dim 128); 379, 367 and 382 us after one, two and three
+    // (head_dim 64).
     static constexpr int FIRST_PART = D == 128 ? 3 : 2;
     static constexpr int OFF_Q = 0;                         // tile A, then tile B
     static constexpr int OFF_KV = 2 * Q_BYTES;
@@ -180,6 +185,7 @@ __global__ void __launch_bounds__(kWpThreads, 1)
             mbar_init(&bars->p_full[i][0], 4);
             mbar_init(&bars->p_full[i][1], 4);
             mbar_init(&bars->o_done[i], 1);
+            mbar_init(&bars->turn[i], 1);
         }
         mbar_init(&bars->cancel, 1);
         mbar_init(&bars->q_full, 1);
@@ -385,7 +391,12 @@ __global__ void __launch_bounds__(kWpThreads, 1)
             const uint64_t k_desc = tc::smem_desc_sw128(sbase + Sh::OFF_KV, 16, Sh::GROUP);
             const uint64_t v_desc = tc::smem_desc_sw128(sbase + Sh::OFF_KV + Sh::TILE, 1024, Sh::GROUP);
             uint32_t g = 0;     // key tiles done
-            auto issue_s = [&](uint32_t k, bool last) {   // S = Q K^T of key tile k, the unit's last?
+            // The two tiles take turns: P V of a key tile and S of the next are
+            // one turn, so that a tile's softmax runs beside the other's turn.
+            auto pass_turn = [&]() {
+                if (TILES == 2 && lane == 0) tc::mbar_arrive_cta(&bars->turn[1 - t]);
+            };
+            auto issue_s = [&](uint32_t k, bool last, bool pass) {   // S = Q K^T of key tile k, the unit's last?
                 if (!wait_all(&bars->k_full[k % kWpStages], k / kWpStages)) return false;
                 tc::fence_after_sync();
                 const uint64_t kb = k_desc + (uint64_t)(((k % kWpStages) * Sh::STAGE_BYTES) >> 4);
@@ -393,6 +404,7 @@ __global__ void __launch_bounds__(kWpThreads, 1)
                 for (int kk = 0; kk < D / 16; ++kk) {
                     const uint32_t qo = ((kk >> 2) * Sh::Q_HALF + (kk & 3) * 32) >> 4;
                     const uint32_t ko = ((kk >> 2) * 1024 + (kk & 3) * 32) >> 4;
+                    if (pass && kk == D / 16 - 2) pass_turn();   // on its way while the rest is issued
                     if (leader) tc::mma_f16_ss(d_s, q_desc + qo, kb + ko, idesc_s, kk > 0);
                 }
                 if (leader) {
@@ -411,11 +423,12 @@ __global__ void __launch_bounds__(kWpThreads, 1)
                 if (lane == 0) tc::mbar_arrive_cta(&bars->unit_empty[n & 1]);
                 if (tiles == 0) break;
                 // (S may be written: the product that read P over it was issued before)
-                ok = wait_all(&bars->q_full, (uint32_t)n) && issue_s(g, tiles == 1);
+                ok = wait_all(&bars->q_full, (uint32_t)n) && issue_s(g, tiles == 1, false);
                 for (int j = 0; ok && j < tiles; ++j, ++g) {
                     const uint64_t vb = v_desc + (uint64_t)(((g % kWpStages) * Sh::STAGE_BYTES) >> 4);
                     const bool dirty = WpHidden(u, j * kWpKeys, p.sinks, kWpKeys).any();
                     ok = wait_all(dirty ? &bars->v_clean[g % kWpStages] : &bars->v_full[g % kWpStages], g / kWpStages);
+                    if (TILES == 2 && (t == 1 || g > 0)) ok = ok && wait_all(&bars->turn[t], t == 1 ? g : g - 1);
 #pragma unroll
                     for (int part = 0; part < 2; ++part) {
                         // P of a unit's first tile is there only after the unit before's O was read
@@ -438,7 +451,10 @@ __global__ void __launch_bounds__(kWpThreads, 1)
                         tc::mma_commit(&bars->v_empty[g % kWpStages]);
                         if (j + 1 == tiles) tc::mma_commit(&bars->o_done[t]);
                     }
-                    if (j + 1 < tiles) ok = issue_s(g + 1, j + 2 == tiles);
+                    if (j + 1 < tiles)
+                        ok = issue_s(g + 1, j + 2 == tiles, true);
+                    else
+                        pass_turn();
                 }
                 if (!ok) break;
             }
