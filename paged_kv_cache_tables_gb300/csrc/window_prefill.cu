@@ -39,20 +39,22 @@
 // P is rounded to 16 bits once when the output is 16 bits wide, an error of the
 // output's own kind: half a step of each weight (2^-8 sum p|v| for bf16, 2^-11
 // for fp16).  A 32-bit output gets a second product with the rounding residual.
-// Three chunks of 3,500 to 4,100 rows x 32 heads, window 4,096, head_dim 128: 457
-// us, 1,620 TFLOP/s of the rows' own products (85 % of the measured cuBLAS burst;
-// without turns 509 us); 8 chunks of 512, window 1,024: 64 us (72).  The causal kernel's design with a window
-// took 764 and 122 us: residual products 1.25x, pages loaded as two boxes of 2 KB
-// (1.45 us for 64 KB an SM, these 0.92), V cleared by the softmax warps, the first
-// tokens' pages a tile of their own, one unit a CTA.
+// Three chunks of 3,500 to 4,100 rows x 32 heads, window 4,096, head_dim 128: 441
+// us, 1,680 TFLOP/s of the rows' own products (88 % of the measured cuBLAS burst;
+// without turns 509 us); 8 chunks of 512, window 1,024: 61 us (72).  The causal
+// kernel's design with a window took 764 and 122 us: residual products 1.25x, pages
+// loaded as two boxes of 2 KB (1.45 us for 64 KB an SM, these 0.92), V cleared by
+// the softmax warps, the first tokens' pages a tile of their own, one unit a CTA.
 // What bounds it now: the tensor cores' turns, 1.35 us a key tile of both query
-// tiles (products alone 1.2 us, loads alone 0.9), and between units the wait for
-// the next Q.  Measured and left, each before the tiles took turns (then 509 to
-// 515 us): 64-key tiles with two score buffers each (S then runs ahead, but an
-// N = 64 product costs as much as N = 128, since reading Q out of shared memory
-// bounds both: 633 us); two warpgroups a tile (677 us); a polynomial for every
-// eighth exp2 (550 us); four parts of P instead of two (616 us); P by the maximum
-// so far, the tile's own taken beside it (565 us).
+// tiles (products alone 1.2 us, loads alone 0.9), and at a unit's end its outputs,
+// 1.7 us where all SMs store at once.  Measured and left: the next unit worked out
+// and its Q loaded while the last tile runs (464 us and, 8 x 2,048 rows, 193 us
+// instead of 457 and 178), units halved for the last round of CTAs (487 us).
+// Before the tiles took turns (then 509 to 515 us): 64-key tiles with two score
+// buffers each (S then runs ahead, but an N = 64 product costs as much as N = 128,
+// since reading Q out of shared memory bounds both: 633 us); two warpgroups a tile
+// (677 us); a polynomial for every eighth exp2 (550 us); four parts of P instead of
+// two (616 us); P by the maximum so far, the tile's own taken beside it (565 us).
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -141,13 +143,13 @@ struct WpShape {
     static constexpr int TILE = kWpPages * PAGE;
     static constexpr int STAGE_BYTES = 2 * TILE;            // K then V
     // 32-key groups of P after which the first part of P V may start.  Three
-    // chunks of 3,500-4,100 rows, window 4,096: 459 us after two groups, 453
-    // after three (head_dim 128); 379, 367 and 382 us after one, two and three
-    // (head_dim 64).
-    static constexpr int FIRST_PART = D == 128 ? 3 : 2;
+    // chunks of 3,500-4,100 rows, window 4,096, after one, two and three groups:
+    // 382, 371 and 380 us with head_dim 64; 441 and 449 after two and three with 128.
+    static constexpr int FIRST_PART = 2;
     static constexpr int OFF_Q = 0;                         // tile A, then tile B
     static constexpr int OFF_KV = 2 * Q_BYTES;
-    static constexpr int OFF_UNIT = OFF_KV + kWpStages * STAGE_BYTES;
+    static constexpr int OFF_OUT = OFF_KV + kWpStages * STAGE_BYTES;   // outputs on their way out: 128 bytes of 32 rows a warp
+    static constexpr int OFF_UNIT = OFF_OUT + 8 * 4096;
     static constexpr int OFF_CANCEL = OFF_UNIT + 2 * (int)sizeof(WpUnit);
     static constexpr int OFF_BAR = OFF_CANCEL + 16;
     static constexpr int SMEM_BYTES = 1024 + OFF_BAR + (int)sizeof(WpBars) + 16;
@@ -602,28 +604,42 @@ __global__ void __launch_bounds__(kWpThreads, 1)
             if (!ok) break;
             tc::fence_after_sync();
             const float inv = 1.f / l;
-            const int64_t ob = ((int64_t)(u.row0 + tok) * p.Hq + (int64_t)u.h * p.G + head) * D;
+            // 128 bytes of each row at a time: a thread has a row of O, but stores
+            // want a row's bytes side by side, so they change hands in shared memory
+            // (16-byte chunks, swizzled).  Straight from the rows, 32 lines an
+            // instruction, 3 x 4000 rows take 457 us instead of 447.
+            constexpr int kCols = RESIDUAL ? 32 : 64;      // a 32-bit output or a 16-bit one
+            constexpr int kSize = RESIDUAL ? 4 : 2;
+            const int64_t at = valid ? ((int64_t)(u.row0 + tok) * p.Hq + (int64_t)u.h * p.G + head) * D * kSize : -1;
+            uint8_t *stage = sm + Sh::OFF_OUT + (warp - 4) * 4096;
 #pragma unroll 1
-            for (int cc = 0; cc < D; cc += 32) {
-                float v[32];
-                tc::tmem_ld32(ocol + cc, v);
+            for (int cc = 0; cc < D; cc += kCols) {
+                float v[kCols];
+#pragma unroll
+                for (int e = 0; e < kCols; e += 32) tc::tmem_ld32(ocol + cc + e, *reinterpret_cast<float(*)[32]>(v + e));
                 tc::tmem_wait_ld();
-                if (valid) {
-                    if constexpr (RESIDUAL) {   // a 32-bit output
-                        float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(p.out) + ob + cc);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            dst[e] = make_float4(v[4 * e] * inv, v[4 * e + 1] * inv, v[4 * e + 2] * inv, v[4 * e + 3] * inv);
-                    } else {
-                        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<T *>(p.out) + ob + cc);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            dst[e] = make_uint4(pack2<T>(v[8 * e] * inv, v[8 * e + 1] * inv),
-                                                pack2<T>(v[8 * e + 2] * inv, v[8 * e + 3] * inv),
-                                                pack2<T>(v[8 * e + 4] * inv, v[8 * e + 5] * inv),
-                                                pack2<T>(v[8 * e + 6] * inv, v[8 * e + 7] * inv));
-                    }
+                for (int e = 0; e < 8; ++e) {
+                    uint4 w;
+                    if constexpr (RESIDUAL)
+                        w = make_uint4(__float_as_uint(v[4 * e] * inv), __float_as_uint(v[4 * e + 1] * inv),
+                                       __float_as_uint(v[4 * e + 2] * inv), __float_as_uint(v[4 * e + 3] * inv));
+                    else
+                        w = make_uint4(pack2<T>(v[8 * e] * inv, v[8 * e + 1] * inv),
+                                       pack2<T>(v[8 * e + 2] * inv, v[8 * e + 3] * inv),
+                                       pack2<T>(v[8 * e + 4] * inv, v[8 * e + 5] * inv),
+                                       pack2<T>(v[8 * e + 6] * inv, v[8 * e + 7] * inv));
+                    *reinterpret_cast<uint4 *>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) = w;
                 }
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int row = 4 * i + (lane >> 3);
+                    const uint4 w = *reinterpret_cast<const uint4 *>(stage + row * 128 + (((lane ^ row) & 7) << 4));
+                    const int64_t to = __shfl_sync(0xffffffffu, at, row);
+                    if (to >= 0) *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.out) + to + cc * kSize + (lane & 7) * 16) = w;
+                }
+                __syncwarp();
             }
             // O has been read: ordered before this unit's successor's P, whose
             // arrival lets the tensor core write O again
@@ -717,10 +733,10 @@ extern "C" int pkv_paged_window_prefill_attention(void *out, const void *q, cons
     if (rc != PKV_OK) return rc;
     const int rtok = kWpRows / G;
     // query tiles of a unit: two, which share every K and V tile; or one, when
-    // all units then run at once: a step of 128 keys takes 1.40 us with two tiles on
-    // an SM and 0.95 us with one (512 rows behind 4,096, window 1,024: 24.1 and 17.2
-    // us; three chunks of 3,500-4,100, which fill the GPU either way, 509 and 789).
-    // A 32-bit output always takes two.
+    // all units then run at once: a step of 128 keys takes 1.33 us with two tiles on
+    // an SM and 0.95 us with one (two / one, us: 512 rows behind 4,096, window
+    // 1,024: 18.8 / 17.2; 16 rows: 7.1 / 6.1; three chunks of 3,500-4,100 rows, which
+    // fill the GPU either way: 449 / 776).  A 32-bit output always takes two.
     auto units_of = [&](int tiles) { return ((int64_t)max_q_len + tiles * rtok - 1) / (tiles * rtok); };
     const bool one = out_dtype != PKV_DTYPE_F32 && num_seqs * units_of(1) * num_kv_heads <= sms;
     const int qtiles = one ? 1 : 2;
