@@ -39,17 +39,19 @@
 // P is rounded to 16 bits once when the output is 16 bits wide, an error of the
 // output's own kind: half a step of each weight (2^-8 sum p|v| for bf16, 2^-11
 // for fp16).  A 32-bit output gets a second product with the rounding residual.
-// Three chunks of 3,500 to 4,100 rows x 32 heads, window 4,096, head_dim 128: 441
-// us, 1,680 TFLOP/s of the rows' own products (88 % of the measured cuBLAS burst;
-// without turns 509 us); 8 chunks of 512, window 1,024: 61 us (72).  The causal
+// Three chunks of 3,500 to 4,100 rows x 32 heads, window 4,096, head_dim 128: 445
+// us, 1,665 TFLOP/s of the rows' own products (87 % of the measured cuBLAS burst;
+// without turns 509 us); 8 chunks of 512, window 1,024: 60 us (72).  The causal
 // kernel's design with a window took 764 and 122 us: residual products 1.25x, pages
 // loaded as two boxes of 2 KB (1.45 us for 64 KB an SM, these 0.92), V cleared by
 // the softmax warps, the first tokens' pages a tile of their own, one unit a CTA.
 // What bounds it now: the tensor cores' turns, 1.35 us a key tile of both query
-// tiles (products alone 1.2 us, loads alone 0.9), and at a unit's end its outputs,
-// 1.7 us where all SMs store at once.  Measured and left: the next unit worked out
-// and its Q loaded while the last tile runs (464 us and, 8 x 2,048 rows, 193 us
-// instead of 457 and 178), units halved for the last round of CTAs (487 us).
+// tiles (products alone 1.2 us, loads alone 0.9), the masks of a unit's first and
+// last key tiles, 0.5 us each, and at a unit's end its outputs and the wait for the
+// next Q, 1.3 us each.  Measured and left: the next unit worked out while the last
+// tile runs (head_dim 64: 368 -> 395 us, 3 x 4000: 445 -> 442) and its Q loaded to
+// a third slot (3 x 4000: 457 -> 464, 8 x 2,048: 178 -> 193, before outputs were
+// staged), units halved for the last round of CTAs (453 -> 487 us).
 // Before the tiles took turns (then 509 to 515 us): 64-key tiles with two score
 // buffers each (S then runs ahead, but an N = 64 product costs as much as N = 128,
 // since reading Q out of shared memory bounds both: 633 us); two warpgroups a tile
@@ -96,6 +98,7 @@ struct WindowPrefillParams {
     int window, sinks, total_q;
     float scale_log2;
     int out_dtype;
+    bool boxes;   // a warp's 32 rows are whole tokens: tout has a box for them
 };
 
 // One unit of work, as the scheduler publishes it (tiles == 0: no more).
@@ -165,11 +168,27 @@ __device__ __forceinline__ void load_page(void *dst, const CUtensorMap *map, int
         : "memory");
 }
 
+// 128 bytes of a warp's rows from shared memory to the output, asynchronously.
+__device__ __forceinline__ void store_rows(const CUtensorMap *map, const void *src, int column, int head, int token) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(column), "r"(head), "r"(token), "r"(smem_addr(src))
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
+// Until what this thread's stores read may be overwritten.
+__device__ __forceinline__ void stores_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+
+// Until this thread's stores are complete.
+__device__ __forceinline__ void stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
 // TILES: query tiles of a unit, 2, or 1 (A alone)
 template <typename T, int D, bool RESIDUAL, int TILES>
 __global__ void __launch_bounds__(kWpThreads, 1)
     window_prefill_kernel(const WindowPrefillParams p, const __grid_constant__ CUtensorMap tk,
-                          const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tq) {
+                          const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tq,
+                          const __grid_constant__ CUtensorMap tout) {
     using Sh = WpShape<D>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -606,18 +625,24 @@ __global__ void __launch_bounds__(kWpThreads, 1)
             const float inv = 1.f / l;
             // 128 bytes of each row at a time: a thread has a row of O, but stores
             // want a row's bytes side by side, so they change hands in shared memory
-            // (16-byte chunks, swizzled).  Straight from the rows, 32 lines an
-            // instruction, 3 x 4000 rows take 457 us instead of 447.
+            // (16-byte chunks, swizzled as TMA swizzles).  Straight from the rows, 32
+            // lines an instruction, 8 x 2,048 rows take 178 us instead of 169.  Where
+            // the warp's 32 rows are whole tokens TMA stores them, beside the next
+            // 128 bytes or the next unit: 162 us instead of 165 (8 x 1,000-1,500 rows
+            // of 8 heads, window 128: 21.9 and 22.8; 3 x 4000: 445 and 440).
             constexpr int kCols = RESIDUAL ? 32 : 64;      // a 32-bit output or a 16-bit one
             constexpr int kSize = RESIDUAL ? 4 : 2;
             const int64_t at = valid ? ((int64_t)(u.row0 + tok) * p.Hq + (int64_t)u.h * p.G + head) * D * kSize : -1;
             uint8_t *stage = sm + Sh::OFF_OUT + (warp - 4) * 4096;
+            const bool box = !RESIDUAL && p.boxes && __all_sync(0xffffffffu, valid);
 #pragma unroll 1
             for (int cc = 0; cc < D; cc += kCols) {
                 float v[kCols];
 #pragma unroll
                 for (int e = 0; e < kCols; e += 32) tc::tmem_ld32(ocol + cc + e, *reinterpret_cast<float(*)[32]>(v + e));
                 tc::tmem_wait_ld();
+                if (lane == 0) stores_read();
+                __syncwarp();
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     uint4 w;
@@ -630,6 +655,12 @@ __global__ void __launch_bounds__(kWpThreads, 1)
                                        pack2<T>(v[8 * e + 4] * inv, v[8 * e + 5] * inv),
                                        pack2<T>(v[8 * e + 6] * inv, v[8 * e + 7] * inv));
                     *reinterpret_cast<uint4 *>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) = w;
+                }
+                if (box) {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) store_rows(&tout, stage, cc, u.h * p.G, u.row0 + tok);
+                    continue;
                 }
                 __syncwarp();
 #pragma unroll
@@ -645,6 +676,7 @@ __global__ void __launch_bounds__(kWpThreads, 1)
             // arrival lets the tensor core write O again
             tc::fence_before_sync();
         }
+        if (lane == 0) stores_done();
     }
 
     tc::fence_before_sync();
@@ -668,7 +700,7 @@ static int encode_page_map(CUtensorMap *map, const void *base, int num_blocks, i
 
 template <typename T, int D, bool RESIDUAL, int TILES>
 static int launch_window_prefill(const WindowPrefillParams &prm, const CUtensorMap &tk, const CUtensorMap &tv,
-                                 const CUtensorMap &tq, int grid, cudaStream_t stream) {
+                                 const CUtensorMap &tq, const CUtensorMap &tout, int grid, cudaStream_t stream) {
     using Sh = WpShape<D>;
     // the register split inside the kernel waits for registers that only exist
     // if the compiled count is the one it was sized for: check it (once; the
@@ -695,7 +727,7 @@ static int launch_window_prefill(const WindowPrefillParams &prm, const CUtensorM
         mark_done_on_device(&attr_set);
     }
     cudaError_t e = launch_pdl(window_prefill_kernel<T, D, RESIDUAL, TILES>, dim3(grid), dim3(kWpThreads), Sh::SMEM_BYTES, stream,
-                               prm, tk, tv, tq);
+                               prm, tk, tv, tq, tout);
     if (e == cudaSuccess) e = cudaGetLastError();
     return e == cudaSuccess ? PKV_OK : cuda_fail(e);
 }
@@ -755,6 +787,13 @@ extern "C" int pkv_paged_window_prefill_attention(void *out, const void *q, cons
     rc = encode_tiled_map(&tq, q, 3, dims, strides, box);
     if (rc != PKV_OK) return rc;
     WindowPrefillParams prm;
+    prm.boxes = out_dtype == dtype && 32 % G == 0;
+    CUtensorMap tout = tq;
+    if (prm.boxes) {
+        const uint32_t rows[3] = {64, (uint32_t)G, 32u / (uint32_t)G};
+        rc = encode_tiled_map(&tout, out, 3, dims, strides, rows);
+        if (rc != PKV_OK) return rc;
+    }
     prm.out = out;
     prm.cu_seqlens = cu_seqlens;
     prm.block_tables = block_tables;
@@ -779,8 +818,8 @@ extern "C" int pkv_paged_window_prefill_attention(void *out, const void *q, cons
         using T = decltype(type);
         constexpr bool R = decltype(residual)::value;
         constexpr int N = decltype(tiles)::value;
-        return head_dim == 128 ? launch_window_prefill<T, 128, R, N>(prm, tk, tv, tq, (int)grid, st)
-                               : launch_window_prefill<T, 64, R, N>(prm, tk, tv, tq, (int)grid, st);
+        return head_dim == 128 ? launch_window_prefill<T, 128, R, N>(prm, tk, tv, tq, tout, (int)grid, st)
+                               : launch_window_prefill<T, 64, R, N>(prm, tk, tv, tq, tout, (int)grid, st);
     };
     using Yes = std::true_type;
     using No = std::false_type;
