@@ -12,8 +12,8 @@
 //
 // What bounds it: latency.  The step of 4,020 sequences and 127,780 rows
 // writes 1.6 MB, 0.24 us at the measured copy rate; the launch, the reads of
-// the lengths, the scan and the reads of ids are a chain of round trips, 3.5 us
-// for 256 sequences and 9.4 us for those 4,020 (in 8 CTAs 11.6 us).
+// the lengths, the scan and the reads of ids are a chain of round trips, 2.9 us
+// for 256 sequences and 8.2 us for those 4,020.
 // So everything is one launch without a workspace: a small step is one CTA;
 // a larger one is one cluster of CTAs, each of which scans all lengths itself
 // (at most 16,384 of them, out of L2) and fills its share of the outputs, its
@@ -47,40 +47,35 @@ struct TablesParams {
     bool vec;   // slot_mapping and token_pos are 16-byte aligned
 };
 
-// Inclusive scan over the CTA of a pair of 64-bit values.
 struct Pair64 {
     int64_t a, b;
 };
 
-__device__ __forceinline__ Pair64 cta_scan(Pair64 v, Pair64 *sh, Pair64 *total) {
+// A pair of sums that stay at 2^32 - 1 once they get there (adding so is
+// associative): more than any count that is allowed.
+struct PairSat {
+    uint32_t a, b;
+};
+
+__device__ __forceinline__ uint32_t add_sat(uint32_t x, uint32_t y) { return x + y < x ? 0xffffffffu : x + y; }
+
+// Inclusive scan over the CTA.
+__device__ __forceinline__ PairSat cta_scan(PairSat v, PairSat *sh, PairSat *total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const int64_t a = __shfl_up_sync(0xffffffffu, v.a, off), b = __shfl_up_sync(0xffffffffu, v.b, off);
-        if (lane >= off) {
-            v.a += a;
-            v.b += b;
-        }
-    }
-    if (lane == 31) sh[warp] = v;
-    __syncthreads();
-    if (warp == 0) {
-        Pair64 w = lane < warps ? sh[lane] : Pair64{0, 0};
+    auto scan = [&](PairSat x) {
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
-            const int64_t a = __shfl_up_sync(0xffffffffu, w.a, off), b = __shfl_up_sync(0xffffffffu, w.b, off);
-            if (lane >= off) {
-                w.a += a;
-                w.b += b;
-            }
+            const uint32_t a = __shfl_up_sync(0xffffffffu, x.a, off), b = __shfl_up_sync(0xffffffffu, x.b, off);
+            if (lane >= off) x = {add_sat(x.a, a), add_sat(x.b, b)};
         }
-        sh[lane] = w;
-    }
+        return x;
+    };
+    v = scan(v);
+    if (lane == 31) sh[warp] = v;
     __syncthreads();
-    if (warp > 0) {
-        v.a += sh[warp - 1].a;
-        v.b += sh[warp - 1].b;
-    }
+    if (warp == 0) sh[lane] = scan(lane < warps ? sh[lane] : PairSat{0, 0});
+    __syncthreads();
+    if (warp > 0) v = {add_sat(v.a, sh[warp - 1].a), add_sat(v.b, sh[warp - 1].b)};
     *total = sh[31];
     return v;
 }
@@ -99,9 +94,12 @@ __device__ __forceinline__ int last_at_most(const int *prefix, int n, int x) {
     return lo;
 }
 
+// Blocks that n tokens behind l take.
+__device__ __forceinline__ uint32_t blocks_needed(uint32_t l, uint32_t n) { return ((l + n + 15) >> 4) - ((l + 15) >> 4); }
+
 __global__ void __launch_bounds__(kTabThreads, 1) step_tables_kernel(const TablesParams p) {
     extern __shared__ int tab_smem[];
-    __shared__ Pair64 sh_scan[32];
+    __shared__ PairSat sh_scan[32];
     __shared__ int sh_bad;
     const int S = p.S;
     int *cu = tab_smem;          // [S + 1] tokens before each sequence
@@ -121,7 +119,7 @@ __global__ void __launch_bounds__(kTabThreads, 1) step_tables_kernel(const Table
     const int64_t limit = (int64_t)p.max_blocks * 16;
     const int count = p.free_count[0];
     int bad = 0;
-    Pair64 sum{0, 0};
+    PairSat sum{0, 0};
     for (int s0 = s_lo; s0 < s_hi; s0 += kTabBatch) {
         int ls[kTabBatch], ns[kTabBatch];   // on their way together
 #pragma unroll
@@ -140,24 +138,25 @@ __global__ void __launch_bounds__(kTabThreads, 1) step_tables_kernel(const Table
             } else if (n < 0 || n > p.max_tokens) {
                 bad |= PKV_DEV_BAD_CHUNK;
             } else {
-                sum.a += n;
-                sum.b += (int)(((int64_t)l + n + 15) >> 4) - (int)(((int64_t)l + 15) >> 4);
+                sum.a = add_sat(sum.a, n);
+                sum.b += blocks_needed(l, n);   // (a table has at most 2^26 entries)
             }
         }
     }
-    Pair64 total;
-    const Pair64 incl = cta_scan(sum, sh_scan, &total);
-    if (total.a > p.max_tokens) bad |= PKV_DEV_BAD_CHUNK;
-    if (count < 0 || count > p.free_capacity || total.b > count) bad |= PKV_DEV_FREE_LIST;
+    PairSat total;
+    const PairSat incl = cta_scan(sum, sh_scan, &total);
+    if (total.a > (uint32_t)p.max_tokens) bad |= PKV_DEV_BAD_CHUNK;
+    if (count < 0 || count > p.free_capacity || total.b > (uint32_t)count) bad |= PKV_DEV_FREE_LIST;
     if (bad) atomicOr(&sh_bad, bad);
     {
-        int64_t a = incl.a - sum.a, b = incl.b - sum.b;
+        // (of use only where all lengths and sums are good)
+        uint32_t a = incl.a - sum.a, b = incl.b - sum.b;
         for (int s = s_lo; s < s_hi; ++s) {
             const int l = len[s], n = cu[s];
             cu[s] = (int)a;
             bx[s] = (int)b;
             a += n;
-            b += (int)(((int64_t)l + n + 15) >> 4) - (int)(((int64_t)l + 15) >> 4);
+            b += blocks_needed(l, n);
         }
     }
     if (tid == 0) {
@@ -173,7 +172,9 @@ __global__ void __launch_bounds__(kTabThreads, 1) step_tables_kernel(const Table
     if (fail && rank == 0 && tid == 0) set_status(p.dev_status, sh_bad);
 
     // ---- per-sequence outputs ----
-    const int gt = rank * nt + tid, gn = ranks * nt;
+    // warps in turn over the CTAs, so that few rows are spread over all of them
+    // (4,000 rows: 6.9 us; CTA after CTA 9.3 us)
+    const int gt = ((tid >> 5) * ranks + rank) * 32 + (tid & 31), gn = ranks * nt;
     for (int s = gt; s <= S; s += gn) {
         p.cu_seqlens[s] = fail ? 0 : cu[s];
         if (s < S) p.context_lens[s] = fail ? len[s] : len[s] + (cu[s + 1] - cu[s]);
@@ -187,42 +188,61 @@ __global__ void __launch_bounds__(kTabThreads, 1) step_tables_kernel(const Table
     const int32_t first_id = gt < taken ? top[-gt] : 0;
     int status = 0;
 
-    // ---- slots and positions, four rows at a time: a row's block is the
-    // sequence's open block (in its table) or one of those taken now ----
-    for (int64_t t0 = (int64_t)gt * 4; t0 < p.max_tokens; t0 += (int64_t)gn * 4) {
-        int64_t slot[4];
-        int32_t pos[4], id[4];
-        int s = t0 < tokens ? last_at_most(cu, S, (int)t0) : 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int64_t t = t0 + e;
-            id[e] = -1;
-            pos[e] = 0;
-            if (t < tokens) {
-                while (cu[s + 1] <= t) ++s;   // skips sequences without new tokens
-                const int q = len[s] + (int)(t - cu[s]);
-                const int j = q >> 4, old = (len[s] + 15) >> 4;
-                pos[e] = q;
-                id[e] = *(j < old ? p.block_tables + (int64_t)s * p.max_blocks + j : top - (bx[s] + j - old));
+    // ---- slots and positions: a row's block is the sequence's open block (in
+    // its table) or one of those taken now ----
+    auto entry = [&](int s, int t, int32_t &pos) {   // of row t of sequence s
+        pos = len[s] + (t - cu[s]);
+        const int j = pos >> 4, old = (len[s] + 15) >> 4;
+        return j < old ? p.block_tables + (int64_t)s * p.max_blocks + j : top - (bx[s] + j - old);
+    };
+    auto slot_of = [&](int32_t id, int32_t pos) {
+        if (id >= 0 && id < p.num_blocks) return (int64_t)id * 16 + (pos & 15);
+        status |= PKV_DEV_BAD_BLOCK_ID;
+        return (int64_t)-1;
+    };
+    if (p.max_tokens <= gn) {
+        // a row a thread: no walk from one row to the next (256 rows: 2.9 us instead
+        // of 3.4 in fours)
+        if (gt < p.max_tokens) {
+            int64_t slot = -1;
+            int32_t pos = 0;
+            if (gt < tokens) {
+                const int32_t id = *entry(last_at_most(cu, S, gt), gt, pos);
+                slot = slot_of(id, pos);
             }
+            p.slot_mapping[gt] = slot;
+            p.token_pos[gt] = pos;
         }
+    } else {
+        // four rows a thread
+        for (int64_t t0 = (int64_t)gt * 4; t0 < p.max_tokens; t0 += (int64_t)gn * 4) {
+            int64_t slot[4];
+            int32_t pos[4], id[4];
+            int s = t0 < tokens ? last_at_most(cu, S, (int)t0) : 0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const bool held = id[e] >= 0 && id[e] < p.num_blocks;
-            if (!held && t0 + e < tokens) status |= PKV_DEV_BAD_BLOCK_ID;
-            slot[e] = held ? (int64_t)id[e] * 16 + (pos[e] & 15) : -1;
-        }
-        if (p.vec && t0 + 4 <= p.max_tokens) {
-            reinterpret_cast<longlong2 *>(p.slot_mapping + t0)[0] = make_longlong2(slot[0], slot[1]);
-            reinterpret_cast<longlong2 *>(p.slot_mapping + t0)[1] = make_longlong2(slot[2], slot[3]);
-            *reinterpret_cast<int4 *>(p.token_pos + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (t0 + e < p.max_tokens) {
-                    p.slot_mapping[t0 + e] = slot[e];
-                    p.token_pos[t0 + e] = pos[e];
+            for (int e = 0; e < 4; ++e) {
+                id[e] = -1;
+                pos[e] = 0;
+                if (t0 + e < tokens) {
+                    const int t = (int)t0 + e;
+                    while (cu[s + 1] <= t) ++s;   // skips sequences without new tokens
+                    id[e] = *entry(s, t, pos[e]);
                 }
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) slot[e] = t0 + e < tokens ? slot_of(id[e], pos[e]) : -1;
+            if (p.vec && t0 + 4 <= p.max_tokens) {
+                reinterpret_cast<longlong2 *>(p.slot_mapping + t0)[0] = make_longlong2(slot[0], slot[1]);
+                reinterpret_cast<longlong2 *>(p.slot_mapping + t0)[1] = make_longlong2(slot[2], slot[3]);
+                *reinterpret_cast<int4 *>(p.token_pos + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (t0 + e < p.max_tokens) {
+                        p.slot_mapping[t0 + e] = slot[e];
+                        p.token_pos[t0 + e] = pos[e];
+                    }
+            }
         }
     }
     for (int k = gt; k < taken; k += gn) {
@@ -469,8 +489,12 @@ extern "C" int pkv_step_tables(const int32_t *seq_lens, const int32_t *new_lens,
     prm.num_blocks = num_blocks;
     prm.max_tokens = max_tokens;
     prm.vec = aligned(slot_mapping, 16) && aligned(token_pos, 16);
-    const bool small = num_seqs <= kTabThreads && max_tokens <= 4 * kTabThreads;
-    const int threads = small && num_seqs <= 256 && max_tokens <= 1024 ? 256 : kTabThreads;
+    // One CTA while it has a thread for each row, else a cluster; its scan of few
+    // sequences is quicker with fewer warps (1,400 sequences: 4.1 us in CTAs of 512
+    // threads, 4.5 in 1,024; 2,000 and 20 x 512 rows: 5.2 and 4.8; 16 sequences and
+    // 900 rows: 3.0 us in one CTA, 2.7 in 16).
+    const bool small = num_seqs <= 256 && max_tokens <= 256;
+    const int threads = small ? 256 : num_seqs <= 1536 ? 512 : kTabThreads;
     cudaError_t e = launch_cluster(step_tables_kernel, small ? 1 : kTabCluster, small ? 1 : kTabCluster, threads,
                                    (size_t)(3 * num_seqs + 2) * 4, static_cast<cudaStream_t>(stream), prm);
     if (e == cudaSuccess) e = cudaGetLastError();
