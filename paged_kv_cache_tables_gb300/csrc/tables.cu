@@ -264,6 +264,7 @@ struct ReleaseParams {
     int32_t *counts;     // workspace: [S] blocks each row gives back, then the list's count before the call
     int *dev_status;
     int S, max_blocks, free_capacity, num_blocks, window, sinks;
+    bool vec;            // the table's rows are 16-byte aligned
 };
 
 // Table entries [lo, hi) of sequence s that the call gives back.
@@ -288,70 +289,98 @@ __device__ __forceinline__ void release_range(const ReleaseParams &p, int s, int
     }
 }
 
-// A warp a row, kRelLoads entries of it under way in each lane; the blocks go
-// on the list in the order of the rows and of the blocks within a row.  Two
-// forms.  Up to kRelSmallRows rows are one launch: a cluster of CTAs counts its
-// rows' blocks, exchanges the CTAs' totals through distributed shared memory
-// and moves the blocks.  More rows are two launches over the whole GPU: one
-// counts into the workspace, the other sums the counts of the rows before its
-// own (each CTA reads them all, out of L2) and moves.  4,000 rows of up to
-// 2,048 blocks take 13 us so, and 49 us in one cluster of 16 CTAs of 1,024
-// threads; 256 rows of up to 512 take 5.8 us in one launch and 5.2 us in two,
-// which cost the host another 7 us (a launch, and the workspace).
+// A warp a row, 128 neighbouring entries a load; the blocks go on the list in the
+// order of the rows and of the blocks within a row.  Two forms.  Up to
+// kRelSmallRows rows are one launch: a cluster of CTAs counts its rows' blocks,
+// exchanges the CTAs' totals through distributed shared memory and moves the
+// blocks.  More rows are two launches over the whole GPU: one counts into the
+// workspace, the other sums the counts of the rows before its own (each CTA reads
+// them all, out of L2) and moves.  4,000 rows of up to 2,048 blocks take 11.8 us
+// so, and took 49 us in one cluster of 16 CTAs of 1,024 threads; 256 rows of up to
+// 512 take 5.5 us in one launch; two, 0.6 us less, cost the host another 7 us (a
+// launch, and the workspace).  Loads under way in a warp: few rows want the chain
+// of a long row short, many rows want registers for more warps (256 rows of up to
+// 2,048 blocks: 10.1 us with four and 11.5 with two, 4,000 of up to 333 13.4 and
+// 12.3, a copy of the table and the list included).
 constexpr int kRelThreads = 256;
-constexpr int kRelLoads = 8;
+constexpr int kRelSmallLoads = 4, kRelLoads = 2;
 constexpr int kRelSmallWarps = 16;
 constexpr int kRelSmallRows = kTabCluster * kRelSmallWarps;
 
-// visit(j0, ids): the entries j0 + 32 u + lane, u < kRelLoads, of row s that
-// are given back (others -1), in order
-template <typename F>
+// visit(j, ids): the entries j .. j + 3 of row s, of this lane and load, that are
+// given back (others -1); a load of the warp is 128 neighbouring entries, and the
+// loads come in order
+template <int LOADS, typename F>
 __device__ __forceinline__ void walk_row(const ReleaseParams &p, int s, int lane, int &status, F visit) {
     int lo, hi;
     release_range(p, s, lo, hi, status);
     const int32_t *row = p.block_tables + (int64_t)s * p.max_blocks;
-    for (int j0 = lo; j0 < hi; j0 += 32 * kRelLoads) {
-        int32_t id[kRelLoads];
+    for (int j0 = lo & ~3; j0 < hi; j0 += 128 * LOADS) {
+        int4 id[LOADS];
 #pragma unroll
-        for (int u = 0; u < kRelLoads; ++u) {
-            const int j = j0 + 32 * u + lane;
-            id[u] = j < hi ? row[j] : -1;
+        for (int u = 0; u < LOADS; ++u) {
+            const int j = j0 + 128 * u + 4 * lane;
+            id[u] = make_int4(-1, -1, -1, -1);
+            if (p.vec) {
+                if (j < hi) id[u] = *reinterpret_cast<const int4 *>(row + j);
+            } else {
+                if (j < hi) id[u].x = row[j];
+                if (j + 1 < hi) id[u].y = row[j + 1];
+                if (j + 2 < hi) id[u].z = row[j + 2];
+                if (j + 3 < hi) id[u].w = row[j + 3];
+            }
         }
 #pragma unroll
-        for (int u = 0; u < kRelLoads; ++u)
-            if (id[u] >= p.num_blocks) {
-                status |= PKV_DEV_BAD_BLOCK_ID;
-                id[u] = -1;
+        for (int u = 0; u < LOADS; ++u) {
+            const int j = j0 + 128 * u + 4 * lane;
+            int32_t e[4] = {id[u].x, id[u].y, id[u].z, id[u].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (j + i < lo || j + i >= hi) e[i] = -1;
+                if (e[i] >= p.num_blocks) {
+                    status |= PKV_DEV_BAD_BLOCK_ID;
+                    e[i] = -1;
+                }
             }
-        visit(j0, id);
+            visit(j, e);
+        }
     }
 }
 
 // Blocks of row s given back (all lanes get the count).
+template <int LOADS>
 __device__ __forceinline__ int count_row(const ReleaseParams &p, int s, int lane) {
     int status = 0, n = 0;
-    walk_row(p, s, lane, status, [&](int, const int32_t(&id)[kRelLoads]) {
+    walk_row<LOADS>(p, s, lane, status, [&](int, const int32_t(&e)[4]) {
 #pragma unroll
-        for (int u = 0; u < kRelLoads; ++u) n += id[u] >= 0;
+        for (int i = 0; i < 4; ++i) n += e[i] >= 0;
     });
     if (status) set_status(p.dev_status, status);
     return __reduce_add_sync(0xffffffffu, n);
 }
 
 // Moves row s's blocks to free_list[at..].
+template <int LOADS>
 __device__ __forceinline__ void move_row(const ReleaseParams &p, int s, int lane, int64_t at) {
     int ignored = 0;
     int32_t *row = p.block_tables + (int64_t)s * p.max_blocks;
-    walk_row(p, s, lane, ignored, [&](int j0, const int32_t(&id)[kRelLoads]) {
+    const unsigned before = (1u << lane) - 1u;
+    walk_row<LOADS>(p, s, lane, ignored, [&](int j, const int32_t(&e)[4]) {
+        int mine = 0, all = 0;
 #pragma unroll
-        for (int u = 0; u < kRelLoads; ++u) {
-            const unsigned m = __ballot_sync(0xffffffffu, id[u] >= 0);
-            if (id[u] >= 0) {
-                p.free_list[at + __popc(m & ((1u << lane) - 1u))] = id[u];
-                row[j0 + 32 * u + lane] = -1;
-            }
-            at += __popc(m);
+        for (int i = 0; i < 4; ++i) {
+            const unsigned m = __ballot_sync(0xffffffffu, e[i] >= 0);
+            mine += __popc(m & before);
+            all += __popc(m);
         }
+        int32_t *to = p.free_list + at + mine;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (e[i] >= 0) {
+                *to++ = e[i];
+                row[j + i] = -1;
+            }
+        at += all;
     });
 }
 
@@ -364,7 +393,7 @@ __global__ void __launch_bounds__(kRelSmallWarps * 32) release_small_kernel(cons
     pdl_wait_primary();
     pdl_launch_dependents();
     const int count = p.free_count[0];
-    const int n = s < p.S ? count_row(p, s, lane) : 0;
+    const int n = s < p.S ? count_row<kRelSmallLoads>(p, s, lane) : 0;
     if (lane == 0) sh_count[warp] = n;
     __syncthreads();
     int64_t at = 0, all = 0;
@@ -389,7 +418,7 @@ __global__ void __launch_bounds__(kRelSmallWarps * 32) release_small_kernel(cons
         return;
     }
     if (rank == 0 && threadIdx.x == 0) p.free_count[0] = count + (int)all;
-    if (n > 0) move_row(p, s, lane, count + at);
+    if (n > 0) move_row<kRelSmallLoads>(p, s, lane, count + at);
 }
 
 __global__ void __launch_bounds__(kRelThreads) release_count_kernel(const ReleaseParams p) {
@@ -398,7 +427,7 @@ __global__ void __launch_bounds__(kRelThreads) release_count_kernel(const Releas
     pdl_launch_dependents();
     if (blockIdx.x == 0 && threadIdx.x == 0) p.counts[p.S] = p.free_count[0];
     if (s >= p.S) return;
-    const int n = count_row(p, s, lane);
+    const int n = count_row<kRelLoads>(p, s, lane);
     if (lane == 0) p.counts[s] = n;
 }
 
@@ -410,11 +439,23 @@ __global__ void __launch_bounds__(kRelThreads) release_move_kernel(const Release
     pdl_launch_dependents();
     // blocks given back by the rows before this CTA's, and by all
     Pair64 sum{0, 0};
-    for (int i = tid; i < p.S; i += kRelThreads) {
-        const int n = p.counts[i];
-        sum.b += n;
-        if (i < first) sum.a += n;
+    constexpr int kBatch = 16;   // loads under way
+    for (int i0 = tid; i0 < p.S; i0 += kBatch * kRelThreads) {
+        int n[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int i = i0 + u * kRelThreads;
+            n[u] = i < p.S ? p.counts[i] : 0;
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            sum.b += n[u];
+            if (i0 + u * kRelThreads < first) sum.a += n[u];
+        }
     }
+    // and by this CTA's rows, one in each of its first lanes
+    const int near = lane < kRelThreads / 32 && first + lane < p.S ? p.counts[first + lane] : 0;
+    const int count = p.counts[p.S];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         sum.a += __shfl_xor_sync(0xffffffffu, sum.a, o);
@@ -428,15 +469,14 @@ __global__ void __launch_bounds__(kRelThreads) release_move_kernel(const Release
         at += sh_sum[w].a;
         all += sh_sum[w].b;
     }
-    const int count = p.counts[p.S];
     if (count < 0 || count > p.free_capacity || count + all > p.free_capacity) {
         if (blockIdx.x == 0 && tid == 0) set_status(p.dev_status, PKV_DEV_FREE_LIST);
         return;
     }
     if (blockIdx.x == 0 && tid == 0) p.free_count[0] = count + (int)all;
-    if (s >= p.S || p.counts[s] == 0) return;
-    for (int i = first; i < s; ++i) at += p.counts[i];
-    move_row(p, s, lane, count + at);
+    if (__shfl_sync(0xffffffffu, near, warp) == 0) return;
+    at += __reduce_add_sync(0xffffffffu, lane < warp ? near : 0);
+    move_row<kRelLoads>(p, s, lane, count + at);
 }
 
 }  // namespace pkv
@@ -537,6 +577,7 @@ extern "C" int pkv_release_blocks(int32_t *block_tables, int max_blocks_per_seq,
     prm.num_blocks = num_blocks;
     prm.window = window;
     prm.sinks = num_sinks;
+    prm.vec = aligned(block_tables, 16) && max_blocks_per_seq % 4 == 0;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (small) {
