@@ -89,6 +89,19 @@ def test_step_tables_many_sequences(cuda_lib, S):
     assert got[1] == 0
 
 
+@pytest.mark.parametrize("S", [21, 1537, 2100])
+@pytest.mark.parametrize("misaligned", [False, True])
+def test_step_tables_many_rows(cuda_lib, S, misaligned):
+    """More rows than the launch has threads, few and many sequences, padding behind."""
+    rng = random.Random(S)
+    lens = [rng.randint(0, 100) for _ in range(S)]
+    new = [1000 if s < 20 else rng.choice([0, 1, 5]) for s in range(S)]
+    pool = Pool(lens, 70, 20 * 64 + S, seed=S)
+    T = sum(new) + 1003
+    got, status = run_step(pool, new, 70, T, misaligned)
+    assert got == ref.step_tables(lens, new, pool.table, pool.free, pool.count, T) and status == 0
+
+
 def test_step_tables_without_sequences(cuda_lib):
     pool = Pool([], 4, 3)
     got, status = run_step(pool, [], 4, 6)
@@ -220,6 +233,28 @@ def test_release_long_rows(cuda_lib, S):
                    workspace=work, dev_status=status)
     want = ref.release(pool.table, lens, fin, 5000, 100, pool.free, pool.count, pool.num_blocks)
     assert (table.tolist(), free.tolist(), count.item()) == tuple(want) and status.item() == 0
+
+
+@pytest.mark.parametrize("S", [9, 300])
+@pytest.mark.parametrize("mb,offset", [(333, 0), (334, 0), (335, 0), (336, 1), (336, 2), (336, 4)])
+def test_release_rows_of_any_alignment(cuda_lib, S, mb, offset):
+    rng = random.Random(mb + offset)
+    lens = [rng.randint(0, mb * 16) for _ in range(S)]
+    pool = Pool(lens, mb, 3, seed=S)
+    for r in pool.table:
+        for j in rng.sample(range(mb), 50):
+            r[j] = -1
+    pool.free += [-7] * (S * mb)
+    fin = [int(rng.random() < 0.3) for _ in lens]
+    lens_d, _, free, count = pool.device(mb)
+    room = torch.full((offset + S * mb + 4,), -9, dtype=torch.int32, device="cuda")
+    table = room[offset:offset + S * mb].view(S, mb)
+    table.copy_(i32(pool.table))
+    status = i32([0])
+    release_blocks(table, lens_d, free, count, pool.num_blocks, finished=i32(fin), window=700, num_sinks=37, dev_status=status)
+    want = ref.release(pool.table, lens, fin, 700, 37, pool.free, pool.count, pool.num_blocks)
+    assert (table.tolist(), free.tolist(), count.item()) == tuple(want) and status.item() == 0
+    assert (room[:offset] == -9).all() and (room[offset + S * mb:] == -9).all()
 
 
 @pytest.mark.parametrize("S", [40, 400])

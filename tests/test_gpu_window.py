@@ -175,6 +175,18 @@ def test_prefill_head_layouts(cuda_lib, Hq, Hkv, d, dtype):
     assert st.status.item() == 0
 
 
+@pytest.mark.parametrize("Hq,Hkv,d,dtype,out_dtype", [(32, 2, 64, BF16, BF16), (32, 2, 128, F16, F16), (32, 2, 128, BF16, F32),
+                                                      (20, 4, 128, BF16, BF16), (20, 4, 64, F16, F32)])
+@pytest.mark.parametrize("window,sinks", [(300, 20), (40, 0), (5000, 0)])
+def test_prefill_of_many_units(cuda_lib, Hq, Hkv, d, dtype, out_dtype, window, sinks):
+    """More units than SMs: a CTA takes several, of one key tile up to many, and some chunks have none."""
+    st = Step([700, 1400, 333, 900, 640, 0], [700, 650, 1, 512, 333, 0], Hq, Hkv, d, dtype, window, sinks)
+    want, bound = st.reference(out_dtype, True)
+    got = st.prefill(out_dtype)
+    ref.assert_within(got, want, bound)
+    assert torch.equal(got, st.prefill(out_dtype)) and st.status.item() == 0
+
+
 def test_prefill_without_sinks_far_behind(cuda_lib):
     """Rows whose first walked key tile holds none of their keys, long contexts."""
     st = Step([6000, 5000], [300, 1], 4, 1, 128, BF16, 20, 0, seed=3)
