@@ -437,17 +437,8 @@ def release_blocks(block_tables, seq_lens, free_list, free_count, num_blocks, fi
     free_list int32 [capacity] / free_count int32 [1]; their entries in
     block_tables int32 [S, max_blocks] become -1.  workspace: uint8 CUDA tensor
     (allocated here if None and needed)."""
-    calls = _calls or _load_calls()
-    if workspace is None and len(block_tables) > 256:
-        import torch
-        n = release_workspace_size(len(block_tables))
-        if stream is None:
-            workspace = torch.empty(n, dtype=torch.uint8, device=block_tables.device)
-        else:   # memory of the stream that the call runs on
-            with torch.cuda.stream(stream):
-                workspace = torch.empty(n, dtype=torch.uint8, device=block_tables.device)
-    st = calls.release_blocks(block_tables, seq_lens, free_list, free_count, num_blocks, finished, window, num_sinks,
-                              workspace, dev_status, stream)
+    st = (_calls or _load_calls()).release_blocks(block_tables, seq_lens, free_list, free_count, num_blocks, finished, window,
+                                                  num_sinks, workspace, dev_status, stream)
     if st:
         raise PkvError("pkv_release_blocks", st)
 

@@ -10,6 +10,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -136,6 +137,20 @@ void *stream_arg(PyObject *o, int device) {
         refuse(PyExc_ValueError, "the stream belongs to another device than the tensors");
     return reinterpret_cast<void *>((uintptr_t)number("cuda_stream"));
 }
+
+// Torch's memory for what is launched on a stream of the current device before
+// this goes: what takes it next there runs behind that.
+struct StreamMemory {
+    void *p = nullptr;
+    StreamMemory() = default;
+    StreamMemory(const StreamMemory &) = delete;
+    void *get(size_t bytes, void *stream) {
+        return p = c10::cuda::CUDACachingAllocator::raw_alloc_with_stream(bytes, static_cast<cudaStream_t>(stream));
+    }
+    ~StreamMemory() {
+        if (p) c10::cuda::CUDACachingAllocator::raw_delete(p);
+    }
+};
 
 int *status_arg(PyObject *o, int device) {
     return static_cast<int *>(ptr_or_null(o, "dev_status", at::kInt, {1}, device));
@@ -335,10 +350,14 @@ PyObject *release_blocks(PyObject *, Args a, Py_ssize_t n) {
             work = ptr(a[8], "workspace", at::kByte, {(int64_t)nwork}, dev);
         }
         c10::cuda::OptionalCUDAGuard guard(c10::Device(c10::kCUDA, (c10::DeviceIndex)dev));
+        void *stream = stream_arg(a[10], dev);
+        // without a workspace of the caller's: memory of the stream that the call runs on
+        StreamMemory own;
+        if (a[8] == Py_None && (nwork = pkv_release_workspace_size(size_arg(S, "block_tables"))) > 0)
+            work = own.get(nwork, stream);
         return pkv_release_blocks(tables, size_arg(MB, "block_tables"), lens, finished, size_arg(S, "block_tables"),
                                   int_arg(a[6], "window"), int_arg(a[7], "num_sinks"), list, size_arg(capacity, "free_list"),
-                                  count, int_arg(a[4], "num_blocks"), 16, work, nwork, status_arg(a[9], dev),
-                                  stream_arg(a[10], dev));
+                                  count, int_arg(a[4], "num_blocks"), 16, work, nwork, status_arg(a[9], dev), stream);
     });
 }
 

@@ -348,3 +348,23 @@ def test_step_then_release_on_a_side_stream_with_padding_rows(cuda_lib):
     assert slots.tolist() == sl and pos.tolist() == ps
     tab, fr, n = ref.release(tab, lens, [0, 1, 0], 20, 4, pool.free, n, pool.num_blocks)
     assert table.tolist() == tab and free.tolist()[:n] == fr[:n] and count.item() == n and status.item() == 0
+
+
+def test_release_of_many_rows_on_a_given_stream(cuda_lib):
+    """Its workspace is the given stream's memory: what the current stream takes meanwhile is another's."""
+    rng = random.Random(8)
+    S, mb = 2000, 64
+    lens = [rng.randint(0, mb * 16) for _ in range(S)]
+    pool = Pool(lens, mb, 3)
+    pool.free += [-7] * (S * mb)
+    fin = [rng.randint(0, 1) for _ in lens]
+    lens_d, table, free, count = pool.device(mb)
+    status, fin_d, st = i32([0]), i32(fin), torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    release_blocks(table, lens_d, free, count, pool.num_blocks, finished=fin_d, window=100, num_sinks=4, dev_status=status,
+                   stream=st)
+    others = [torch.full((4 * S + 4,), 255, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    torch.cuda.current_stream().wait_stream(st)
+    want = ref.release(pool.table, lens, fin, 100, 4, pool.free, pool.count, pool.num_blocks)
+    assert (table.tolist(), free.tolist(), count.item()) == tuple(want) and status.item() == 0
+    assert all((o == 255).all() for o in others)
