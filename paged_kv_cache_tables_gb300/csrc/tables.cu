@@ -269,8 +269,8 @@ struct ReleaseParams {
 
 // Table entries [lo, hi) of sequence s that the call gives back.
 __device__ __forceinline__ void release_range(const ReleaseParams &p, int s, int &lo, int &hi, int &status) {
-    int64_t l = p.seq_lens[s];
-    const bool finished = p.finished != nullptr && p.finished[s] != 0;
+    int64_t l = __ldcg(p.seq_lens + s);
+    const bool finished = p.finished != nullptr && __ldcg(p.finished + s) != 0;
     if (l < 0 || l > (int64_t)p.max_blocks * 16) {
         status |= PKV_DEV_BAD_CONTEXT;
         l = l < 0 ? 0 : (int64_t)p.max_blocks * 16;
@@ -295,9 +295,9 @@ __device__ __forceinline__ void release_range(const ReleaseParams &p, int s, int
 // exchanges the CTAs' totals through distributed shared memory and moves the
 // blocks.  More rows are two launches over the whole GPU: one counts into the
 // workspace, the other sums the counts of the rows before its own (each CTA reads
-// them all, out of L2) and moves.  4,000 rows of up to 2,048 blocks take 11.8 us
+// them all, out of L2) and moves.  4,000 rows of up to 2,048 blocks take 11.6 us
 // so, and took 49 us in one cluster of 16 CTAs of 1,024 threads; 256 rows of up to
-// 512 take 5.5 us in one launch; two, 0.6 us less, cost the host another 7 us (a
+// 512 take 5.2 us in one launch; two, 0.6 us less, cost the host another 7 us (a
 // launch, and the workspace).  Loads under way in a warp: few rows want the chain
 // of a long row short, many rows want registers for more warps (256 rows of up to
 // 2,048 blocks: 10.1 us with four and 11.5 with two, 4,000 of up to 333 13.4 and
@@ -307,13 +307,11 @@ constexpr int kRelSmallLoads = 4, kRelLoads = 2;
 constexpr int kRelSmallWarps = 16;
 constexpr int kRelSmallRows = kTabCluster * kRelSmallWarps;
 
-// visit(j, ids): the entries j .. j + 3 of row s, of this lane and load, that are
-// given back (others -1); a load of the warp is 128 neighbouring entries, and the
+// visit(j, ids): of the entries [lo, hi) of row s, those at j .. j + 3, of this
+// lane and load, that are given back (others -1); a load of the warp is 128 neighbouring entries, and the
 // loads come in order
 template <int LOADS, typename F>
-__device__ __forceinline__ void walk_row(const ReleaseParams &p, int s, int lane, int &status, F visit) {
-    int lo, hi;
-    release_range(p, s, lo, hi, status);
+__device__ __forceinline__ void walk_row(const ReleaseParams &p, int s, int lo, int hi, int lane, int &status, F visit) {
     const int32_t *row = p.block_tables + (int64_t)s * p.max_blocks;
     for (int j0 = lo & ~3; j0 < hi; j0 += 128 * LOADS) {
         int4 id[LOADS];
@@ -349,9 +347,10 @@ __device__ __forceinline__ void walk_row(const ReleaseParams &p, int s, int lane
 
 // Blocks of row s given back (all lanes get the count).
 template <int LOADS>
-__device__ __forceinline__ int count_row(const ReleaseParams &p, int s, int lane) {
+__device__ __forceinline__ int count_row(const ReleaseParams &p, int s, int &lo, int &hi, int lane) {
     int status = 0, n = 0;
-    walk_row<LOADS>(p, s, lane, status, [&](int, const int32_t(&e)[4]) {
+    release_range(p, s, lo, hi, status);
+    walk_row<LOADS>(p, s, lo, hi, lane, status, [&](int, const int32_t(&e)[4]) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) n += e[i] >= 0;
     });
@@ -361,11 +360,11 @@ __device__ __forceinline__ int count_row(const ReleaseParams &p, int s, int lane
 
 // Moves row s's blocks to free_list[at..].
 template <int LOADS>
-__device__ __forceinline__ void move_row(const ReleaseParams &p, int s, int lane, int64_t at) {
+__device__ __forceinline__ void move_row(const ReleaseParams &p, int s, int lo, int hi, int lane, int64_t at) {
     int ignored = 0;
     int32_t *row = p.block_tables + (int64_t)s * p.max_blocks;
     const unsigned before = (1u << lane) - 1u;
-    walk_row<LOADS>(p, s, lane, ignored, [&](int j, const int32_t(&e)[4]) {
+    walk_row<LOADS>(p, s, lo, hi, lane, ignored, [&](int j, const int32_t(&e)[4]) {
         int mine = 0, all = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -393,7 +392,8 @@ __global__ void __launch_bounds__(kRelSmallWarps * 32) release_small_kernel(cons
     pdl_wait_primary();
     pdl_launch_dependents();
     const int count = p.free_count[0];
-    const int n = s < p.S ? count_row<kRelSmallLoads>(p, s, lane) : 0;
+    int lo = 0, hi = 0;
+    const int n = s < p.S ? count_row<kRelSmallLoads>(p, s, lo, hi, lane) : 0;
     if (lane == 0) sh_count[warp] = n;
     __syncthreads();
     int64_t at = 0, all = 0;
@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(kRelSmallWarps * 32) release_small_kernel(cons
         return;
     }
     if (rank == 0 && threadIdx.x == 0) p.free_count[0] = count + (int)all;
-    if (n > 0) move_row<kRelSmallLoads>(p, s, lane, count + at);
+    if (n > 0) move_row<kRelSmallLoads>(p, s, lo, hi, lane, count + at);
 }
 
 __global__ void __launch_bounds__(kRelThreads) release_count_kernel(const ReleaseParams p) {
@@ -427,7 +427,8 @@ __global__ void __launch_bounds__(kRelThreads) release_count_kernel(const Releas
     pdl_launch_dependents();
     if (blockIdx.x == 0 && threadIdx.x == 0) p.counts[p.S] = p.free_count[0];
     if (s >= p.S) return;
-    const int n = count_row<kRelLoads>(p, s, lane);
+    int lo, hi;
+    const int n = count_row<kRelLoads>(p, s, lo, hi, lane);
     if (lane == 0) p.counts[s] = n;
 }
 
@@ -435,6 +436,10 @@ __global__ void __launch_bounds__(kRelThreads) release_move_kernel(const Release
     __shared__ Pair64 sh_sum[kRelThreads / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int first = blockIdx.x * (kRelThreads / 32), s = first + warp;
+    // the lengths do not come from the launch before, which waited for the one they
+    // come from before it let this one start; they are read past the L1 cache
+    int lo = 0, hi = 0, reported = 0;
+    if (s < p.S) release_range(p, s, lo, hi, reported);
     pdl_wait_primary();
     pdl_launch_dependents();
     // blocks given back by the rows before this CTA's, and by all
@@ -476,7 +481,7 @@ __global__ void __launch_bounds__(kRelThreads) release_move_kernel(const Release
     if (blockIdx.x == 0 && tid == 0) p.free_count[0] = count + (int)all;
     if (__shfl_sync(0xffffffffu, near, warp) == 0) return;
     at += __reduce_add_sync(0xffffffffu, lane < warp ? near : 0);
-    move_row<kRelLoads>(p, s, lane, count + at);
+    move_row<kRelLoads>(p, s, lo, hi, lane, count + at);
 }
 
 }  // namespace pkv
