@@ -32,9 +32,8 @@
 // us, 77 %; 64 tokens: 1.6 us.  Before the loads were issued together: 50.2, 24.8
 // and 1.9 us.  Measured and left: CTAs of one warp (20.0 us, but calls of many
 // small rows are then bound by the launch of CTAs, about 3 a ns), key and value
-// heads in one warp (21.1 us), the
-// norms of all groups worked out first (21.2 us), the weights folded into cos and
-// sin besides (23.4 us).
+// heads in one warp (21.1 us), the norms of all groups worked out first (21.2 us),
+// the weights folded into cos and sin besides (23.4 us).
 #include <cuda_runtime.h>
 
 #include <cmath>
