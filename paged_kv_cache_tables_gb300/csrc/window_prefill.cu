@@ -32,23 +32,24 @@
 // While one tile's softmax runs, the tensor cores work on the other's products:
 // the two issuers take turns, P V of a key tile and S of the next one turn.  Left
 // to themselves the tiles fall into step, both softmaxes at once and then both
-// products: 3,500 to 3,750 cycles a key tile for the two, in turns 2,650 to 2,900.
+// products (with P rounded once, 3,500 to 3,750 cycles a key tile for the two, in
+// turns 2,650 to 2,900).
 // Loads, products and softmax run across the units: while a unit's outputs are
 // stored, the next one's Q, K and V arrive.
 //
-// P is rounded to 16 bits once when the output is 16 bits wide, an error of the
-// output's own kind: half a step of each weight (2^-8 sum p|v| for bf16, 2^-11
-// for fp16).  A 32-bit output gets a second product with the rounding residual.
-// Three chunks of 3,500 to 4,100 rows x 32 heads, window 4,096, head_dim 128: 445
-// us, 1,665 TFLOP/s of the rows' own products (87 % of the measured cuBLAS burst;
-// without turns 509 us); 8 chunks of 512, window 1,024: 60 us (72).  The causal
-// kernel's design with a window took 764 and 122 us: residual products 1.25x, pages
-// loaded as two boxes of 2 KB (1.45 us for 64 KB an SM, these 0.92), V cleared by
-// the softmax warps, the first tokens' pages a tile of their own, one unit a CTA.
-// What bounds it now: the tensor cores' turns, 1.35 us a key tile of both query
-// tiles (products alone 1.2 us, loads alone 0.9), the masks of a unit's first and
-// last key tiles, 0.5 us each, and at a unit's end its outputs and the wait for the
-// next Q, 1.3 us each.  Measured and left: the next unit worked out while the last
+// P goes to the tensor cores as a 16-bit value and its 16-bit rounding residual, two
+// products with V: about 16 significant bits, as in the other attention kernels.  P
+// rounded once would err by half a step of each weight (2^-8 sum p|v| for bf16), as
+// much as the output's own rounding: against 64 bits 0.0023 relative instead of
+// 0.0017, and past 2e-3 where a row sees few keys.  What it would save: 445 us
+// instead of 641 below, 60 instead of 80.
+// Three chunks of 3,500 to 4,100 rows x 32 heads, window 4,096, head_dim 128: 641
+// us, 740 GFLOP of the rows' own products at 1,155 TFLOP/s (61 % of the measured
+// cuBLAS burst), 1,110 with the residual's at 1,732 (91 %); 32-bit output 695 to 716.
+// 8 chunks of 512, window 1,024: 80 us (92).  What bounds it: the tensor cores' turns,
+// the masks of a unit's first and last key tiles, and at a unit's end its outputs and
+// the wait for the next Q.
+// Measured with P rounded once (445 us), and left: the next unit worked out while the last
 // tile runs (head_dim 64: 368 -> 395 us, 3 x 4000: 445 -> 442) and its Q loaded to
 // a third slot (3 x 4000: 457 -> 464, 8 x 2,048: 178 -> 193, before outputs were
 // staged), units halved for the last round of CTAs (453 -> 487 us).
@@ -147,7 +148,7 @@ struct WpShape {
     static constexpr int STAGE_BYTES = 2 * TILE;            // K then V
     // 32-key groups of P after which the first part of P V may start.  Three
     // chunks of 3,500-4,100 rows, window 4,096, after one, two and three groups:
-    // 382, 371 and 380 us with head_dim 64; 441 and 449 after two and three with 128.
+    // 538, 536 and 547 us with head_dim 64; 632, 641 and 644 with 128.
     static constexpr int FIRST_PART = 2;
     static constexpr int OFF_Q = 0;                         // tile A, then tile B
     static constexpr int OFF_KV = 2 * Q_BYTES;
@@ -183,8 +184,8 @@ __device__ __forceinline__ void stores_read() { asm volatile("cp.async.bulk.wait
 // Until this thread's stores are complete.
 __device__ __forceinline__ void stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
-// TILES: query tiles of a unit, 2, or 1 (A alone)
-template <typename T, int D, bool RESIDUAL, int TILES>
+// WIDE: a 32-bit output.  TILES: query tiles of a unit, 2, or 1 (A alone)
+template <typename T, int D, bool WIDE, int TILES>
 __global__ void __launch_bounds__(kWpThreads, 1)
     window_prefill_kernel(const WindowPrefillParams p, const __grid_constant__ CUtensorMap tk,
                           const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tq,
@@ -463,7 +464,7 @@ __global__ void __launch_bounds__(kWpThreads, 1)
                             const uint64_t vp = vb + (uint32_t)(kk * Sh::PAGE >> 4);
                             if (leader) {
                                 tc::mma_f16_ts(d_o, ph, vp, idesc_o, j > 0 || kk > 0);
-                                if constexpr (RESIDUAL) tc::mma_f16_ts(d_o, ph + 16, vp, idesc_o, true);
+                                tc::mma_f16_ts(d_o, ph + 16, vp, idesc_o, true);   // the weights' rounding residual
                             }
                         }
                     }
@@ -584,7 +585,7 @@ __global__ void __launch_bounds__(kWpThreads, 1)
                     }
                 }
                 // P = 2^(x - m_used) over the same columns, 32 keys at a time: 16
-                // columns of rounded pairs, then (RESIDUAL) 16 of residual pairs.
+                // columns of rounded pairs, then 16 of residual pairs.
                 // A row that has seen no key yet has nothing to subtract.
                 const float sub = m_used == -INFINITY ? 0.f : m_used;
                 const uint64_t negm2 = f2_pack(-sub, -sub);
@@ -600,13 +601,10 @@ __global__ void __launch_bounds__(kWpThreads, 1)
                         b = exp2_approx(b);
                         const uint64_t ab = f2_pack(a, b);
                         sum2[e & 1] = f2_add(sum2[e & 1], ab);
-                        if constexpr (RESIDUAL)
-                            pack2_split2<T>(ab, a, b, hi[e], lo[e]);
-                        else
-                            hi[e] = pack2<T>(a, b);
+                        pack2_split2<T>(ab, a, b, hi[e], lo[e]);
                     }
                     tc::tmem_st16(scol + cc * 32, hi);
-                    if constexpr (RESIDUAL) tc::tmem_st16(scol + cc * 32 + 16, lo);
+                    tc::tmem_st16(scol + cc * 32 + 16, lo);
                     if (cc == Sh::FIRST_PART - 1 || cc == 3) {   // a part of P is ready
                         tc::tmem_wait_st();
                         tc::fence_before_sync();
@@ -629,12 +627,13 @@ __global__ void __launch_bounds__(kWpThreads, 1)
             // lines an instruction, 8 x 2,048 rows take 178 us instead of 169.  Where
             // the warp's 32 rows are whole tokens TMA stores them, beside the next
             // 128 bytes or the next unit: 162 us instead of 165 (8 x 1,000-1,500 rows
-            // of 8 heads, window 128: 21.9 and 22.8; 3 x 4000: 445 and 440).
-            constexpr int kCols = RESIDUAL ? 32 : 64;      // a 32-bit output or a 16-bit one
-            constexpr int kSize = RESIDUAL ? 4 : 2;
+            // of 8 heads, window 128: 21.9 and 22.8; 3 x 4000: 445 and 440; all with
+            // P rounded once).
+            constexpr int kCols = WIDE ? 32 : 64;      // a 32-bit output or a 16-bit one
+            constexpr int kSize = WIDE ? 4 : 2;
             const int64_t at = valid ? ((int64_t)(u.row0 + tok) * p.Hq + (int64_t)u.h * p.G + head) * D * kSize : -1;
             uint8_t *stage = sm + Sh::OFF_OUT + (warp - 4) * 4096;
-            const bool box = !RESIDUAL && p.boxes && __all_sync(0xffffffffu, valid);
+            const bool box = !WIDE && p.boxes && __all_sync(0xffffffffu, valid);
 #pragma unroll 1
             for (int cc = 0; cc < D; cc += kCols) {
                 float v[kCols];
@@ -646,7 +645,7 @@ __global__ void __launch_bounds__(kWpThreads, 1)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     uint4 w;
-                    if constexpr (RESIDUAL)
+                    if constexpr (WIDE)
                         w = make_uint4(__float_as_uint(v[4 * e] * inv), __float_as_uint(v[4 * e + 1] * inv),
                                        __float_as_uint(v[4 * e + 2] * inv), __float_as_uint(v[4 * e + 3] * inv));
                     else
@@ -698,7 +697,7 @@ static int encode_page_map(CUtensorMap *map, const void *base, int num_blocks, i
     return encode_tiled_map(map, base, 4, dims, strides, box);
 }
 
-template <typename T, int D, bool RESIDUAL, int TILES>
+template <typename T, int D, bool WIDE, int TILES>
 static int launch_window_prefill(const WindowPrefillParams &prm, const CUtensorMap &tk, const CUtensorMap &tv,
                                  const CUtensorMap &tq, const CUtensorMap &tout, int grid, cudaStream_t stream) {
     using Sh = WpShape<D>;
@@ -708,7 +707,7 @@ static int launch_window_prefill(const WindowPrefillParams &prm, const CUtensorM
     static int regs_ok = 0;   // 0 unknown, 1 as sized, -1 not
     if (regs_ok == 0) {
         cudaFuncAttributes fa;
-        cudaError_t e = cudaFuncGetAttributes(&fa, window_prefill_kernel<T, D, RESIDUAL, TILES>);
+        cudaError_t e = cudaFuncGetAttributes(&fa, window_prefill_kernel<T, D, WIDE, TILES>);
         if (e != cudaSuccess) return cuda_fail(e);
         regs_ok = fa.numRegs == kWpLaunchRegs ? 1 : -1;
         if (regs_ok < 0) {
@@ -721,12 +720,12 @@ static int launch_window_prefill(const WindowPrefillParams &prm, const CUtensorM
     if (regs_ok < 0) return PKV_ERR_UNSUPPORTED;
     static unsigned long long attr_set = 0;   // per instantiation and device
     if (!done_on_device(&attr_set)) {
-        cudaError_t e = cudaFuncSetAttribute(window_prefill_kernel<T, D, RESIDUAL, TILES>,
+        cudaError_t e = cudaFuncSetAttribute(window_prefill_kernel<T, D, WIDE, TILES>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::SMEM_BYTES);
         if (e != cudaSuccess) return cuda_fail(e);
         mark_done_on_device(&attr_set);
     }
-    cudaError_t e = launch_pdl(window_prefill_kernel<T, D, RESIDUAL, TILES>, dim3(grid), dim3(kWpThreads), Sh::SMEM_BYTES, stream,
+    cudaError_t e = launch_pdl(window_prefill_kernel<T, D, WIDE, TILES>, dim3(grid), dim3(kWpThreads), Sh::SMEM_BYTES, stream,
                                prm, tk, tv, tq, tout);
     if (e == cudaSuccess) e = cudaGetLastError();
     return e == cudaSuccess ? PKV_OK : cuda_fail(e);
@@ -765,10 +764,11 @@ extern "C" int pkv_paged_window_prefill_attention(void *out, const void *q, cons
     if (rc != PKV_OK) return rc;
     const int rtok = kWpRows / G;
     // query tiles of a unit: two, which share every K and V tile; or one, when
-    // all units then run at once: a step of 128 keys takes 1.33 us with two tiles on
-    // an SM and 0.95 us with one (two / one, us: 512 rows behind 4,096, window
-    // 1,024: 18.8 / 17.2; 16 rows: 7.1 / 6.1; three chunks of 3,500-4,100 rows, which
-    // fill the GPU either way: 449 / 776).  A 32-bit output always takes two.
+    // all units then run at once and a step of 128 keys has one tile's products
+    // (two / one, us, window 1,024: 512 rows behind up to 4,096 26.2 / 23.6, behind
+    // 4,096 24.1 / 23.4; 2 x 256 rows 24.2 / 22.2; 16 rows 23.9 / 22.9; three chunks of
+    // 3,500-4,100 rows, which fill the GPU either way, with P rounded once: 449 / 776).
+    // A 32-bit output always takes two.
     auto units_of = [&](int tiles) { return ((int64_t)max_q_len + tiles * rtok - 1) / (tiles * rtok); };
     const bool one = out_dtype != PKV_DTYPE_F32 && num_seqs * units_of(1) * num_kv_heads <= sms;
     const int qtiles = one ? 1 : 2;
@@ -814,12 +814,12 @@ extern "C" int pkv_paged_window_prefill_attention(void *out, const void *q, cons
     prm.scale_log2 = scale * 1.4426950408889634f;
     prm.out_dtype = out_dtype;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    auto launch = [&](auto type, auto residual, auto tiles) {
+    auto launch = [&](auto type, auto wide, auto tiles) {
         using T = decltype(type);
-        constexpr bool R = decltype(residual)::value;
+        constexpr bool W = decltype(wide)::value;
         constexpr int N = decltype(tiles)::value;
-        return head_dim == 128 ? launch_window_prefill<T, 128, R, N>(prm, tk, tv, tq, tout, (int)grid, st)
-                               : launch_window_prefill<T, 64, R, N>(prm, tk, tv, tq, tout, (int)grid, st);
+        return head_dim == 128 ? launch_window_prefill<T, 128, W, N>(prm, tk, tv, tq, tout, (int)grid, st)
+                               : launch_window_prefill<T, 64, W, N>(prm, tk, tv, tq, tout, (int)grid, st);
     };
     using Yes = std::true_type;
     using No = std::false_type;
