@@ -407,13 +407,14 @@ int pkv_paged_window_decode_attention(void *out, const void *q, const void *k_ca
  * pkv_paged_window_prefill_attention -- pkv_paged_prefill_attention over a
  * window: row i of chunk c sits at position context_lens[c] - q_len + i.
  * Arguments as there; scale must be positive; out and q are 16-B aligned.  A
- * chunk whose rows lie outside [0, total_q) is skipped and sets
- * PKV_DEV_BAD_CHUNK.  The softmax weights meet V as a 16-bit value and its
- * rounding residual for either output type, as in pkv_paged_prefill_attention.
- * Positions that no row of the chunk sees may hold anything; an infinity or NaN
- * in V at a position that some of a chunk's rows see can reach neighbouring
- * rows that do not (a hidden weight is a multiplication by zero), as it can in
- * pkv_paged_prefill_attention.
+ * chunk whose rows lie outside [0, total_q), or that is longer than max_q_len
+ * (lengths built on the device can be), is skipped and sets PKV_DEV_BAD_CHUNK.
+ * (With num_seqs, max_q_len or total_q 0 nothing is launched, nor reported.)
+ * The softmax weights meet V as a 16-bit value and its rounding residual for
+ * either output type, as in pkv_paged_prefill_attention.  Positions that no row
+ * of the chunk sees may hold anything; an infinity or NaN in V at a position
+ * that some of a chunk's rows see can reach neighbouring rows that do not (a
+ * hidden weight is a multiplication by zero), as it can there.
  */
 int pkv_paged_window_prefill_attention(void *out, const void *q, const int32_t *cu_seqlens, int num_seqs,
                                        int max_q_len, int total_q, const void *k_cache, const void *v_cache,

@@ -96,7 +96,7 @@ struct WindowPrefillParams {
     int *dev_status;
     int max_blocks, num_blocks, Hq, Hkv, G;
     int rtok, units_per_seq;
-    int window, sinks, total_q;
+    int window, sinks, total_q, max_q_len;
     float scale_log2;
     int out_dtype;
     bool boxes;   // a warp's 32 rows are whole tokens: tout has a box for them
@@ -283,7 +283,8 @@ __global__ void __launch_bounds__(kWpThreads, 1)
                 const int ctx = __ldg(p.context_lens + c);
                 const int i0 = unit * TILES * p.rtok;
                 int bad = 0;
-                if (q_len < 0 || q_len > ctx || q0 < 0 || q_len > p.total_q - q0)
+                // (rows past max_q_len have no unit)
+                if (q_len < 0 || q_len > ctx || q_len > p.max_q_len || q0 < 0 || q_len > p.total_q - q0)
                     bad = PKV_DEV_BAD_CHUNK;
                 else if (ctx > p.max_blocks * 16)
                     bad = PKV_DEV_BAD_CONTEXT;
@@ -811,6 +812,7 @@ extern "C" int pkv_paged_window_prefill_attention(void *out, const void *q, cons
     prm.window = window < capacity ? window : (int)capacity;   // no context is longer
     prm.sinks = num_sinks < capacity ? num_sinks : (int)capacity;
     prm.total_q = total_q;
+    prm.max_q_len = max_q_len;
     prm.scale_log2 = scale * 1.4426950408889634f;
     prm.out_dtype = out_dtype;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
