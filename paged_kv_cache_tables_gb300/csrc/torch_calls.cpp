@@ -152,6 +152,17 @@ struct StreamMemory {
     }
 };
 
+// The interpreter is free for other threads while this lives: a launch waits
+// when the stream's queue is full.  Nothing of Python's may be used meanwhile.
+class OtherThreads {
+    PyThreadState *state_ = PyEval_SaveThread();
+
+  public:
+    OtherThreads() = default;
+    OtherThreads(const OtherThreads &) = delete;
+    ~OtherThreads() { PyEval_RestoreThread(state_); }
+};
+
 int *status_arg(PyObject *o, int device) {
     return static_cast<int *>(ptr_or_null(o, "dev_status", at::kInt, {1}, device));
 }
@@ -212,12 +223,17 @@ PyObject *window_decode(PyObject *, Args a, Py_ssize_t n) {
         const int64_t S = t.q_shape[0], MB = dims(tensor(a[4], "block_tables"), "block_tables", 2)[1];
         void *tables = ptr(a[4], "block_tables", at::kInt, {S, MB}, t.device);
         void *ctx = ptr(a[5], "context_lens", at::kInt, {S}, t.device);
+        const int max_blocks = size_arg(MB, "block_tables"), seqs = size_arg(S, "q");
+        const int window = int_arg(a[6], "window"), sinks = int_arg(a[7], "num_sinks");
+        const float scale = t.scale(a[8]);
+        const int type = dtype_code(t.type, "q"), out_type = dtype_code(t.out_type, "out");
+        int *status = status_arg(a[9], t.device);
+        void *stream = stream_arg(a[10], t.device);
+        OtherThreads run;
         c10::cuda::OptionalCUDAGuard guard(c10::Device(c10::kCUDA, (c10::DeviceIndex)t.device));
-        return pkv_paged_window_decode_attention(
-            t.out, t.q, t.k, t.v, static_cast<int32_t *>(tables), size_arg(MB, "block_tables"), static_cast<int32_t *>(ctx),
-            size_arg(S, "q"), t.NB, t.Hq, t.Hkv, t.d, t.bs, int_arg(a[6], "window"), int_arg(a[7], "num_sinks"),
-            t.scale(a[8]), dtype_code(t.type, "q"), dtype_code(t.out_type, "out"), status_arg(a[9], t.device),
-            stream_arg(a[10], t.device));
+        return pkv_paged_window_decode_attention(t.out, t.q, t.k, t.v, static_cast<int32_t *>(tables), max_blocks,
+                                                 static_cast<int32_t *>(ctx), seqs, t.NB, t.Hq, t.Hkv, t.d, t.bs, window,
+                                                 sinks, scale, type, out_type, status, stream);
     });
 }
 
@@ -230,13 +246,19 @@ PyObject *window_prefill(PyObject *, Args a, Py_ssize_t n) {
         void *cu = ptr(a[2], "cu_seqlens", at::kInt, {S + 1}, t.device);
         void *tables = ptr(a[6], "block_tables", at::kInt, {S, MB}, t.device);
         void *ctx = ptr(a[7], "context_lens", at::kInt, {S}, t.device);
+        const int max_blocks = size_arg(MB, "block_tables"), seqs = size_arg(S, "block_tables");
+        const int max_q = int_arg(a[3], "max_q_len"), total_q = size_arg(t.q_shape[0], "q");
+        const int window = int_arg(a[8], "window"), sinks = int_arg(a[9], "num_sinks");
+        const float scale = t.scale(a[10]);
+        const int type = dtype_code(t.type, "q"), out_type = dtype_code(t.out_type, "out");
+        int *status = status_arg(a[11], t.device);
+        void *stream = stream_arg(a[12], t.device);
+        OtherThreads run;
         c10::cuda::OptionalCUDAGuard guard(c10::Device(c10::kCUDA, (c10::DeviceIndex)t.device));
-        return pkv_paged_window_prefill_attention(
-            t.out, t.q, static_cast<int32_t *>(cu), size_arg(S, "block_tables"), int_arg(a[3], "max_q_len"),
-            size_arg(t.q_shape[0], "q"), t.k, t.v, static_cast<int32_t *>(tables), size_arg(MB, "block_tables"),
-            static_cast<int32_t *>(ctx), t.NB, t.Hq, t.Hkv, t.d, t.bs, int_arg(a[8], "window"), int_arg(a[9], "num_sinks"),
-            t.scale(a[10]), dtype_code(t.type, "q"), dtype_code(t.out_type, "out"), status_arg(a[11], t.device),
-            stream_arg(a[12], t.device));
+        return pkv_paged_window_prefill_attention(t.out, t.q, static_cast<int32_t *>(cu), seqs, max_q, total_q, t.k, t.v,
+                                                  static_cast<int32_t *>(tables), max_blocks, static_cast<int32_t *>(ctx),
+                                                  t.NB, t.Hq, t.Hkv, t.d, t.bs, window, sinks, scale, type, out_type,
+                                                  status, stream);
     });
 }
 
@@ -246,7 +268,10 @@ struct Rotation {
     int64_t T, Hq, Hkv, d, pairs;
     at::ScalarType type, weight_type = at::kFloat;
     Rows q, k, q_out;
-    void *positions, *freqs, *q_weight, *k_weight;
+    const int32_t *positions;
+    const int64_t *freqs;
+    void *q_weight, *k_weight;
+    int T_arg, Hq_arg, Hkv_arg, d_arg, rotary_dim, code, weight_code;   // as the C entry points take them
     Rotation(PyObject *o_q_out, PyObject *o_q, PyObject *o_k, PyObject *o_pos, PyObject *o_freqs, PyObject *o_wq,
              PyObject *o_wk) {
         const at::Tensor &tq = tensor(o_q, "q"), &tf = tensor(o_freqs, "freqs");
@@ -259,12 +284,15 @@ struct Rotation {
         q = rows(o_q, "q", type, {T, Hq, d}, device);
         k = rows(o_k, "k", type, {T, Hkv, d}, device);
         q_out = rows(o_q_out, "q_out", type, {T, Hq, d}, device);
-        positions = ptr(o_pos, "positions", at::kInt, {T}, device);
-        freqs = ptr(o_freqs, "freqs", at::kLong, {pairs}, device);
+        positions = static_cast<int32_t *>(ptr(o_pos, "positions", at::kInt, {T}, device));
+        freqs = static_cast<int64_t *>(ptr(o_freqs, "freqs", at::kLong, {pairs}, device));
         if (o_wq != Py_None || o_wk != Py_None)
             weight_type = tensor(o_wq != Py_None ? o_wq : o_wk, "the weights").scalar_type();
         q_weight = ptr_or_null(o_wq, "q_weight", weight_type, {d}, device);
         k_weight = ptr_or_null(o_wk, "k_weight", weight_type, {d}, device);
+        T_arg = size_arg(T, "q"), Hq_arg = size_arg(Hq, "q"), Hkv_arg = size_arg(Hkv, "k"), d_arg = size_arg(d, "q");
+        rotary_dim = size_arg(2 * pairs, "freqs");
+        code = dtype_code(type, "q"), weight_code = dtype_code(weight_type, "the weights");
     }
 };
 
@@ -273,13 +301,14 @@ PyObject *qk_rope(PyObject *, Args a, Py_ssize_t n) {
     return guarded("qk_rope", n, 12, [&] {
         const Rotation t(a[0], a[2], a[3], a[4], a[5], a[8], a[9]);
         const Rows k_out = rows(a[1], "k_out", t.type, {t.T, t.Hkv, t.d}, t.device);
+        const bool interleaved = bool_arg(a[6]);
+        const float mscale = float_arg(a[7]), eps = float_arg(a[10]);
+        void *stream = stream_arg(a[11], t.device);
+        OtherThreads run;
         c10::cuda::OptionalCUDAGuard guard(c10::Device(c10::kCUDA, (c10::DeviceIndex)t.device));
         return pkv_qk_rope(t.q_out.p, t.q_out.stride, k_out.p, k_out.stride, t.q.p, t.q.stride, t.k.p, t.k.stride,
-                           static_cast<int32_t *>(t.positions), static_cast<int64_t *>(t.freqs),
-                           size_arg(2 * t.pairs, "freqs"), bool_arg(a[6]), float_arg(a[7]), t.q_weight, t.k_weight,
-                           dtype_code(t.weight_type, "the weights"), float_arg(a[10]), size_arg(t.T, "q"),
-                           size_arg(t.Hq, "q"), size_arg(t.Hkv, "k"), size_arg(t.d, "q"), dtype_code(t.type, "q"),
-                           stream_arg(a[11], t.device));
+                           t.positions, t.freqs, t.rotary_dim, interleaved, mscale, t.q_weight, t.k_weight, t.weight_code,
+                           eps, t.T_arg, t.Hq_arg, t.Hkv_arg, t.d_arg, t.code, stream);
     });
 }
 
@@ -294,14 +323,17 @@ PyObject *qk_rope_append(PyObject *, Args a, Py_ssize_t n) {
         const int64_t NB = cs[0], bs = cs[2];
         void *kc = ptr(a[7], "k_cache", t.type, {NB, t.Hkv, bs, t.d}, t.device);
         void *vc = ptr(a[8], "v_cache", t.type, {NB, t.Hkv, bs, t.d}, t.device);
+        const bool interleaved = bool_arg(a[9]);
+        const float mscale = float_arg(a[10]), eps = float_arg(a[13]);
+        const int blocks = size_arg(NB, "k_cache"), block_size = size_arg(bs, "k_cache");
+        int *status = status_arg(a[14], t.device);
+        void *stream = stream_arg(a[15], t.device);
+        OtherThreads run;
         c10::cuda::OptionalCUDAGuard guard(c10::Device(c10::kCUDA, (c10::DeviceIndex)t.device));
-        return pkv_qk_rope_append(t.q_out.p, t.q_out.stride, t.q.p, t.q.stride, t.k.p, t.k.stride, v.p, v.stride,
-                                  static_cast<int32_t *>(t.positions), static_cast<int64_t *>(slots),
-                                  static_cast<int64_t *>(t.freqs), size_arg(2 * t.pairs, "freqs"), bool_arg(a[9]),
-                                  float_arg(a[10]), t.q_weight, t.k_weight, dtype_code(t.weight_type, "the weights"),
-                                  float_arg(a[13]), size_arg(t.T, "q"), kc, vc, size_arg(NB, "k_cache"),
-                                  size_arg(bs, "k_cache"), size_arg(t.Hq, "q"), size_arg(t.Hkv, "k"), size_arg(t.d, "q"),
-                                  dtype_code(t.type, "q"), status_arg(a[14], t.device), stream_arg(a[15], t.device));
+        return pkv_qk_rope_append(t.q_out.p, t.q_out.stride, t.q.p, t.q.stride, t.k.p, t.k.stride, v.p, v.stride, t.positions,
+                                  static_cast<int64_t *>(slots), t.freqs, t.rotary_dim, interleaved, mscale, t.q_weight,
+                                  t.k_weight, t.weight_code, eps, t.T_arg, kc, vc, blocks, block_size, t.Hq_arg, t.Hkv_arg,
+                                  t.d_arg, t.code, status, stream);
     });
 }
 
@@ -323,10 +355,15 @@ PyObject *step_tables(PyObject *, Args a, Py_ssize_t n) {
         int32_t *list = i32(3, "free_list", {capacity}), *ctx = i32(6, "context_lens", {S}), *cu = i32(7, "cu_seqlens", {S + 1});
         int64_t *slots = static_cast<int64_t *>(ptr(a[8], "slot_mapping", at::kLong, {T}, dev));
         int32_t *pos = i32(9, "token_pos", {T});
+        const int seqs = size_arg(S, "block_tables"), max_blocks = size_arg(MB, "block_tables");
+        const int room = size_arg(capacity, "free_list"), tokens = size_arg(T, "slot_mapping");
+        const int blocks = int_arg(a[5], "num_blocks");
+        int *status = status_arg(a[11], dev);
+        void *stream = stream_arg(a[12], dev);
+        OtherThreads run;
         c10::cuda::OptionalCUDAGuard guard(c10::Device(c10::kCUDA, (c10::DeviceIndex)dev));
-        return pkv_step_tables(lens, fresh, size_arg(S, "block_tables"), tables, size_arg(MB, "block_tables"), list,
-                               size_arg(capacity, "free_list"), count, count_out, int_arg(a[5], "num_blocks"), 16, ctx, cu,
-                               slots, pos, size_arg(T, "slot_mapping"), status_arg(a[11], dev), stream_arg(a[12], dev));
+        return pkv_step_tables(lens, fresh, seqs, tables, max_blocks, list, room, count, count_out, blocks, 16, ctx, cu, slots,
+                               pos, tokens, status, stream);
     });
 }
 
@@ -349,15 +386,19 @@ PyObject *release_blocks(PyObject *, Args a, Py_ssize_t n) {
             nwork = (size_t)tensor(a[8], "workspace").numel();
             work = ptr(a[8], "workspace", at::kByte, {(int64_t)nwork}, dev);
         }
-        c10::cuda::OptionalCUDAGuard guard(c10::Device(c10::kCUDA, (c10::DeviceIndex)dev));
+        const int seqs = size_arg(S, "block_tables"), max_blocks = size_arg(MB, "block_tables");
+        const int room = size_arg(capacity, "free_list"), blocks = int_arg(a[4], "num_blocks");
+        const int window = int_arg(a[6], "window"), sinks = int_arg(a[7], "num_sinks");
+        int *status = status_arg(a[9], dev);
         void *stream = stream_arg(a[10], dev);
+        const bool take = a[8] == Py_None;
+        OtherThreads run;
+        c10::cuda::OptionalCUDAGuard guard(c10::Device(c10::kCUDA, (c10::DeviceIndex)dev));
         // without a workspace of the caller's: memory of the stream that the call runs on
         StreamMemory own;
-        if (a[8] == Py_None && (nwork = pkv_release_workspace_size(size_arg(S, "block_tables"))) > 0)
-            work = own.get(nwork, stream);
-        return pkv_release_blocks(tables, size_arg(MB, "block_tables"), lens, finished, size_arg(S, "block_tables"),
-                                  int_arg(a[6], "window"), int_arg(a[7], "num_sinks"), list, size_arg(capacity, "free_list"),
-                                  count, int_arg(a[4], "num_blocks"), 16, work, nwork, status_arg(a[9], dev), stream);
+        if (take && (nwork = pkv_release_workspace_size(seqs)) > 0) work = own.get(nwork, stream);
+        return pkv_release_blocks(tables, max_blocks, lens, finished, seqs, window, sinks, list, room, count, blocks, 16, work,
+                                  nwork, status, stream);
     });
 }
 
