@@ -178,9 +178,10 @@ size_t pkv_decode_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads
  * before it waits for the work enqueued ahead of the call.  By then that work
  * has ended, or has signalled its dependents through programmatic dependent
  * launch.  So context_lens must not be written by a kernel just before the
- * call that signals its dependents before that write (the library's own
- * kernels never write it).  Everything else is read and written only after
- * the wait.
+ * call that signals its dependents before that write (of the library's own
+ * kernels only pkv_step_tables' writes it, and it signals nothing: a call
+ * straight behind it starts when it has ended).  Everything else is read and
+ * written only after the wait.
  * One persistent kernel: every warp starts on an equal share of the
  * (sequence, KV head, block) list, and warps that finish early take over the
  * far half of busier warps' unclaimed blocks.  A (sequence, KV head) range

@@ -9,7 +9,8 @@ import torch
 
 import window_ref as ref
 from paged_kv_cache_tables_gb300 import _binding as B
-from test_gpu_window import F16, F32, Step
+from paged_kv_cache_tables_gb300 import paged_decode_attention, step_tables
+from test_gpu_window import BF16, F16, F32, Step
 
 pytestmark = pytest.mark.gpu
 
@@ -23,6 +24,56 @@ def test_a_chunk_longer_than_max_q_len_is_skipped_and_reported(cuda_lib, rows, m
     got = st.prefill(out_dtype, max_q=max_q)
     assert torch.isnan(got[:rows]).all() and st.status.item() == B.DEV_BAD_CHUNK
     ref.assert_within(got[rows:], want[rows:], bound[rows:])
+
+
+@pytest.mark.parametrize("S", [3, 200, 300])
+def test_step_tables_straight_before_decode_attention(cuda_lib, S):
+    """Plain decode reads context_lens to plan before it waits for the work ahead of it: here the launch that writes them,
+    in place, every step another length, captured and replayed."""
+    MB, NB = 12, S * 12
+    g = torch.Generator().manual_seed(S)
+    k = torch.randn(NB, 2, 16, 64, generator=g).to(BF16).cuda()
+    v = torch.randn(NB, 2, 16, 64, generator=g).to(BF16).cuda()
+    q = torch.randn(S, 4, 64, generator=g).to(BF16)
+    lens = [(7 * s) % 60 for s in range(S)]
+    table = [list(range(s * 12, s * 12 + -(-n // 16))) + [-1] * (MB - -(-n // 16)) for s, n in enumerate(lens)]
+    held = {b for r in table for b in r}
+    free = [b for b in torch.randperm(NB, generator=g).tolist() if b not in held]
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")   # noqa: E731
+    d_lens, d_table, d_free, d_count = i32(lens), i32(table), i32(free), i32([len(free)])
+    new = i32([1 + s % 2 for s in range(S)])
+    T = int(new.sum())
+    cu, pos, status = i32([0] * (S + 1)), i32([0] * T), i32([0])
+    slots = torch.zeros(T, dtype=torch.int64, device="cuda")
+    steps = 40
+    out = torch.full((steps, S, 4, 64), float("nan"), device="cuda")
+    now = torch.zeros(S, 4, 64, device="cuda")
+    dq = q.cuda()
+    work = torch.empty(B.decode_workspace_size(S, 4, 2, 64), dtype=torch.uint8, device="cuda")
+
+    def step():
+        step_tables(d_lens, new, d_table, d_free, d_count, NB, d_lens, cu, slots, pos, dev_status=status)
+        paged_decode_attention(now, dq, k, v, d_table, d_lens, workspace=work, dev_status=status)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    for i in range(steps):
+        graph.replay() if i % 2 else step()
+        out[i] = now
+    count, fresh = len(free), new.tolist()
+    for i in range(steps):
+        table, count, lens, _, _, _ = ref.step_tables(lens, fresh, table, free, count, T)
+        if i % 13 and i != steps - 1:
+            continue
+        for s in range(0, S, 1 + S // 60):
+            keys, values = ref.gathered(k, torch.tensor(table[s]), lens[s]), ref.gathered(v, torch.tensor(table[s]), lens[s])
+            want, spread, mass = ref.attend(q[s:s + 1].double(), lens[s] - 1, keys, values, 10 ** 6, 0, 0.125)
+            ref.assert_within(out[i, s:s + 1], want, ref.attention_bound(want, spread, mass, 64, 0.125, F32), (i, s))
+    assert status.item() == 0 and d_lens.tolist() == lens and d_table.tolist() == table
 
 
 FAKE = """
