@@ -2,7 +2,8 @@
 
 Each translation unit compiles in its own process (in parallel), then nvcc
 links the shared library and g++ the Python module that calls it with torch
-tensors (against the installed torch's headers and libraries).  The CUDA runtime is linked statically; the
+tensors (against the installed torch's headers and libraries; without a torch
+the library is built alone).  The CUDA runtime is linked statically; the
 driver's tensor-map encoder is looked up at run time, so the library loads
 on a machine without a GPU (the host scheduler works there).
 """
@@ -63,6 +64,20 @@ def _torch_dir() -> str:
     return list(spec.submodule_search_locations)[0]
 
 
+def _torch_built_for():
+    """What _torch_calls.so is made for: the Python and the torch that import it.  None without a torch."""
+    try:
+        torch = _torch_dir()
+    except RuntimeError:
+        return None
+    text = "%s\n%s\n" % (sysconfig.get_config_var("SOABI"), torch)
+    version = os.path.join(torch, "version.py")
+    if os.path.exists(version):
+        with open(version) as f:
+            text += f.read()
+    return text
+
+
 def _run(what: str, cmd) -> None:
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
@@ -86,22 +101,39 @@ def _link_calls(obj: str) -> None:
     os.replace(tmp, CALLS)
 
 
-def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    if not force and all(os.path.exists(p) and os.path.getmtime(p) >= _inputs_mtime() for p in (LIB, CALLS)):
-        return LIB
-    os.makedirs(BUILD, exist_ok=True)
-    srcs = [s for s in SOURCES if os.path.exists(os.path.join(CSRC, s))]
-    with cf.ThreadPoolExecutor(max_workers=len(srcs) + 1) as ex:
-        calls = ex.submit(_compile_calls)
-        objs = list(ex.map(lambda s: _compile(s, verbose_ptxas), srcs))
-        calls_obj = calls.result()
+def _link(objs) -> None:
     tmp = LIB + ".tmp.%d" % os.getpid()
     cmd = [nvcc()] + ARCH + ["-shared", "-o", tmp] + objs + ["-lcudart_static", "-lrt", "-ldl", "-lpthread"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError("link failed:\n%s\n%s" % (" ".join(cmd), res.stderr))
     os.replace(tmp, LIB)
-    _link_calls(calls_obj)
+
+
+def build(force: bool = False, verbose_ptxas: bool = False) -> str:
+    """libpkv.so where it is older than its sources; then _torch_calls.so where it is, or was made for another torch or
+    Python.  libpkv.so needs no torch: without one it is built alone (the calls of _torch_calls.so say what is missing),
+    and where _torch_calls.so cannot be made it is in its place before the error is raised."""
+    newest = _inputs_mtime()
+    fresh = lambda p: not force and os.path.exists(p) and os.path.getmtime(p) >= newest   # noqa: E731
+    made_for, wanted = os.path.join(BUILD, "torch_calls.for"), _torch_built_for()
+    lib_fresh, calls_fresh = fresh(LIB), wanted is None
+    if fresh(CALLS) and os.path.exists(made_for):
+        with open(made_for) as f:
+            calls_fresh = calls_fresh or f.read() == wanted
+    if lib_fresh and calls_fresh:
+        return LIB
+    os.makedirs(BUILD, exist_ok=True)
+    srcs = [] if lib_fresh else [s for s in SOURCES if os.path.exists(os.path.join(CSRC, s))]
+    with cf.ThreadPoolExecutor(max_workers=len(srcs) + 1) as ex:
+        calls = None if calls_fresh else ex.submit(_compile_calls)
+        objs = list(ex.map(lambda s: _compile(s, verbose_ptxas), srcs))
+    if objs:
+        _link(objs)
+    if calls is not None:
+        _link_calls(calls.result())
+        with open(made_for, "w") as f:
+            f.write(wanted)
     return LIB
 
 
