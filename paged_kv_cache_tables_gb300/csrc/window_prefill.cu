@@ -98,7 +98,6 @@ struct WindowPrefillParams {
     int rtok, units_per_seq;
     int window, sinks, total_q, max_q_len;
     float scale_log2;
-    int out_dtype;
     bool boxes;   // a warp's 32 rows are whole tokens: tout has a box for them
 };
 
@@ -814,7 +813,6 @@ extern "C" int pkv_paged_window_prefill_attention(void *out, const void *q, cons
     prm.total_q = total_q;
     prm.max_q_len = max_q_len;
     prm.scale_log2 = scale * 1.4426950408889634f;
-    prm.out_dtype = out_dtype;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     auto launch = [&](auto type, auto wide, auto tiles) {
         using T = decltype(type);
