@@ -392,11 +392,14 @@ int pkv_paged_decode_attention_static(void *out, const void *q, const void *k_ca
  * Arguments as there, without a workspace; scale must be positive, out and q
  * 16-B aligned.  One launch; a range's parts meet in shared memory (of a
  * thread-block cluster where a range has several CTAs), in an order fixed by
- * the context lengths, so equal inputs give equal bits.  Hidden positions of a block that is read may hold
- * anything (NaN, infinity) in K and V.  context_lens is read after the wait
- * for the work enqueued before the call.  Further limits: num_seqs *
- * num_kv_heads * 16 and num_seqs * max_blocks_per_seq below 2^31,
- * max_blocks_per_seq <= 2^26 (PKV_ERR_UNSUPPORTED).
+ * the call's sizes and the context lengths: equal calls give equal bits.  The
+ * sizes choose how a range is split, so a sequence's last bits may change with
+ * num_seqs, the head counts, max_blocks_per_seq, window, num_sinks and the
+ * device's SM count.  Hidden positions of a block that is read may hold anything
+ * (NaN, infinity) in K and V.  context_lens is read after the wait for the
+ * work enqueued before the call.  Further limits: num_seqs * num_kv_heads * 16
+ * and num_seqs * max_blocks_per_seq below 2^31, max_blocks_per_seq <= 2^26
+ * (PKV_ERR_UNSUPPORTED).
  */
 int pkv_paged_window_decode_attention(void *out, const void *q, const void *k_cache, const void *v_cache,
                                       const int32_t *block_tables, int max_blocks_per_seq,

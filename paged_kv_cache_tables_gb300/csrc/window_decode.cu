@@ -24,7 +24,7 @@
 // with the query heads of the group as one (padded) row tile.  The warps'
 // parts meet in shared memory, the CTAs' parts through distributed shared
 // memory, so there is no workspace, no second launch, and the order of every
-// sum is fixed by the lengths alone.
+// sum is fixed by the call's sizes (which choose the split) and the lengths.
 //
 // What bounds it: HBM.  256 sequences x 8 KV heads, window 1,024 (597 MB of
 // visible K and V): 90.6 us, 97 % of the measured copy rate; 16 x 8, window
