@@ -451,7 +451,8 @@ int pkv_paged_window_prefill_attention(void *out, const void *q, const int32_t *
 
 /*
  * Fills freqs (HOST array, rotary_dim / 2 entries) with the frequencies as
- * turns per position in 64-bit fixed point, round(f_i / 2 pi * 2^64), and
+ * turns per position in 64-bit fixed point, round(f_i / 2 pi * 2^64), f_i
+ * computed in double (an error below 2^-52 turns; about 2^-55 measured), and
  * *mscale with the factor on cos and sin.  The caller keeps them on the device
  * for the calls below.  base > 1; factor >= 1 (not read by PLAIN);
  * original_context > 0 and 0 < low < high (read by BANDS and YARN).
@@ -467,8 +468,10 @@ int pkv_rope_frequencies(int64_t *freqs, float *mscale, int rotary_dim, double b
  *     (y_i, y_j) -> mscale * (y_i cos a - y_j sin a, y_i sin a + y_j cos a),
  *     a = positions[token] * f_k, for the pairs k of the first rotary_dim
  *     dimensions: (2k, 2k + 1) when interleaved, else (k, k + rotary_dim / 2);
- * the other dimensions stay y.  Computed in fp32 from the 16-bit input, the
- * angle exactly modulo a turn at any int32 position, rounded once at the store.
+ * the other dimensions stay y.  Computed in fp32 from the 16-bit input,
+ * rounded once at the store.  positions[token] * freqs[k] is taken exactly modulo
+ * a turn at any int32 position, so the angle is off by the position times the
+ * frequency's own error (see pkv_rope_frequencies) and fp32's rounding of it.
  *   q, k          device, num_tokens rows of num_q_heads / num_kv_heads heads
  *                 of head_dim contiguous elements; q_stride / k_stride
  *                 elements from a token to the next, multiples of 8 (slices of

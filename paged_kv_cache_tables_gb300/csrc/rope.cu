@@ -14,8 +14,8 @@
 // The angle.  p * f in fp32 loses whole radians at far positions, and fp64 is
 // slow here.  A frequency is kept as a fraction of a turn in 64-bit fixed
 // point, F = round(f / 2 pi * 2^64): p * F modulo 2^64 is p turns of it with
-// the whole turns gone and an error of p * 2^-65 turns, from integer
-// multiplies alone.  Its top 32 bits, as a signed number of half turns, go to
+// the whole turns gone, exactly, from integer multiplies alone; what is left is p
+// times F's own error, that of f in double (below 2^-52 turns, 2^-55 measured).  Its top 32 bits, as a signed number of half turns, go to
 // sincospif, which needs no reduction.
 //
 // What bounds it: HBM, each row read and written once, if the instructions per
