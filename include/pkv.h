@@ -452,7 +452,8 @@ int pkv_paged_window_prefill_attention(void *out, const void *q, const int32_t *
 /*
  * Fills freqs (HOST array, rotary_dim / 2 entries) with the frequencies as
  * turns per position in 64-bit fixed point, round(f_i / 2 pi * 2^64), f_i
- * computed in double (an error below 2^-52 turns; about 2^-55 measured), and
+ * computed in double (an error below 2^-52 turns, about 2^-55 measured; BANDS
+ * with low close to high: high / (high - low) times that), and
  * *mscale with the factor on cos and sin.  The caller keeps them on the device
  * for the calls below.  base > 1; factor >= 1 (not read by PLAIN);
  * original_context > 0 and 0 < low < high (read by BANDS and YARN).

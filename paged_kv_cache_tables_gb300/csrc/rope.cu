@@ -15,8 +15,9 @@
 // slow here.  A frequency is kept as a fraction of a turn in 64-bit fixed
 // point, F = round(f / 2 pi * 2^64): p * F modulo 2^64 is p turns of it with
 // the whole turns gone, exactly, from integer multiplies alone; what is left is p
-// times F's own error, that of f in double (below 2^-52 turns, 2^-55 measured).  Its top 32 bits, as a signed number of half turns, go to
-// sincospif, which needs no reduction.
+// times F's own error, that of f in double (below 2^-52 turns, 2^-55 measured).
+// The product's top 32 bits, as a signed number of half turns, go to sincospif,
+// which needs no reduction.
 //
 // What bounds it: HBM, each row read and written once, if the instructions per
 // byte stay few and enough bytes are on their way.  A row is head_dim / 16
