@@ -9,8 +9,10 @@ import torch
 
 import window_ref as ref
 from paged_kv_cache_tables_gb300 import _binding as B
-from paged_kv_cache_tables_gb300 import paged_decode_attention, step_tables
+from paged_kv_cache_tables_gb300 import (paged_decode_attention, paged_window_decode_attention,
+                                         paged_window_prefill_attention, step_tables)
 from test_gpu_window import BF16, F16, F32, Step
+from test_gpu_window_step import SINKS, WINDOW, Loop
 
 pytestmark = pytest.mark.gpu
 
@@ -74,6 +76,28 @@ def test_step_tables_straight_before_decode_attention(cuda_lib, S):
             want, spread, mass = ref.attend(q[s:s + 1].double(), lens[s] - 1, keys, values, 10 ** 6, 0, 0.125)
             ref.assert_within(out[i, s:s + 1], want, ref.attention_bound(want, spread, mass, 64, 0.125, F32), (i, s))
     assert status.item() == 0 and d_lens.tolist() == lens and d_table.tolist() == table
+
+
+@pytest.mark.parametrize("d,dtype", [(64, BF16), (128, F16)])
+def test_a_step_of_chunks_and_decodes(cuda_lib, d, dtype):
+    """One batch, its tables built once: the first P sequences are chunks, the others decode a token each, on slices of the
+    step's arrays."""
+    loop = Loop(6, 8, 2, d, dtype, max_blocks=16, pool=60, capacity=200, chunk=60)
+    idle = [0] * 6
+    loop.fill([1, 30, 0, 17, 16, 48], idle)
+    loop.prefill()
+    loop.verify([1, 30, 0, 17, 16, 48], idle, 112)
+    for P, chunks in ((3, [60, 5, 33]), (1, [59]), (5, [1, 2, 17, 1, 40])):
+        new, Tp = chunks + [1] * (6 - P), sum(chunks)
+        T = Tp + 6 - P
+        loop.fill(new, idle)
+        loop.front()
+        paged_window_prefill_attention(loop.out[:Tp], loop.q_out[:Tp], loop.cu[:P + 1], 60, loop.kc, loop.vc, loop.table[:P],
+                                       loop.lens[:P], WINDOW, num_sinks=SINKS, dev_status=loop.status)
+        paged_window_decode_attention(loop.out[Tp:T], loop.q_out[Tp:T], loop.kc, loop.vc, loop.table[P:], loop.lens[P:], WINDOW,
+                                      num_sinks=SINKS, dev_status=loop.status)
+        loop.back()
+        loop.verify(new, idle, T)
 
 
 FAKE = """
