@@ -295,10 +295,11 @@ __device__ __forceinline__ void release_range(const ReleaseParams &p, int s, int
 // exchanges the CTAs' totals through distributed shared memory and moves the
 // blocks.  More rows are two launches over the whole GPU: one counts into the
 // workspace, the other sums the counts of the rows before its own (each CTA reads
-// them all, out of L2) and moves.  4,000 rows of up to 2,048 blocks take 11.6 us
-// so, and took 49 us in one cluster of 16 CTAs of 1,024 threads; 256 rows of up to
-// 512 take 5.2 us in one launch; two, 0.6 us less, cost the host another 7 us (a
-// launch, and the workspace).  Loads under way in a warp: few rows want the chain
+// them all, out of L2) and moves.  4,000 rows of up to 2,048 blocks take 11.9 us
+// so, and took 49 us in one cluster of 16 CTAs of 1,024 threads.  Up to 256 rows,
+// in one launch and in two: 256 rows of up to 512 blocks 5.2 and 4.7 us, 64 of them
+// 3.7 and 3.6, 256 of up to 2,048 8.2 and 8.6, 64 of them 6.8 and 7.5; and 2.2 us of
+// host time a call instead of 4.1 (a launch, and the workspace).  Loads under way in a warp: few rows want the chain
 // of a long row short, many rows want registers for more warps (256 rows of up to
 // 2,048 blocks: 10.1 us with four and 11.5 with two, 4,000 of up to 333 13.4 and
 // 12.3, a copy of the table and the list included).
