@@ -10,10 +10,12 @@
 // and belongs to the last s with bx_s <= k; token t of the step belongs to the
 // last s with cu_s <= t and sits at position len_s + t - cu_s.
 //
-// What bounds it: latency.  The step of 4,020 sequences and 127,780 rows
-// writes 1.6 MB, 0.24 us at the measured copy rate; the launch, the reads of
-// the lengths, the scan and the reads of ids are a chain of round trips, 2.9 us
-// for 256 sequences and 8.2 us for those 4,020.
+// What bounds it: of few sequences latency, the launch, the reads of the lengths,
+// the scan and the reads of ids being a chain of round trips, 2.9 us for 256
+// sequences.  The step of 4,020 sequences and 127,780 rows writes 1.6 MB, 0.24 us
+// at the measured copy rate, and takes 8.2 us: the launch of 16 CTAs 1.0, the scan
+// of all lengths, repeated in each of them, 3.5, two rounds of bisection, ids and
+// stores 3.7.
 // So everything is one launch without a workspace: a small step is one CTA;
 // a larger one is one cluster of CTAs, each of which scans all lengths itself
 // (at most 16,384 of them, out of L2) and fills its share of the outputs, its
@@ -290,7 +292,9 @@ __device__ __forceinline__ void release_range(const ReleaseParams &p, int s, int
 }
 
 // A warp a row, 128 neighbouring entries a load; the blocks go on the list in the
-// order of the rows and of the blocks within a row.  Two forms.  Up to
+// order of the rows and of the blocks within a row.  A running row is walked from
+// its first tokens' blocks on in every call, through the entries given back before.
+// Two forms.  Up to
 // kRelSmallRows rows are one launch: a cluster of CTAs counts its rows' blocks,
 // exchanges the CTAs' totals through distributed shared memory and moves the
 // blocks.  More rows are two launches over the whole GPU: one counts into the
