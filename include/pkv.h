@@ -427,6 +427,85 @@ int pkv_paged_window_prefill_attention(void *out, const void *q, const int32_t *
                                        int head_dim, int block_size, int window, int num_sinks, float scale, int dtype,
                                        int out_dtype, int *dev_status, void *stream);
 
+/* ---- the cache held in 8 bits -----------------------------------------------------
+ * The caches above in half the bytes: k_cache and v_cache hold e4m3 codes (one
+ * byte an element, the layout above), and
+ *   kv_scales      device float [num_blocks][num_kv_heads][2], 8-B aligned: the
+ *                  scale of a (block, KV head)'s K tile, then of its V tile
+ * A value is its code times its tile's scale.  The pages describe no such cache;
+ * it is how a serving engine holds twice the context in the same HBM.
+ * pkv_copy_blocks moves such caches as it does others, and kv_scales too (blocks
+ * of 8 * num_kv_heads bytes, where that is a multiple of 16).
+ */
+
+/*
+ * pkv_kv_append_e4m3 -- pkv_kv_append into a cache held in 8 bits.
+ *   k, v          device, num_tokens rows of num_kv_heads heads of head_dim
+ *                 contiguous elements of dtype; k_stride / v_stride elements
+ *                 from a token to the next, multiples of 8 (slices of a fused
+ *                 projection's rows); 16-B aligned
+ * For each (block, KV head) tile of K, and of V, that the call writes rows to,
+ * let a be the largest finite magnitude among those rows and r(a) the least
+ * power of two, at least 2^-60, with a <= 448 r(a).  Its scale s becomes
+ *     s' = r(a) where the call writes offset 0 of the block (the block starts
+ *     anew: what it held is gone), else max(s, r(a));
+ * each row is stored as the codes next to x / s' (ties to even; infinities as
+ * +-448, NaN as NaN), and where s' > s the block's other rows as those next to
+ * their code times s / s' (exact, short of e4m3's subnormals).  A scale s that is
+ * not above 0 counts as 0.
+ * The rows of one block must stand next to one another in the call, as the
+ * scheduler and pkv_step_tables lay a step out, and slots must be unique: else
+ * what that block holds afterwards is not specified.  slot_mapping, padding
+ * rows and slots outside the pool as in pkv_kv_append.  num_tokens *
+ * num_kv_heads < 2^30 (PKV_ERR_UNSUPPORTED).  One launch.
+ */
+int pkv_kv_append_e4m3(const void *k, int64_t k_stride, const void *v, int64_t v_stride, const int64_t *slot_mapping,
+                       int num_tokens, void *k_cache, void *v_cache, float *kv_scales, int num_blocks, int block_size,
+                       int num_kv_heads, int head_dim, int dtype, int *dev_status, void *stream);
+
+/*
+ * pkv_kv_gather_e4m3 -- reads rows of sequences back from a cache held in 8
+ * bits: for a dense computation over them, or to hand them over.
+ *   k, v          device, [total][num_kv_heads][head_dim] of out_dtype (F16,
+ *                 BF16 or F32), 16-B aligned
+ *   cu_seqlens    device int32 [num_seqs + 1], cu[0] = 0, non-decreasing: row
+ *                 cu[s] + i receives position first[s] + i of sequence s, its
+ *                 codes times their scale, rounded once
+ *   first         device int32 [num_seqs], or NULL: 0 for all
+ * Rows from cu[num_seqs] on are left as they were.  A position outside the table
+ * (PKV_DEV_BAD_CONTEXT) or a block id outside the pool (PKV_DEV_BAD_BLOCK_ID)
+ * gives zeros.
+ */
+int pkv_kv_gather_e4m3(void *k, void *v, const void *k_cache, const void *v_cache, const float *kv_scales,
+                       const int32_t *block_tables, int max_blocks_per_seq, const int32_t *cu_seqlens,
+                       const int32_t *first, int num_seqs, int total, int num_blocks, int block_size, int num_kv_heads,
+                       int head_dim, int out_dtype, int *dev_status, void *stream);
+
+/*
+ * pkv_paged_decode_attention_e4m3 -- pkv_paged_window_decode_attention over a
+ * cache held in 8 bits; a window of at least max_blocks_per_seq * block_size is
+ * the whole context.  Arguments, limits and guarantees as there.  kv_scales of
+ * blocks that are read must be positive and finite (any such value will do, not
+ * just powers of two).  A block id outside the pool reads zeros.
+ */
+int pkv_paged_decode_attention_e4m3(void *out, const void *q, const void *k_cache, const void *v_cache,
+                                    const float *kv_scales, const int32_t *block_tables, int max_blocks_per_seq,
+                                    const int32_t *context_lens, int num_seqs, int num_blocks, int num_q_heads,
+                                    int num_kv_heads, int head_dim, int block_size, int window, int num_sinks, float scale,
+                                    int dtype, int out_dtype, int *dev_status, void *stream);
+
+/*
+ * pkv_paged_prefill_attention_e4m3 -- pkv_paged_window_prefill_attention over a
+ * cache held in 8 bits, with the window and kv_scales of
+ * pkv_paged_decode_attention_e4m3.
+ */
+int pkv_paged_prefill_attention_e4m3(void *out, const void *q, const int32_t *cu_seqlens, int num_seqs, int max_q_len,
+                                     int total_q, const void *k_cache, const void *v_cache, const float *kv_scales,
+                                     const int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,
+                                     int num_blocks, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                                     int window, int num_sinks, float scale, int dtype, int out_dtype, int *dev_status,
+                                     void *stream);
+
 /* ---- queries and keys: norm, rotary positions, append ---------------------------- */
 
 /* Scalings of the rotation's frequencies f_i = base^(-2 i / rotary_dim) for

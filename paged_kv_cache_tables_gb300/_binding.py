@@ -96,6 +96,11 @@ def lib():
         "pkv_paged_window_decode_attention": ([P, P, P, P, P, I, P, I, I, I, I, I, I, I, I, F, I, I, P, P], I),
         "pkv_paged_window_prefill_attention": ([P, P, P, I, I, I, P, P, P, I, P, I, I, I, I, I, I, I, F, I, I, P, P],
                                                I),
+        "pkv_kv_append_e4m3": ([P, I64, P, I64, P, I, P, P, P, I, I, I, I, I, P, P], I),
+        "pkv_kv_gather_e4m3": ([P, P, P, P, P, P, I, P, P, I, I, I, I, I, I, I, P, P], I),
+        "pkv_paged_decode_attention_e4m3": ([P, P, P, P, P, P, I, P, I, I, I, I, I, I, I, I, F, I, I, P, P], I),
+        "pkv_paged_prefill_attention_e4m3": ([P, P, P, I, I, I, P, P, P, P, I, P, I, I, I, I, I, I, I, F, I, I, P, P],
+                                             I),
         "pkv_rope_frequencies": ([P, ctypes.POINTER(F), I, D, I, D, D, D, D], I),
         "pkv_qk_rope": ([P, I64, P, I64, P, I64, P, I64, P, P, I, I, F, P, P, I, F, I, I, I, I, I, P], I),
         "pkv_qk_rope_append": ([P, I64, P, I64, P, I64, P, I64, P, P, P, I, I, F, P, P, I, F, I, P, P, I, I, I, I, I,
@@ -376,6 +381,51 @@ def paged_window_prefill_attention(out, q, cu_seqlens, max_q_len, k_cache, v_cac
                                                   context_lens, window, num_sinks, scale, dev_status, stream)
     if st:
         raise PkvError("pkv_paged_window_prefill_attention", st)
+
+
+# A cache held in 8 bits: k_cache, v_cache float8_e4m3fn [NB, Hkv, 16, d] and
+# kv_scales float32 [NB, Hkv, 2] (K, V); a value is its code times its scale.
+
+_WHOLE = 2 ** 31 - 1   # a window that no context exceeds
+
+
+def kv_append_e4m3(k, v, slot_mapping, k_cache, v_cache, kv_scales, dev_status=None, stream=None):
+    """pkv_kv_append_e4m3: k, v [T, Hkv, d], each token's heads contiguous;
+    slot_mapping int64 [T], the rows of a block next to one another."""
+    st = (_calls or _load_calls()).append_e4m3(k, v, slot_mapping, k_cache, v_cache, kv_scales, dev_status, stream)
+    if st:
+        raise PkvError("pkv_kv_append_e4m3", st)
+
+
+def kv_gather_e4m3(k, v, k_cache, v_cache, kv_scales, block_tables, cu_seqlens, first=None, dev_status=None,
+                   stream=None):
+    """pkv_kv_gather_e4m3: rows cu_seqlens[s] + i of k, v [total, Hkv, d] (16-bit
+    or float32) receive position first[s] + i (first int32 [S]; None: 0)."""
+    st = (_calls or _load_calls()).gather_e4m3(k, v, k_cache, v_cache, kv_scales, block_tables, cu_seqlens, first,
+                                               dev_status, stream)
+    if st:
+        raise PkvError("pkv_kv_gather_e4m3", st)
+
+
+def paged_decode_attention_e4m3(out, q, k_cache, v_cache, kv_scales, block_tables, context_lens, window=None, num_sinks=0,
+                                scale=None, dev_status=None, stream=None):
+    """pkv_paged_decode_attention_e4m3: q/out [S, Hq, d]; block_tables int32
+    [S, max_blocks]; context_lens int32 [S].  window None: the whole context."""
+    st = (_calls or _load_calls()).decode_e4m3(out, q, k_cache, v_cache, kv_scales, block_tables, context_lens,
+                                               _WHOLE if window is None else window, num_sinks, scale, dev_status, stream)
+    if st:
+        raise PkvError("pkv_paged_decode_attention_e4m3", st)
+
+
+def paged_prefill_attention_e4m3(out, q, cu_seqlens, max_q_len, k_cache, v_cache, kv_scales, block_tables, context_lens,
+                                 window=None, num_sinks=0, scale=None, dev_status=None, stream=None):
+    """pkv_paged_prefill_attention_e4m3: q/out [total_q, Hq, d]; cu_seqlens int32
+    [S + 1].  window None: each row sees all positions up to its own."""
+    st = (_calls or _load_calls()).prefill_e4m3(out, q, cu_seqlens, max_q_len, k_cache, v_cache, kv_scales, block_tables,
+                                                context_lens, _WHOLE if window is None else window, num_sinks, scale,
+                                                dev_status, stream)
+    if st:
+        raise PkvError("pkv_paged_prefill_attention_e4m3", st)
 
 
 def rope_frequencies(rotary_dim, base=10000.0, scaling=ROPE_PLAIN, factor=1.0, original_context=0, low=1.0, high=32.0,

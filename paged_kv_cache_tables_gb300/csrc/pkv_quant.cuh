@@ -1,0 +1,60 @@
+// The cache held in 8 bits: e4m3 codes, converted two at a time, and the scale
+// of a block.  Inline PTX, written for this library.
+#pragma once
+
+#include <stdint.h>
+
+#include "pkv_device.cuh"
+
+namespace pkv {
+
+constexpr float kCodeMax = 448.f;   // the largest e4m3 value
+
+// Two e4m3 codes (the low byte first) as an fp16 pair; exact.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 lo, hi;\n\t"
+        "mov.b32 {lo, hi}, %1;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, lo;\n\t}"
+        : "=r"(r)
+        : "r"(codes));
+    return r;
+}
+
+// Four codes as two pairs.
+__device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t codes, uint32_t &first, uint32_t &second) {
+    asm("{\n\t.reg .b16 lo, hi;\n\t"
+        "mov.b32 {lo, hi}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, lo;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+        : "=r"(first), "=r"(second)
+        : "r"(codes));
+}
+
+// The codes next to four values (ties to even; beyond 448 the code of 448; NaN
+// stays NaN), `a` in the lowest byte.
+__device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 lo, hi;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+        "mov.b32 %0, {lo, hi};\n\t}"
+        : "=r"(r)
+        : "f"(a), "f"(b), "f"(c), "f"(d));
+    return r;
+}
+
+__device__ __forceinline__ float2 f16x2_to_f32(uint32_t pair) { return __half22float2(*reinterpret_cast<__half2 *>(&pair)); }
+
+// The scale for values of magnitude at most a (finite): the least power of two
+// s >= 2^-60 with a <= 448 s.  448 = 1.75 * 2^8.  A power of two, so that x / s
+// and a later change of scale are exact (short of e4m3's subnormals): e4m3 is
+// a floating-point format, and loses no precision to the up to one binade of
+// range that a finer scale would use.
+__device__ __forceinline__ float block_scale(float a) {
+    const uint32_t u = __float_as_uint(a);
+    const int e = (int)(u >> 23) - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+    return __uint_as_float((uint32_t)max(e, 127 - 60) << 23);
+}
+
+}  // namespace pkv

@@ -188,14 +188,14 @@ PyObject *guarded(const char *name, Py_ssize_t n, Py_ssize_t wanted, F body) {
     return nullptr;
 }
 
-// What the two attention calls share.
+// What the attention calls share; `code` is the caches' type, q's where it is not given.
 struct Attention {
     int device;
     at::IntArrayRef q_shape, cache;
     at::ScalarType type, out_type;
     void *out, *q, *k, *v;
     int Hq, d, NB, Hkv, bs;
-    Attention(PyObject *o_out, PyObject *o_q, PyObject *o_k, PyObject *o_v) {
+    Attention(PyObject *o_out, PyObject *o_q, PyObject *o_k, PyObject *o_v, at::ScalarType code = at::ScalarType::Undefined) {
         const at::Tensor &tq = tensor(o_q, "q"), &tout = tensor(o_out, "out"), &tk = tensor(o_k, "k_cache");
         device = device_of(tq, "q");
         q_shape = dims(tq, "q", 3);
@@ -205,8 +205,9 @@ struct Attention {
         if (cache[3] != q_shape[2]) refuse(PyExc_ValueError, "q and the caches must have one head_dim");
         out = ptr(o_out, "out", out_type, q_shape, device);
         q = ptr(o_q, "q", type, q_shape, device);
-        k = ptr(o_k, "k_cache", type, cache, device);
-        v = ptr(o_v, "v_cache", type, cache, device);
+        if (code == at::ScalarType::Undefined) code = type;
+        k = ptr(o_k, "k_cache", code, cache, device);
+        v = ptr(o_v, "v_cache", code, cache, device);
         Hq = size_arg(q_shape[1], "q");
         d = size_arg(q_shape[2], "q");
         NB = size_arg(cache[0], "k_cache");
@@ -259,6 +260,117 @@ PyObject *window_prefill(PyObject *, Args a, Py_ssize_t n) {
                                                   static_cast<int32_t *>(tables), max_blocks, static_cast<int32_t *>(ctx),
                                                   t.NB, t.Hq, t.Hkv, t.d, t.bs, window, sinks, scale, type, out_type,
                                                   status, stream);
+    });
+}
+
+constexpr at::ScalarType kCode = at::kFloat8_e4m3fn;
+
+float *scales_arg(PyObject *o, int64_t NB, int64_t Hkv, int device) {
+    return static_cast<float *>(ptr(o, "kv_scales", at::kFloat, {NB, Hkv, 2}, device));
+}
+
+// (out, q, k_cache, v_cache, kv_scales, block_tables, context_lens, window, num_sinks, scale, dev_status, stream)
+PyObject *decode_e4m3(PyObject *, Args a, Py_ssize_t n) {
+    return guarded("decode_e4m3", n, 12, [&] {
+        const Attention t(a[0], a[1], a[2], a[3], kCode);
+        const float *scales = scales_arg(a[4], t.NB, t.Hkv, t.device);
+        const int64_t S = t.q_shape[0], MB = dims(tensor(a[5], "block_tables"), "block_tables", 2)[1];
+        void *tables = ptr(a[5], "block_tables", at::kInt, {S, MB}, t.device);
+        void *ctx = ptr(a[6], "context_lens", at::kInt, {S}, t.device);
+        const int max_blocks = size_arg(MB, "block_tables"), seqs = size_arg(S, "q");
+        const int window = int_arg(a[7], "window"), sinks = int_arg(a[8], "num_sinks");
+        const float scale = t.scale(a[9]);
+        const int type = dtype_code(t.type, "q"), out_type = dtype_code(t.out_type, "out");
+        int *status = status_arg(a[10], t.device);
+        void *stream = stream_arg(a[11], t.device);
+        OtherThreads run;
+        c10::cuda::OptionalCUDAGuard guard(c10::Device(c10::kCUDA, (c10::DeviceIndex)t.device));
+        return pkv_paged_decode_attention_e4m3(t.out, t.q, t.k, t.v, scales, static_cast<int32_t *>(tables), max_blocks,
+                                               static_cast<int32_t *>(ctx), seqs, t.NB, t.Hq, t.Hkv, t.d, t.bs, window, sinks,
+                                               scale, type, out_type, status, stream);
+    });
+}
+
+// (out, q, cu_seqlens, max_q_len, k_cache, v_cache, kv_scales, block_tables, context_lens, window, num_sinks, scale,
+//  dev_status, stream)
+PyObject *prefill_e4m3(PyObject *, Args a, Py_ssize_t n) {
+    return guarded("prefill_e4m3", n, 14, [&] {
+        const Attention t(a[0], a[1], a[4], a[5], kCode);
+        const float *scales = scales_arg(a[6], t.NB, t.Hkv, t.device);
+        const auto tb = dims(tensor(a[7], "block_tables"), "block_tables", 2);
+        const int64_t S = tb[0], MB = tb[1];
+        void *cu = ptr(a[2], "cu_seqlens", at::kInt, {S + 1}, t.device);
+        void *tables = ptr(a[7], "block_tables", at::kInt, {S, MB}, t.device);
+        void *ctx = ptr(a[8], "context_lens", at::kInt, {S}, t.device);
+        const int max_blocks = size_arg(MB, "block_tables"), seqs = size_arg(S, "block_tables");
+        const int max_q = int_arg(a[3], "max_q_len"), total_q = size_arg(t.q_shape[0], "q");
+        const int window = int_arg(a[9], "window"), sinks = int_arg(a[10], "num_sinks");
+        const float scale = t.scale(a[11]);
+        const int type = dtype_code(t.type, "q"), out_type = dtype_code(t.out_type, "out");
+        int *status = status_arg(a[12], t.device);
+        void *stream = stream_arg(a[13], t.device);
+        OtherThreads run;
+        c10::cuda::OptionalCUDAGuard guard(c10::Device(c10::kCUDA, (c10::DeviceIndex)t.device));
+        return pkv_paged_prefill_attention_e4m3(t.out, t.q, static_cast<int32_t *>(cu), seqs, max_q, total_q, t.k, t.v, scales,
+                                                static_cast<int32_t *>(tables), max_blocks, static_cast<int32_t *>(ctx), t.NB,
+                                                t.Hq, t.Hkv, t.d, t.bs, window, sinks, scale, type, out_type, status, stream);
+    });
+}
+
+// (k, v, slot_mapping, k_cache, v_cache, kv_scales, dev_status, stream)
+PyObject *append_e4m3(PyObject *, Args a, Py_ssize_t n) {
+    return guarded("append_e4m3", n, 8, [&] {
+        const at::Tensor &tk = tensor(a[0], "k");
+        const int dev = device_of(tk, "k");
+        const auto ks = dims(tk, "k", 3);
+        const int64_t T = ks[0], Hkv = ks[1], d = ks[2];
+        const at::ScalarType type = tk.scalar_type();
+        const Rows k = rows(a[0], "k", type, ks, dev), v = rows(a[1], "v", type, ks, dev);
+        void *slots = ptr(a[2], "slot_mapping", at::kLong, {T}, dev);
+        const auto cs = dims(tensor(a[3], "k_cache"), "k_cache", 4);
+        const int64_t NB = cs[0], bs = cs[2];
+        void *kc = ptr(a[3], "k_cache", kCode, {NB, Hkv, bs, d}, dev);
+        void *vc = ptr(a[4], "v_cache", kCode, {NB, Hkv, bs, d}, dev);
+        float *scales = scales_arg(a[5], NB, Hkv, dev);
+        const int tokens = size_arg(T, "k"), blocks = size_arg(NB, "k_cache"), block_size = size_arg(bs, "k_cache");
+        const int heads = size_arg(Hkv, "k"), head_dim = size_arg(d, "k"), code = dtype_code(type, "k");
+        int *status = status_arg(a[6], dev);
+        void *stream = stream_arg(a[7], dev);
+        OtherThreads run;
+        c10::cuda::OptionalCUDAGuard guard(c10::Device(c10::kCUDA, (c10::DeviceIndex)dev));
+        return pkv_kv_append_e4m3(k.p, k.stride, v.p, v.stride, static_cast<int64_t *>(slots), tokens, kc, vc, scales, blocks,
+                                  block_size, heads, head_dim, code, status, stream);
+    });
+}
+
+// (k, v, k_cache, v_cache, kv_scales, block_tables, cu_seqlens, first, dev_status, stream)
+PyObject *gather_e4m3(PyObject *, Args a, Py_ssize_t n) {
+    return guarded("gather_e4m3", n, 10, [&] {
+        const at::Tensor &tk = tensor(a[0], "k");
+        const int dev = device_of(tk, "k");
+        const auto ks = dims(tk, "k", 3);
+        const at::ScalarType type = tk.scalar_type();
+        void *k = ptr(a[0], "k", type, ks, dev), *v = ptr(a[1], "v", type, ks, dev);
+        const auto cs = dims(tensor(a[2], "k_cache"), "k_cache", 4);
+        const int64_t NB = cs[0], bs = cs[2];
+        void *kc = ptr(a[2], "k_cache", kCode, {NB, ks[1], bs, ks[2]}, dev);
+        void *vc = ptr(a[3], "v_cache", kCode, {NB, ks[1], bs, ks[2]}, dev);
+        const float *scales = scales_arg(a[4], NB, ks[1], dev);
+        const auto tb = dims(tensor(a[5], "block_tables"), "block_tables", 2);
+        const int64_t S = tb[0], MB = tb[1];
+        void *tables = ptr(a[5], "block_tables", at::kInt, {S, MB}, dev);
+        void *cu = ptr(a[6], "cu_seqlens", at::kInt, {S + 1}, dev);
+        void *first = ptr_or_null(a[7], "first", at::kInt, {S}, dev);
+        const int seqs = size_arg(S, "block_tables"), max_blocks = size_arg(MB, "block_tables"), total = size_arg(ks[0], "k");
+        const int heads = size_arg(ks[1], "k"), head_dim = size_arg(ks[2], "k"), code = dtype_code(type, "k");
+        const int blocks = size_arg(NB, "k_cache"), block_size = size_arg(bs, "k_cache");
+        int *status = status_arg(a[8], dev);
+        void *stream = stream_arg(a[9], dev);
+        OtherThreads run;
+        c10::cuda::OptionalCUDAGuard guard(c10::Device(c10::kCUDA, (c10::DeviceIndex)dev));
+        return pkv_kv_gather_e4m3(k, v, kc, vc, scales, static_cast<int32_t *>(tables), max_blocks, static_cast<int32_t *>(cu),
+                                  static_cast<int32_t *>(first), seqs, total, blocks, block_size, heads, head_dim, code, status,
+                                  stream);
     });
 }
 
@@ -405,7 +517,8 @@ PyObject *release_blocks(PyObject *, Args a, Py_ssize_t n) {
 #define PKV_METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {PKV_METHOD(window_decode),  PKV_METHOD(window_prefill), PKV_METHOD(qk_rope),
                          PKV_METHOD(qk_rope_append), PKV_METHOD(step_tables),    PKV_METHOD(release_blocks),
-                         {nullptr, nullptr, 0, nullptr}};
+                         PKV_METHOD(decode_e4m3),    PKV_METHOD(prefill_e4m3),   PKV_METHOD(append_e4m3),
+                         PKV_METHOD(gather_e4m3),    {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_torch_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
