@@ -4,6 +4,8 @@
 
 #include <stdint.h>
 
+#include <cmath>
+
 #include "pkv_device.cuh"
 
 namespace pkv {
@@ -55,6 +57,22 @@ __device__ __forceinline__ float block_scale(float a) {
     const uint32_t u = __float_as_uint(a);
     const int e = (int)(u >> 23) - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
     return __uint_as_float((uint32_t)max(e, 127 - 60) << 23);
+}
+
+// What both attention calls refuse.
+inline int quant_attention_refusal(int num_seqs, int num_blocks, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                                   int max_blocks_per_seq, int window, int num_sinks, float scale, int dtype, int out_dtype) {
+    if (num_seqs < 0 || num_blocks <= 0 || num_kv_heads <= 0 || num_q_heads <= 0 || max_blocks_per_seq <= 0 || window <= 0 ||
+        num_sinks < 0)
+        return PKV_ERR_INVALID_ARG;
+    if (num_q_heads % num_kv_heads != 0) return PKV_ERR_INVALID_ARG;
+    if (num_q_heads / num_kv_heads > 16 || block_size != 16 || (head_dim != 64 && head_dim != 128)) return PKV_ERR_UNSUPPORTED;
+    if (dtype != PKV_DTYPE_F16 && dtype != PKV_DTYPE_BF16) return PKV_ERR_UNSUPPORTED;
+    if (out_dtype != dtype && out_dtype != PKV_DTYPE_F32) return PKV_ERR_UNSUPPORTED;
+    if (!(std::isfinite(scale) && scale > 0.f)) return PKV_ERR_INVALID_ARG;
+    if ((int64_t)num_blocks * num_kv_heads * block_size >= (int64_t)1 << 31) return PKV_ERR_UNSUPPORTED;
+    if ((int64_t)num_seqs * max_blocks_per_seq >= (int64_t)1 << 31 || max_blocks_per_seq > (1 << 26)) return PKV_ERR_UNSUPPORTED;
+    return PKV_OK;
 }
 
 }  // namespace pkv

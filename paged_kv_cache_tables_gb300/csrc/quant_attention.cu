@@ -116,46 +116,7 @@ static int quant_attention(QuantAttentionParams p, int num_seqs, int block_size,
     return e == cudaSuccess ? PKV_OK : cuda_fail(e);
 }
 
-static int quant_attention_refusal(int num_seqs, int num_blocks, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
-                                   int max_blocks_per_seq, int window, int num_sinks, float scale, int dtype, int out_dtype) {
-    if (num_seqs < 0 || num_blocks <= 0 || num_kv_heads <= 0 || num_q_heads <= 0 || max_blocks_per_seq <= 0 || window <= 0 ||
-        num_sinks < 0)
-        return PKV_ERR_INVALID_ARG;
-    if (num_q_heads % num_kv_heads != 0) return PKV_ERR_INVALID_ARG;
-    if (num_q_heads / num_kv_heads > 16 || block_size != 16 || (head_dim != 64 && head_dim != 128)) return PKV_ERR_UNSUPPORTED;
-    if (dtype != PKV_DTYPE_F16 && dtype != PKV_DTYPE_BF16) return PKV_ERR_UNSUPPORTED;
-    if (out_dtype != dtype && out_dtype != PKV_DTYPE_F32) return PKV_ERR_UNSUPPORTED;
-    if (!(std::isfinite(scale) && scale > 0.f)) return PKV_ERR_INVALID_ARG;
-    if ((int64_t)num_blocks * num_kv_heads * block_size >= (int64_t)1 << 31) return PKV_ERR_UNSUPPORTED;
-    if ((int64_t)num_seqs * max_blocks_per_seq >= (int64_t)1 << 31 || max_blocks_per_seq > (1 << 26)) return PKV_ERR_UNSUPPORTED;
-    return PKV_OK;
-}
-
 }  // namespace pkv
-
-extern "C" int pkv_paged_decode_attention_e4m3(void *out, const void *q, const void *k_cache, const void *v_cache,
-                                               const float *kv_scales, const int32_t *block_tables, int max_blocks_per_seq,
-                                               const int32_t *context_lens, int num_seqs, int num_blocks, int num_q_heads,
-                                               int num_kv_heads, int head_dim, int block_size, int window, int num_sinks,
-                                               float scale, int dtype, int out_dtype, int *dev_status, void *stream) {
-    pkv::NvtxRange nvtx_range("pkv_paged_decode_attention_e4m3");
-    using namespace pkv;
-    int rc = quant_attention_refusal(num_seqs, num_blocks, num_q_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq,
-                                     window, num_sinks, scale, dtype, out_dtype);
-    if (rc != PKV_OK) return rc;
-    if ((int64_t)num_seqs * num_kv_heads * 16 >= (int64_t)1 << 31) return PKV_ERR_UNSUPPORTED;
-    if (num_seqs == 0) return PKV_OK;
-    if (!out || !q || !k_cache || !v_cache || !kv_scales || !block_tables || !context_lens) return PKV_ERR_INVALID_ARG;
-    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(kv_scales, 8) ||
-        !aligned(block_tables, 4) || !aligned(context_lens, 4))
-        return PKV_ERR_INVALID_ARG;
-    QuantAttentionParams p = {};
-    p.out = out, p.q = q, p.k_cache = static_cast<const uint8_t *>(k_cache), p.v_cache = static_cast<const uint8_t *>(v_cache);
-    p.scales = kv_scales, p.block_tables = block_tables, p.context_lens = context_lens, p.dev_status = dev_status;
-    p.max_blocks = max_blocks_per_seq, p.num_blocks = num_blocks, p.Hq = num_q_heads, p.Hkv = num_kv_heads;
-    p.G = num_q_heads / num_kv_heads, p.total_q = num_seqs, p.max_q_len = 1, p.out_dtype = out_dtype;
-    return quant_attention(p, num_seqs, block_size, head_dim, window, num_sinks, scale, dtype, static_cast<cudaStream_t>(stream));
-}
 
 extern "C" int pkv_paged_prefill_attention_e4m3(void *out, const void *q, const int32_t *cu_seqlens, int num_seqs, int max_q_len,
                                                 int total_q, const void *k_cache, const void *v_cache, const float *kv_scales,

@@ -44,6 +44,7 @@
 #include "pkv_cluster.cuh"
 #include "pkv_device.cuh"
 #include "pkv_host.h"
+#include "pkv_window.cuh"
 
 namespace pkv {
 
@@ -85,31 +86,6 @@ struct WindowShape {
     // behind the ring: barriers, then (m, l) of each warp and of the CTA
     static constexpr int OFF_ML = RING_BYTES + kWinWarps * STAGES * 8;
     static constexpr int SMEM_BYTES = 1024 + OFF_ML + (kWinWarps + 1) * 32 * 4;
-};
-
-// The blocks of a context that hold a position its last token sees.
-struct Visible {
-    int ctx, w0;            // clamped context; the window's first position
-    int sink_blocks, skip;  // entry v of the list is logical block v, or v + skip from sink_blocks on
-    int count;
-    bool bad;
-    __device__ __forceinline__ Visible(const WindowDecodeParams &p, int context) {
-        bad = context < 0 || context > p.max_blocks * 16;
-        ctx = min(max(context, 0), p.max_blocks * 16);
-        const int nblk = (ctx + 15) >> 4;
-        w0 = max(ctx - p.window, 0);
-        sink_blocks = min((p.sinks + 15) >> 4, nblk);
-        skip = max((w0 >> 4) - sink_blocks, 0);
-        count = nblk - skip;
-    }
-    __device__ __forceinline__ int logical(int v) const { return v < sink_blocks ? v : v + skip; }
-    // the visible positions of logical block j, one bit each (never none):
-    // before ctx, and in the window or among the first tokens
-    __device__ __forceinline__ uint32_t bits(int j, int sinks) const {
-        const int t0 = j * 16;
-        const int lim = min(ctx - t0, 16), first = min(max(w0 - t0, 0), 16), sk = min(max(sinks - t0, 0), 16);
-        return ((1u << lim) - 1u) & ((0xffffu << first) | ((1u << sk) - 1u)) & 0xffffu;
-    }
 };
 
 // Issues the TMA loads of block `blk`'s K and V tiles of KV head h into a ring
