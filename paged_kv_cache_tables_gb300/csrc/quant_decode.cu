@@ -16,13 +16,17 @@
 // Layout.  A 16-byte piece of a row goes to one lane, so that a fragment's
 // dimensions (for S) and output rows (for O^T) are not in their order in memory
 // but in an order that suits these loads:
-//   S = Q K^T       lane (g, t4) takes 16 dimensions 16 (t4 + 4 j) .. of token rho(g)
+//   S^T = K Q^T     lane (g, t4) takes 16 dimensions 16 (t4 + 4 j) .. of tokens
+//                   rho(g) and rho(g) + 8
 //   O^T += V^T P^T  lane (g, t4) takes head_dim / 8 dimensions from g on, of tokens
 //                   rho(2 t4), rho(2 t4 + 1), and 8 further; bytes of two tokens
 //                   are put side by side before they are converted
 // rho permutes the tokens of a group of 8 so that neither load meets a bank
 // twice under TMA's 128-byte swizzle (a shared-memory row of 128 bytes is one
-// token's codes, or with head_dim 64 two tokens').
+// token's codes, or with head_dim 64 two tokens').  With tokens as the rows of
+// both products neither pays for absent heads beyond 8, a lane's scores and its
+// accumulator columns belong to the same two heads, and P^T is P of S^T
+// transposed, 8 x 8 at a time (movmatrix).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -58,13 +62,14 @@ struct QuantDecodeParams {
 template <int D, bool MANY>
 struct QuantShape {
     static constexpr int TILE_BYTES = 16 * D;
-    static constexpr int STAGE_BYTES = 2 * TILE_BYTES;  // K then V
-    static constexpr int STAGES = D == 128 ? (MANY ? 4 : 6) : 8;
-    static constexpr int STEP = 2;                      // blocks a warp takes at a time
+    static constexpr int BLOCK_BYTES = 2 * TILE_BYTES;  // K then V
+    static constexpr int STEP = 2;                      // blocks a warp takes at a time: a slot of its ring
+    static constexpr int SLOT_BYTES = STEP * BLOCK_BYTES;
+    static constexpr int SLOTS = D == 128 ? (MANY ? 2 : 3) : 4;
     static constexpr int PER_SM = D == 128 && !MANY ? 2 : 3;
-    static constexpr int RING_BYTES = kQdWarps * STAGES * STAGE_BYTES;
+    static constexpr int RING_BYTES = kQdWarps * SLOTS * SLOT_BYTES;
     // behind the ring: barriers, then (m, l) of each warp and of the CTA
-    static constexpr int OFF_ML = RING_BYTES + kQdWarps * STAGES * 8;
+    static constexpr int OFF_ML = RING_BYTES + kQdWarps * SLOTS * 8;
     static constexpr int SMEM_BYTES = 1024 + OFF_ML + (kQdWarps + 1) * 32 * 4;
     static_assert((kQdWarps + 1) * 16 * D * 4 <= RING_BYTES, "the parts take the ring's place");
 };
@@ -109,24 +114,30 @@ __device__ __forceinline__ void query4(uint2 x, float f, uint32_t &a, uint32_t &
     }
 }
 
-// A warp's part of a range: query fragments (rows = heads of the group, padded
-// to 16), accumulator, running maximum and sum.
+// The transpose of an 8 x 8 matrix of 16-bit elements, a pair a lane.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// A warp's part of a range.  The heads of the group are columns, 8 to a tile
+// (NT tiles): lane (g, t4) has those at 2 t4 and 2 t4 + 1 of each.
 template <typename T, int D, int NT, bool MANY, bool RES>
 struct QuantPart {
     using Sh = QuantShape<D, MANY>;
     static constexpr int STEP = Sh::STEP;
     static constexpr int KT = D / 16;        // steps of 16 dimensions, and of 16 output rows
     static constexpr int NW = D / 32;        // 4-byte words of a token's codes that a lane takes of V
-    uint32_t qa[KT][4];
-    float acc[KT][NT][4];
-    float m_run[NT], l_run[NT];
-    float qscale[NT];                        // a head's score scale, its query's power of two taken back
+    uint32_t qb[KT][NT][2];
+    float acc[KT][NT][4];                    // [output rows][tile][row g heads 2, row g + 8 heads 2]
+    float m_run[NT][2], off[NT][2];          // running maximum; what P subtracts
+    float l_run[NT][2];
+    float qscale[NT][2];                     // a head's score scale, its query's power of two taken back
 
     // q: G rows of D elements
     __device__ __forceinline__ void start(const T *q, int G, float scale_log2, int lane) {
         const int g = lane >> 2, t4 = lane & 3;
-#pragma unroll
-        for (int kk = 0; kk < KT; ++kk) qa[kk][1] = qa[kk][3] = 0u;   // rows 8..15, for groups of at most 8
 #pragma unroll
         for (int pn = 0; pn < NT; ++pn) {
             const int row = pn * 8 + g;
@@ -149,50 +160,54 @@ struct QuantPart {
                 f = __uint_as_float((uint32_t)(254 - e) << 23);
                 back = __uint_as_float((uint32_t)e << 23);
             }
-            qscale[pn] = back * scale_log2;
 #pragma unroll
-            for (int kk = 0; kk < KT; ++kk) query4<T>(x[kk], f, qa[kk][pn], qa[kk][pn + 2]);
-        }
+            for (int e = 0; e < 2; ++e) qscale[pn][e] = __shfl_sync(0xffffffffu, back, 4 * (2 * t4 + e)) * scale_log2;
 #pragma unroll
-        for (int mt = 0; mt < KT; ++mt)
+            for (int kk = 0; kk < KT; ++kk) query4<T>(x[kk], f, qb[kk][pn][0], qb[kk][pn][1]);
 #pragma unroll
-            for (int pn = 0; pn < NT; ++pn)
+            for (int mt = 0; mt < KT; ++mt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[mt][pn][e] = 0.f;
 #pragma unroll
-        for (int pn = 0; pn < NT; ++pn) {
-            m_run[pn] = -INFINITY;
-            l_run[pn] = 0.f;
+            for (int e = 0; e < 2; ++e) {
+                m_run[pn][e] = -INFINITY;
+                off[pn][e] = -7.f;
+                l_run[pn][e] = 0.f;
+            }
         }
     }
 
-    // STEP blocks of 16 tokens in ring slots at `slot`, of scales ks, vs; bit t of
-    // `bits` set where token t of them is seen (some token of the first block
-    // is).  `release` runs once the slots have been read.
+    // STEP blocks of 16 tokens in the ring slot at `slot`, of scales ks, vs; bit t
+    // of `bits` set where token t of them is seen (all of them: `all`).
+    // `release` runs once the slot has been read.
     template <typename F>
-    __device__ __forceinline__ void attend(const uint32_t (&slot)[STEP], const float (&ks)[STEP], const float (&vs)[STEP],
-                                           uint32_t bits, int lane, F release) {
+    __device__ __forceinline__ void attend(uint32_t slot, const float (&ks)[STEP], const float (&vs)[STEP], uint32_t bits,
+                                           bool all, int lane, F release) {
         const int g = lane >> 2, t4 = lane & 3;
-        float s[2 * STEP][4];
+        // S^T = K Q^T, two chains a block
+        float s[STEP][2][NT][4];
 #pragma unroll
-        for (int nt = 0; nt < 2 * STEP; ++nt)
+        for (int b = 0; b < STEP; ++b)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
+            for (int pn = 0; pn < NT; ++pn)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[b][0][pn][e] = s[b][1][pn][e] = 0.f;
+        const int tok_k = token_at<D>(g);
 #pragma unroll
         for (int b = 0; b < STEP; ++b)
 #pragma unroll
             for (int j = 0; j < D / 64; ++j) {
-                const int tok = token_at<D>(g);
-                const uint4 k0 = lds128(slot[b] + piece_at<D>(tok, t4 + 4 * j));
-                const uint4 k1 = lds128(slot[b] + piece_at<D>(tok + 8, t4 + 4 * j));
+                const uint4 k0 = lds128(slot + b * Sh::BLOCK_BYTES + piece_at<D>(tok_k, t4 + 4 * j));
+                const uint4 k1 = lds128(slot + b * Sh::BLOCK_BYTES + piece_at<D>(tok_k + 8, t4 + 4 * j));
                 const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    uint32_t x, y;
-                    e4m3x4_to_f16x4(w0[i], x, y);
-                    mma_16816<__half>(s[2 * b], qa[4 * j + i], x, y);
-                    e4m3x4_to_f16x4(w1[i], x, y);
-                    mma_16816<__half>(s[2 * b + 1], qa[4 * j + i], x, y);
+                    uint32_t a[4];
+                    e4m3x4_to_f16x4(w0[i], a[0], a[2]);
+                    e4m3x4_to_f16x4(w1[i], a[1], a[3]);
+#pragma unroll
+                    for (int pn = 0; pn < NT; ++pn)
+                        mma_16816<__half>(s[b][i & 1][pn], a, qb[4 * j + i][pn][0], qb[4 * j + i][pn][1]);
                 }
             }
         // [block][token rho(2 t4), rho(2 t4 + 1), and those + 8][words]
@@ -202,63 +217,56 @@ struct QuantPart {
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 const int tok = token_at<D>(2 * t4 + (u & 1)) + 8 * (u >> 1);
+                const uint32_t tile = slot + b * Sh::BLOCK_BYTES + Sh::TILE_BYTES;
                 if constexpr (D == 128) {
-                    const uint4 v = lds128(slot[b] + Sh::TILE_BYTES + piece_at<D>(tok, g));
+                    const uint4 v = lds128(tile + piece_at<D>(tok, g));
                     vw[b][u][0] = v.x, vw[b][u][1] = v.y, vw[b][u][2] = v.z, vw[b][u][3] = v.w;
                 } else {
-                    const uint2 v = lds64(slot[b] + Sh::TILE_BYTES + piece_at<D>(tok, g >> 1) + (g & 1) * 8);
+                    const uint2 v = lds64(tile + piece_at<D>(tok, g >> 1) + (g & 1) * 8);
                     vw[b][u][0] = v.x, vw[b][u][1] = v.y;
                 }
             }
         release();
 
-        float lv[STEP], rv[STEP];
+        // y in place of the scores: [block][tile][token rho(g) heads 2, token rho(g) + 8 heads 2]
+        float y[STEP][NT][4], rv[STEP];
+        bool past = false;
 #pragma unroll
         for (int b = 0; b < STEP; ++b) {
-            lv[b] = __log2f(vs[b]);
-            rv[b] = exp2_approx(-lv[b]);
+            const float lv = __log2f(vs[b]);
+            rv[b] = exp2_approx(-lv);
+#pragma unroll
+            for (int pn = 0; pn < NT; ++pn)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    y[b][pn][e] = fmaf(s[b][0][pn][e] + s[b][1][pn][e], qscale[pn][e & 1] * ks[b], lv);
+                    if (!all && !((bits >> (16 * b + tok_k + 8 * (e >> 1))) & 1u)) y[b][pn][e] = -INFINITY;
+                    past |= y[b][pn][e] > m_run[pn][e & 1] + 8.f;
+                }
         }
-        const bool all = bits == (uint32_t)((1ull << (16 * STEP)) - 1u);
-        float pr[2 * STEP][2 * NT];
-        float alpha[NT];
-        bool moved = false;
+        // the maximum is only moved when it grows by more than 2^8
+        if (__any_sync(0xffffffffu, past)) {
 #pragma unroll
-        for (int pn = 0; pn < NT; ++pn) {
-            float x[2 * STEP][2];
-            float mx = -INFINITY;
-#pragma unroll
-            for (int nt = 0; nt < 2 * STEP; ++nt) {
-                const float f = qscale[pn] * ks[nt >> 1];
+            for (int pn = 0; pn < NT; ++pn)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    x[nt][e] = fmaf(s[nt][pn * 2 + e], f, lv[nt >> 1]);
-                    if (!all && !((bits >> (nt * 8 + token_at<D>(2 * t4 + e))) & 1u)) x[nt][e] = -INFINITY;
-                    mx = fmaxf(mx, x[nt][e]);
-                }
-            }
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            // the maximum is only moved when it grows by more than 2^8
-            const bool move = m_run[pn] == -INFINITY || mx > m_run[pn] + 8.f;
-            const float m_new = move ? fmaxf(m_run[pn], mx) : m_run[pn];
-            // no finite score so far (keys of infinities): nothing to subtract
-            const float sub = m_new == -INFINITY ? 0.f : m_new;
-            alpha[pn] = move ? exp2_approx(m_run[pn] - sub) : 1.f;
-            moved |= move;
-            m_run[pn] = m_new;
-            l_run[pn] *= alpha[pn];
+                    float mx = fmaxf(y[0][pn][e], y[0][pn][e + 2]);
 #pragma unroll
-            for (int b = 0; b < STEP; ++b) {
-                float rs = 0.f;
+                    for (int b = 1; b < STEP; ++b) mx = fmaxf(mx, fmaxf(y[b][pn][e], y[b][pn][e + 2]));
 #pragma unroll
-                for (int nt = 2 * b; nt < 2 * b + 2; ++nt)
+                    for (int d = 4; d < 32; d *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+                    if (mx > m_run[pn][e] + 8.f) {
+                        const float alpha = exp2_approx(m_run[pn][e] - mx);
+                        m_run[pn][e] = mx;
+                        off[pn][e] = mx - 7.f;
+                        l_run[pn][e] *= alpha;
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        pr[nt][pn * 2 + e] = exp2_approx(x[nt][e] - (sub - 7.f));
-                        rs += pr[nt][pn * 2 + e];
+                        for (int mt = 0; mt < KT; ++mt) {
+                            acc[mt][pn][e] *= alpha;
+                            acc[mt][pn][e + 2] *= alpha;
+                        }
                     }
-                l_run[pn] = fmaf(rs, rv[b], l_run[pn]);
-            }
+                }
         }
         // hidden positions may hold anything (even NaN codes): zero, so that 0 x
         // garbage cannot reach the accumulator
@@ -273,30 +281,28 @@ struct QuantPart {
                     for (int i = 0; i < NW; ++i) vw[b][u][i] &= keep;
                 }
         }
-        if (__any_sync(0xffffffffu, moved))
-#pragma unroll
-            for (int pn = 0; pn < NT; ++pn) {
-                const float a_lo = __shfl_sync(0xffffffffu, alpha[pn], 8 * t4);
-                const float a_hi = __shfl_sync(0xffffffffu, alpha[pn], 8 * t4 + 4);
-#pragma unroll
-                for (int mt = 0; mt < KT; ++mt) {
-                    acc[mt][pn][0] *= a_lo;
-                    acc[mt][pn][1] *= a_hi;
-                    acc[mt][pn][2] *= a_lo;
-                    acc[mt][pn][3] *= a_hi;
-                }
-            }
 #pragma unroll
         for (int b = 0; b < STEP; ++b) {
-            uint32_t pb0[NT][2], pb1[NT][2];
+            // P^T fragments: tokens 0..7 and 8..15 of the block; value, residual
+            uint32_t pb[NT][2][2];
 #pragma unroll
             for (int pn = 0; pn < NT; ++pn) {
+                float w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[e] = exp2_approx(y[b][pn][e] - off[pn][e & 1]);
+                l_run[pn][0] = fmaf(w[0] + w[2], rv[b], l_run[pn][0]);
+                l_run[pn][1] = fmaf(w[1] + w[3], rv[b], l_run[pn][1]);
                 if constexpr (RES) {
-                    pack2_split<__half>(pr[2 * b][pn * 2], pr[2 * b][pn * 2 + 1], pb0[pn][0], pb0[pn][1]);
-                    pack2_split<__half>(pr[2 * b + 1][pn * 2], pr[2 * b + 1][pn * 2 + 1], pb1[pn][0], pb1[pn][1]);
+                    pack2_split<__half>(w[0], w[1], pb[pn][0][0], pb[pn][0][1]);
+                    pack2_split<__half>(w[2], w[3], pb[pn][1][0], pb[pn][1][1]);
                 } else {
-                    pb0[pn][0] = pack2<__half>(pr[2 * b][pn * 2], pr[2 * b][pn * 2 + 1]);
-                    pb1[pn][0] = pack2<__half>(pr[2 * b + 1][pn * 2], pr[2 * b + 1][pn * 2 + 1]);
+                    pb[pn][0][0] = pack2<__half>(w[0], w[1]);
+                    pb[pn][1][0] = pack2<__half>(w[2], w[3]);
+                }
+#pragma unroll
+                for (int r = 0; r < (RES ? 2 : 1); ++r) {
+                    pb[pn][0][r] = transpose8(pb[pn][0][r]);
+                    pb[pn][1][r] = transpose8(pb[pn][1][r]);
                 }
             }
 #pragma unroll
@@ -311,38 +317,33 @@ struct QuantPart {
 #pragma unroll
                     for (int r = 0; r < (RES ? 2 : 1); ++r)
 #pragma unroll
-                        for (int pn = 0; pn < NT; ++pn) mma_16816<__half>(acc[2 * i + half][pn], a, pb0[pn][r], pb1[pn][r]);
+                        for (int pn = 0; pn < NT; ++pn)
+                            mma_16816<__half>(acc[2 * i + half][pn], a, pb[pn][0][r], pb[pn][1][r]);
                 }
         }
     }
 
-    // The rows' sums over their lanes; lane t4 == 0 of row g then holds row
-    // 8 pn + g's in l_run[pn].
-    __device__ __forceinline__ void finish() {
-#pragma unroll
-        for (int pn = 0; pn < NT; ++pn) {
-            l_run[pn] += __shfl_xor_sync(0xffffffffu, l_run[pn], 1);
-            l_run[pn] += __shfl_xor_sync(0xffffffffu, l_run[pn], 2);
-        }
-    }
-
     // (m, l) of the heads at ml[head], ml[16 + head]; accumulators at part[head * D + d].
-    __device__ __forceinline__ void store(float *ml, float *part, int G, int lane) const {
+    __device__ __forceinline__ void store(float *ml, float *part, int G, int lane) {
         const int g = lane >> 2, t4 = lane & 3;
 #pragma unroll
-        for (int pn = 0; pn < NT; ++pn) {
-            if (t4 == 0) {
-                ml[pn * 8 + g] = m_run[pn];
-                ml[16 + pn * 8 + g] = l_run[pn];
-            }
-            const int ha = pn * 8 + 2 * t4, hb = ha + 1;
+        for (int pn = 0; pn < NT; ++pn)
 #pragma unroll
-            for (int mt = 0; mt < KT; ++mt) {
-                const int d0 = g * (D / 8) + 2 * mt;
-                if (ha < G) *reinterpret_cast<float2 *>(part + ha * D + d0) = make_float2(acc[mt][pn][0], acc[mt][pn][2]);
-                if (hb < G) *reinterpret_cast<float2 *>(part + hb * D + d0) = make_float2(acc[mt][pn][1], acc[mt][pn][3]);
+            for (int e = 0; e < 2; ++e) {
+                const int head = pn * 8 + 2 * t4 + e;
+                float l = l_run[pn][e];
+#pragma unroll
+                for (int d = 4; d < 32; d *= 2) l += __shfl_xor_sync(0xffffffffu, l, d);
+                if (g == 0) {
+                    ml[head] = m_run[pn][e];
+                    ml[16 + head] = l;
+                }
+                if (head < G)
+#pragma unroll
+                    for (int mt = 0; mt < KT; ++mt)
+                        *reinterpret_cast<float2 *>(part + head * D + g * (D / 8) + 2 * mt) =
+                            make_float2(acc[mt][pn][e], acc[mt][pn][e + 2]);
             }
-        }
     }
 };
 
@@ -351,7 +352,7 @@ __global__ void __launch_bounds__(kQdWarps * 32, NT == 1 ? QuantShape<D, MANY>::
     quant_decode_kernel(const QuantDecodeParams p, const __grid_constant__ CUtensorMap tk,
                         const __grid_constant__ CUtensorMap tv) {
     using Sh = QuantShape<D, MANY>;
-    constexpr int STAGES = Sh::STAGES, STEP = Sh::STEP;
+    constexpr int SLOTS = Sh::SLOTS, STEP = Sh::STEP;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Sh::RING_BYTES);
@@ -361,10 +362,10 @@ __global__ void __launch_bounds__(kQdWarps * 32, NT == 1 ? QuantShape<D, MANY>::
     const int range = blockIdx.x / ranks;
     const int G = p.G, s = range / p.Hkv, h = range - s * p.Hkv;
 
-    uint8_t *wring = smem + warp * STAGES * Sh::STAGE_BYTES;
-    uint64_t *wbar = bars + warp * STAGES;
+    uint8_t *wring = smem + warp * SLOTS * Sh::SLOT_BYTES;
+    uint64_t *wbar = bars + warp * SLOTS;
     if (lane == 0) {
-        for (int st = 0; st < STAGES; ++st) mbar_init(&wbar[st], 1);
+        for (int st = 0; st < SLOTS; ++st) mbar_init(&wbar[st], 1);
         fence_mbar_init();
         if (warp == 0) {
             prefetch_tensormap(&tk);
@@ -392,73 +393,79 @@ __global__ void __launch_bounds__(kQdWarps * 32, NT == 1 ? QuantShape<D, MANY>::
         const bool ok = 32 * k + lane < n && id >= 0 && id < p.num_blocks;
         sc = ok ? __ldg(reinterpret_cast<const float2 *>(p.scales) + (int64_t)id * p.Hkv + h) : make_float2(1.f, 1.f);
     };
-    auto issue = [&](int i) {
-        const int blk = __shfl_sync(0xffffffffu, id, i & 31);
+    const int steps = (n + STEP - 1) / STEP;
+    auto issue = [&](int i) {   // step i's blocks into slot i % SLOTS
+        const int k = min(STEP, n - STEP * i);
+        int blk[STEP];
+#pragma unroll
+        for (int b = 0; b < STEP; ++b) blk[b] = __shfl_sync(0xffffffffu, id, (STEP * i + b) & 31);
         if (lane == 0) {
-            const bool bad = blk < 0 || blk >= p.num_blocks;
-            if (bad) set_status(p.dev_status, PKV_DEV_BAD_BLOCK_ID);
-            // past the end for a bad block id: the load fills zeros
-            constexpr int kRows = D / 8;   // 128-byte rows of a tile
-            const int y = bad ? p.num_blocks * p.Hkv * kRows : (blk * p.Hkv + h) * kRows;
-            uint8_t *slot = wring + (i % STAGES) * Sh::STAGE_BYTES;
-            uint64_t *bar = &wbar[i % STAGES];
-            mbar_arrive_expect_tx(bar, Sh::STAGE_BYTES);
-            tma_load_2d(slot, &tk, 0, y, bar, policy);
-            tma_load_2d(slot + Sh::TILE_BYTES, &tv, 0, y, bar, policy);
+            uint8_t *slot = wring + (i % SLOTS) * Sh::SLOT_BYTES;
+            uint64_t *bar = &wbar[i % SLOTS];
+            mbar_arrive_expect_tx(bar, k * Sh::BLOCK_BYTES);
+#pragma unroll
+            for (int b = 0; b < STEP; ++b) {
+                if (b >= k) break;
+                const bool bad = blk[b] < 0 || blk[b] >= p.num_blocks;
+                if (bad) set_status(p.dev_status, PKV_DEV_BAD_BLOCK_ID);
+                // past the end for a bad block id: the load fills zeros
+                constexpr int kRows = D / 8;   // 128-byte rows of a tile
+                const int y = bad ? p.num_blocks * p.Hkv * kRows : (blk[b] * p.Hkv + h) * kRows;
+                tma_load_2d(slot + b * Sh::BLOCK_BYTES, &tk, 0, y, bar, policy);
+                tma_load_2d(slot + b * Sh::BLOCK_BYTES + Sh::TILE_BYTES, &tv, 0, y, bar, policy);
+            }
         }
     };
     fetch(0);
-    int issued = 0;
-    for (; issued < min(n, STAGES); ++issued) issue(issued);
+    int issued = 0;   // steps
+    for (; issued < min(steps, SLOTS); ++issued) issue(issued);
 
     QuantPart<T, D, NT, MANY, RES> part_w;
     part_w.start(static_cast<const T *>(p.q) + ((int64_t)s * p.Hq + (int64_t)h * G) * D, G, p.scale_log2, lane);
     const uint32_t ring_addr = smem_addr(wring);
+    // entries [full_lo, full_hi) of the list are blocks that are seen whole
+    const int full_lo = ((vis.w0 + 15) >> 4) - vis.skip, full_hi = (vis.ctx >> 4) - vis.skip;
 
-    bool timed_out = false;
-    int i = 0;   // blocks taken
-    while (i < n) {
-        // an odd block out is taken with itself, the second time all hidden
-        const int k = min(STEP, n - i);
-        uint32_t slot[STEP], bits = 0;
+    int i = 0;   // steps taken
+    for (; i < steps; ++i) {
+        const bool ok = mbar_wait(&wbar[i % SLOTS], (uint32_t)(i / SLOTS) & 1u, kQdWaitNs);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        const int v0 = v_lo + warp + kQdWarps * STEP * i;
+        const bool all = v0 >= full_lo && v0 + kQdWarps * (STEP - 1) < min(full_hi, v_hi);
+        uint32_t bits = (uint32_t)((1ull << (16 * STEP)) - 1u);
+        if (!all) {
+            bits = 0;
+#pragma unroll
+            for (int b = 0; b < STEP; ++b)
+                if (STEP * i + b < n) bits |= vis.bits(logical(STEP * i + b), p.sinks) << (16 * b);
+        }
+        // (the 32 blocks of the last step issued, or those before)
+        const bool now = STEP * i / 32 == STEP * (issued - 1) / 32;
         float ks[STEP], vs[STEP];
-        bool ok = true;
 #pragma unroll
         for (int b = 0; b < STEP; ++b) {
-            const int x = i + min(b, k - 1);
-            ok = ok && mbar_wait(&wbar[x % STAGES], (uint32_t)(x / STAGES) & 1u, kQdWaitNs);
-            slot[b] = ring_addr + (x % STAGES) * Sh::STAGE_BYTES;
-            if (b < k) bits |= vis.bits(logical(x), p.sinks) << (16 * b);
-            // (the 32 blocks of the last one issued, or those before)
-            const bool now = x / 32 == (issued - 1) / 32;
-            ks[b] = __shfl_sync(0xffffffffu, now ? sc.x : sc_before.x, x & 31);
-            vs[b] = __shfl_sync(0xffffffffu, now ? sc.y : sc_before.y, x & 31);
+            ks[b] = __shfl_sync(0xffffffffu, now ? sc.x : sc_before.x, (STEP * i + b) & 31);
+            vs[b] = __shfl_sync(0xffffffffu, now ? sc.y : sc_before.y, (STEP * i + b) & 31);
         }
-        if (!__all_sync(0xffffffffu, ok)) {
-            timed_out = true;
-            break;
-        }
-        i += k;
-        part_w.attend(slot, ks, vs, bits, lane, [&] {
+        part_w.attend(ring_addr + (i % SLOTS) * Sh::SLOT_BYTES, ks, vs, bits, all, lane, [&] {
             fence_proxy_async_smem();
             __syncwarp();
-            for (int u = 0; u < k && issued < n; ++u, ++issued) {
-                if ((issued & 31) == 0) fetch(issued / 32);
-                issue(issued);
+            if (issued < steps) {
+                if ((STEP * issued & 31) == 0) fetch(STEP * issued / 32);
+                issue(issued++);
             }
         });
     }
-    if (timed_out) {
+    if (i < steps) {
         if (lane == 0) set_status(p.dev_status, PKV_DEV_WAIT_TIMEOUT);
         // what is still in flight must land before the ring is used again
-        for (int k = i; k < issued; ++k) mbar_wait(&wbar[k % STAGES], (uint32_t)(k / STAGES) & 1u, kQdWaitNs / 8);
+        for (int k = i; k < issued; ++k) mbar_wait(&wbar[k % SLOTS], (uint32_t)(k / SLOTS) & 1u, kQdWaitNs / 8);
     }
 
     // ---- the warps' parts: (m, l) per head, accumulators [warp][head][d] over the ring ----
     __syncthreads();   // every warp is done with its slots
     float *part = reinterpret_cast<float *>(smem);
     const int GD = G * D;
-    part_w.finish();
     part_w.store(ml + warp * 32, part + warp * GD, G, lane);
     __syncthreads();
     float *comb = part + kQdWarps * GD;   // the CTA's accumulators, unnormalised
