@@ -48,6 +48,15 @@ __device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d
 
 __device__ __forceinline__ float2 f16x2_to_f32(uint32_t pair) { return __half22float2(*reinterpret_cast<__half2 *>(&pair)); }
 
+// A 16-bit pair as floats.
+template <typename T>
+__device__ __forceinline__ float2 pair_to_f32(uint32_t w) {
+    if constexpr (std::is_same<T, __nv_bfloat16>::value)
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    else
+        return f16x2_to_f32(w);
+}
+
 // The scale for values of magnitude at most a (finite): the least power of two
 // s >= 2^-60 with a <= 448 s.  448 = 1.75 * 2^8.  A power of two, so that x / s
 // and a later change of scale are exact (short of e4m3's subnormals): e4m3 is

@@ -42,14 +42,6 @@ __device__ __forceinline__ uint32_t finite_max8(uint4 x) {
     return m;
 }
 
-template <typename T>
-__device__ __forceinline__ float2 pair_to_f32(uint32_t w) {
-    if constexpr (std::is_same<T, __nv_bfloat16>::value)
-        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-    else
-        return f16x2_to_f32(w);
-}
-
 // Four codes times r, as codes.
 __device__ __forceinline__ uint32_t rescale4(uint32_t codes, float r) {
     uint32_t a, b;
