@@ -23,7 +23,7 @@ LIB = os.path.join(HERE, "libpkv.so")
 CALLS = os.path.join(HERE, "_torch_calls.so")
 
 SOURCES = ["abi.cu", "append.cu", "decode.cu", "decode_static.cu", "prefill.cu", "prefill_tc.cu", "mixed.cu",
-           "tables.cu", "rope.cu", "window_decode.cu", "window_prefill.cu", "quant_cache.cu", "quant_decode.cu", "quant_attention.cu",
+           "tables.cu", "rope.cu", "window_decode.cu", "window_prefill.cu", "quant_cache.cu", "quant_decode.cu", "quant_prefill.cu",
            "host_sched.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

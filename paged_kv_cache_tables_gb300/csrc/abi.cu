@@ -79,7 +79,7 @@ static PFN_cuTensorMapEncodeTiled_v12000 get_encode_fn() {
 }
 
 int encode_tiled_map(CUtensorMap *map, const void *base, int rank, const uint64_t *dims, const uint64_t *strides,
-                     const uint32_t *box) {
+                     const uint32_t *box, int swizzle_bytes) {
     auto fn = get_encode_fn();
     if (!fn) return cuda_fail_driver(-1, "cuTensorMapEncodeTiled lookup");
     cuuint64_t d[5], st[4];
@@ -91,8 +91,9 @@ int encode_tiled_map(CUtensorMap *map, const void *base, int rank, const uint64_
         if (i + 1 < rank) st[i] = strides[i];
     }
     CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, (cuuint32_t)rank, const_cast<void *>(base), d, st, b, es,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                    CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    swizzle_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return cuda_fail_driver((int)r, "cuTensorMapEncodeTiled");
     return PKV_OK;
 }

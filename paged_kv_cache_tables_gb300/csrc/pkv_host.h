@@ -60,10 +60,10 @@ int decode_attention(void *out, const void *q, const void *k_cache, const void *
 int encode_cache_map(CUtensorMap *map, const void *base, int num_blocks, int num_kv_heads,
                      int block_size, int head_dim);
 
-// Generic 2..5-D tiled TMA descriptor over 16-bit elements with 128-byte
+// Generic 2..5-D tiled TMA descriptor over 16-bit elements with 128-byte (or 64-byte)
 // swizzle; strides in bytes for dims 1..rank-1.  Out-of-range boxes read 0.
 int encode_tiled_map(CUtensorMap *map, const void *base, int rank, const uint64_t *dims, const uint64_t *strides,
-                     const uint32_t *box);
+                     const uint32_t *box, int swizzle_bytes = 128);
 
 // Launches `kernel` on `stream` allowing programmatic dependent launch: it may
 // start while the previous kernel on the stream finishes, and waits for that

@@ -48,6 +48,19 @@ __device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d
 
 __device__ __forceinline__ float2 f16x2_to_f32(uint32_t pair) { return __half22float2(*reinterpret_cast<__half2 *>(&pair)); }
 
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    return v;
+}
+
+// log2 x (hardware approximation).
+__device__ __forceinline__ float log2_approx(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // A 16-bit pair as floats.
 template <typename T>
 __device__ __forceinline__ float2 pair_to_f32(uint32_t w) {
@@ -62,10 +75,10 @@ __device__ __forceinline__ float2 pair_to_f32(uint32_t w) {
 // and a later change of scale are exact (short of e4m3's subnormals): e4m3 is
 // a floating-point format, and loses no precision to the up to one binade of
 // range that a finer scale would use.
-__device__ __forceinline__ float block_scale(float a) {
+__device__ __forceinline__ float block_scale(float a, int least = -60) {
     const uint32_t u = __float_as_uint(a);
     const int e = (int)(u >> 23) - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
-    return __uint_as_float((uint32_t)max(e, 127 - 60) << 23);
+    return __uint_as_float((uint32_t)max(e, 127 + least) << 23);
 }
 
 // What both attention calls refuse.

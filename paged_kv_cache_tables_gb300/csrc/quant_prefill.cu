@@ -1,0 +1,877 @@
+// Prefill attention over the cache held in 8 bits, on the 5th-generation tensor
+// cores (pkv_paged_prefill_attention_e4m3).
+//
+// Mathematics.  As window_prefill.cu, with K_t = k_t a_j and V_t = v_t b_j, k and v
+// the e4m3 codes and a, b the scales of t's page j.  Over key tiles of 128
+// positions:
+//     y_t = scale2 f a_j (q' . k_t) + log2 b_j,   P_t = 2^(y_t - m + 7),
+//     l = l c + sum P_t / b_j,   O = O c + P v,   c = 2^(m_old - m),   out = O / l,
+// m the running maximum of y, moved when it grows by more than 2^8: P stays below
+// 2^15 and about 2^7 for the weight that counts most, whatever the scales are.
+//
+// Both products run on the codes without their scales:
+//   S = q' k^T   in e4m3 (kind::f8f6f4, twice the rate of 16 bits): K goes from the
+//                cache to the tensor cores as it is.  A query row is f times the
+//                sum of e4m3 terms, each the rounding of what the ones before
+//                leave, f the power of two with its largest element in (224, 448]:
+//                two terms hold bf16's 8 bits, three fp16's 11, down to 2^-10 (2^-18
+//                of the largest element at most).  As many steps as in 16 bits, or
+//                one and a half times for fp16.
+//   O += P v     in fp16: v is converted on the way (exact).  P for a bf16 output
+//                is rounded once (2^-11 of a weight, an eighth of what the output's
+//                own rounding may be), else value and residual, two products.
+// (P in e4m3 terms would take three for a bf16 output: more steps than fp16's one,
+// and a conversion of every weight three times instead of V's once a tile.)
+//
+// What is walked, the unit of work and the turns that the two query tiles take:
+// as in window_prefill.cu.  Warps (persistent; 16 of them):
+//   0       TMA and scheduler: takes units, publishes them, loads K and V tiles of
+//           codes, 8 pages of 16, a page one box
+//   1, 2    issue the MMAs of query tile A, B
+//   3       scales of a key tile's pages: a, log2 b, 1 / b
+//   4-11    softmax: a warpgroup a query tile, a row per thread; each row's terms
+//           are made by its thread, the next unit's while the last P V of this one
+//           runs
+//   12-15   V's codes to fp16, in the layout of an MN-major operand; rows that no
+//           row of the unit sees become zero (they may hold NaN codes)
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdio>
+#include <type_traits>
+
+#include "pkv.h"
+#include "pkv_cluster.cuh"
+#include "pkv_device.cuh"
+#include "pkv_host.h"
+#include "pkv_quant.cuh"
+#include "pkv_tc.cuh"
+#include "pkv_window.cuh"
+
+namespace pkv {
+
+constexpr int kQpThreads = 512;
+// registers per thread: the launch gives every thread kQpLaunchRegs; the first and
+// the last warpgroup drop and the two softmax warpgroups rise, by no more in all
+constexpr int kQpLaunchRegs = 128;
+constexpr int kQpLowRegs = 56;
+constexpr int kQpConvertRegs = 72;
+constexpr int kQpHighRegs = 192;
+static_assert(128 * (kQpLowRegs + kQpConvertRegs + 2 * kQpHighRegs) <= kQpThreads * kQpLaunchRegs, "register split");
+constexpr int kQpRows = 128;    // MMA rows = (token, head) pairs per query tile
+constexpr int kQpKeys = 128;    // keys per K/V tile
+constexpr int kQpPages = kQpKeys / 16;
+constexpr int kQpScaleStages = 3;
+constexpr uint64_t kQpWaitNs = 2000000000ull;
+// tensor memory: S / P of query tile t at column 256 t, O at 256 t + 128
+constexpr uint32_t kQpTmemCols = 512;
+
+struct QuantPrefillParams {
+    void *out;
+    const void *q;
+    const float *scales;
+    const int32_t *cu_seqlens;
+    const int32_t *block_tables;
+    const int32_t *context_lens;
+    int *dev_status;
+    int max_blocks, num_blocks, Hq, Hkv, G;
+    int rtok, units_per_seq;
+    int window, sinks, total_q, max_q_len;
+    float scale_log2;
+    bool boxes;   // a warp's 32 rows are whole tokens: tout has a box for them
+};
+
+struct QpUnit : WpUnit {
+    int chunk, sink_pages, skip;   // page v of the list is logical page v, or v + skip from sink_pages on
+};
+
+struct QpBars {
+    uint64_t unit_full[2], unit_empty[2], cancel;
+    uint64_t q_full[2];                                    // per query tile
+    uint64_t k_full[2], k_empty[2];
+    uint64_t codes_full[2], codes_empty[2];                // V's codes
+    uint64_t v_full[2], v_empty[2];                        // V in fp16
+    uint64_t scales_full[kQpScaleStages], scales_empty[kQpScaleStages];
+    uint64_t s_full[2], p_full[2][2], o_done[2];           // per query tile (and part of its keys)
+    uint64_t turn[2];                                      // a query tile's turn at the tensor cores
+};
+
+template <typename T, int D>
+struct QpShape {
+    static constexpr int TERMS = std::is_same<T, __half>::value ? 3 : 2;
+    static constexpr int Q_TERM = kQpRows * D;             // a query tile's codes of one term
+    static constexpr int Q_BYTES = TERMS * Q_TERM;
+    static constexpr int CODE_PAGE = 16 * D;
+    static constexpr int CODE_TILE = kQpPages * CODE_PAGE;
+    // V in fp16: a page after another; a page holds, for each group of 8 rows, the
+    // 64-column halves of those rows, each an 8 x 128-byte swizzle atom
+    static constexpr int HALVES = D / 64;
+    static constexpr int GROUP = HALVES * 1024;            // 8 rows
+    static constexpr int PAGE = 2 * GROUP;
+    static constexpr int TILE = kQpPages * PAGE;
+    static constexpr int FIRST_PART = 2;                   // 32-key groups of P after which P V may start
+    static constexpr int OFF_Q = 0;                        // tile A, then tile B
+    static constexpr int OFF_K = 2 * Q_BYTES;
+    static constexpr int OFF_CODES = OFF_K + 2 * CODE_TILE;
+    static constexpr int OFF_V = OFF_CODES + 2 * CODE_TILE;
+    static constexpr int OFF_OUT = OFF_V + 2 * TILE;       // outputs on their way out: 128 bytes of 32 rows a warp
+    // where there is no room for them, the warp's rows of the query's first term
+    // take them, and the next unit's terms are made behind them
+    static constexpr bool OWN_OUT = !(TERMS == 3 && D == 128);
+    static constexpr int OFF_SCALES = OFF_OUT + (OWN_OUT ? 8 * 4096 : 0);
+    static constexpr int OFF_CANCEL = OFF_SCALES + kQpScaleStages * kQpPages * 16;
+    static constexpr int OFF_UNIT = OFF_CANCEL + 16;
+    static constexpr int OFF_BAR = (OFF_UNIT + 2 * (int)sizeof(QpUnit) + 7) & ~7;
+    static constexpr int SMEM_BYTES = 1024 + OFF_BAR + (int)sizeof(QpBars) + 16;
+};
+static_assert(QpShape<__nv_bfloat16, 128>::SMEM_BYTES <= 227 * 1024 && QpShape<__half, 128>::SMEM_BYTES <= 227 * 1024,
+              "shared memory");
+
+// One page of codes (see encode_code_page_map) into shared memory.
+__device__ __forceinline__ void load_code_page(void *dst, const CUtensorMap *map, int row, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(smem_addr(bar))
+        : "memory");
+}
+
+// Byte offset of 16-byte piece c of row r in a tile of codes (K-major operand;
+// 128-byte rows under 128-byte swizzle, 64-byte rows under 64-byte swizzle).
+template <int D>
+__device__ __forceinline__ uint32_t code_piece(int r, int c) {
+    return D == 128 ? (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)) : (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+}
+
+// WIDE: a 32-bit output.  RES: weights as value and residual.  TILES: query tiles
+// of a unit, 2, or 1 (A alone)
+template <typename T, int D, bool WIDE, bool RES, int TILES>
+__global__ void __launch_bounds__(kQpThreads, 1)
+    quant_prefill_kernel(const QuantPrefillParams p, const __grid_constant__ CUtensorMap tk,
+                         const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tout) {
+    using Sh = QpShape<T, D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    QpBars *bars = reinterpret_cast<QpBars *>(sm + Sh::OFF_BAR);
+    QpUnit *units = reinterpret_cast<QpUnit *>(sm + Sh::OFF_UNIT);
+    float4 *page_scales = reinterpret_cast<float4 *>(sm + Sh::OFF_SCALES);   // [stage][page] a, log2 b, 1 / b
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 1);
+    volatile int *gave_up = reinterpret_cast<volatile int *>(tmem_slot + 1);   // a wait of this CTA ran out
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars->unit_full[i], 1);
+            mbar_init(&bars->unit_empty[i], 5 * TILES + 5);   // issuers and softmax of each tile, scales, converters
+            mbar_init(&bars->q_full[i], 4);
+            mbar_init(&bars->k_full[i], 1);
+            mbar_init(&bars->k_empty[i], TILES);
+            mbar_init(&bars->codes_full[i], 1);
+            mbar_init(&bars->codes_empty[i], 4);
+            mbar_init(&bars->v_full[i], 4);
+            mbar_init(&bars->v_empty[i], TILES);
+            mbar_init(&bars->s_full[i], 1);
+            mbar_init(&bars->p_full[i][0], 4);
+            mbar_init(&bars->p_full[i][1], 4);
+            mbar_init(&bars->o_done[i], 1);
+            mbar_init(&bars->turn[i], 1);
+        }
+        for (int i = 0; i < kQpScaleStages; ++i) {
+            mbar_init(&bars->scales_full[i], 1);
+            mbar_init(&bars->scales_empty[i], 4 * TILES);
+        }
+        mbar_init(&bars->cancel, 1);
+        *gave_up = 0;
+        fence_mbar_init();
+        prefetch_tensormap(&tk);
+        prefetch_tensormap(&tv);
+    }
+    if (warp == 1) {
+        tc::tmem_alloc(tmem_slot, kQpTmemCols);
+        tc::tmem_relinquish();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t sbase = smem_addr(sm);
+    // inputs may come from the previous kernel on the stream (the append)
+    pdl_wait_primary();
+    pdl_launch_dependents();
+
+    // A wait that gives up after kQpWaitNs, or once another one of the CTA has.
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+        if (mbar_try_wait(bar, parity & 1u)) return true;
+        const uint64_t t0 = global_timer_ns();
+        while (!mbar_try_wait(bar, parity & 1u)) {
+            if (*gave_up) return false;
+            if (global_timer_ns() - t0 > kQpWaitNs) {
+                *gave_up = 1;
+                set_status(p.dev_status, PKV_DEV_WAIT_TIMEOUT);
+                return false;
+            }
+        }
+        return true;
+    };
+    auto wait_all = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)); };
+    // the n-th unit, once it is published; whether there is one
+    auto take_unit = [&](int n, QpUnit &u) {
+        const bool ok = wait_all(&bars->unit_full[n & 1], (uint32_t)(n / 2));
+        if (!ok) return false;
+        u = units[n & 1];
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive_cta(&bars->unit_empty[n & 1]);
+        return u.tiles > 0;
+    };
+    // the block id of page v of a unit's list; -1: none is wanted there
+    auto page_id = [&](const QpUnit &u, int v) {
+        if (16 * v >= u.ctx) return -1;
+        return __ldg(p.block_tables + (int64_t)u.chunk * p.max_blocks + (v < u.sink_pages ? v : v + u.skip));
+    };
+
+    if (warp < 4) {
+        tc::setmaxnreg_dec<kQpLowRegs>();
+        if (warp == 0) {
+            // ---------------- scheduler and TMA producer ----------------
+            int place = blockIdx.x;
+            int n = 0;              // units published
+            uint32_t g = 0;         // key tiles loaded
+            uint32_t asked = 0;     // places asked for
+            bool ok = true;
+            bool asking = false;
+            auto ask = [&]() {
+                if (!asking && lane == 0) {
+                    mbar_arrive_expect_tx(&bars->cancel, 16);
+                    cancel_next_cta(sm + Sh::OFF_CANCEL, &bars->cancel);
+                }
+                asked += !asking;
+                asking = true;
+            };
+            while (ok) {
+                // place -> unit; chunk by chunk, the last pair of tiles first, the KV heads side by side
+                const int h = place % p.Hkv;
+                const int rest = place / p.Hkv;
+                const int unit = p.units_per_seq - 1 - rest % p.units_per_seq;
+                const int c = rest / p.units_per_seq;
+                const int q0 = __ldg(p.cu_seqlens + c);
+                const int q_len = __ldg(p.cu_seqlens + c + 1) - q0;
+                const int ctx = __ldg(p.context_lens + c);
+                const int i0 = unit * TILES * p.rtok;
+                int bad = 0;
+                // (rows past max_q_len have no unit)
+                if (q_len < 0 || q_len > ctx || q_len > p.max_q_len || q0 < 0 || q_len > p.total_q - q0)
+                    bad = PKV_DEV_BAD_CHUNK;
+                else if (ctx > p.max_blocks * 16)
+                    bad = PKV_DEV_BAD_CONTEXT;
+                if (bad && unit == 0 && lane == 0) set_status(p.dev_status, bad);
+                if (!bad && i0 < q_len) {
+                    QpUnit u = {};
+                    u.h = h;
+                    u.chunk = c;
+                    u.row0 = q0 + i0;
+                    u.tokens = min(TILES * p.rtok, q_len - i0);
+                    u.first = ctx - q_len + i0;
+                    u.wpos = max(u.first - p.window + 1, 0);
+                    u.sink_pages = min((p.sinks + 15) / 16, (ctx + 15) / 16);
+                    u.skip = max(u.wpos / 16 - u.sink_pages, 0);
+                    u.first -= 16 * u.skip;
+                    u.wpos -= 16 * u.skip;
+                    u.ctx = ctx - 16 * u.skip;
+                    u.tiles = (u.first + u.tokens - 1) / kQpKeys + 1;
+                    if (n >= 2) ok = wait_all(&bars->unit_empty[n & 1], (uint32_t)(n / 2 - 1));
+                    if (!ok) break;
+                    if (lane == 0) {
+                        units[n & 1] = u;
+                        tc::mbar_arrive_cta(&bars->unit_full[n & 1]);
+                    }
+                    // lane i < 8 reads the block id of page i of the tile, one tile ahead
+                    int blk_next = lane < kQpPages ? page_id(u, lane) : -1;
+                    for (int j = 0; ok && j < u.tiles; ++j, ++g) {
+                        // the next place is asked for near the unit's end (see window_prefill.cu)
+                        if (j + 2 >= u.tiles) ask();
+                        const int blk = blk_next;
+                        const int v = j * kQpPages + lane;
+                        if (j + 1 < u.tiles) blk_next = lane < kQpPages ? page_id(u, v + kQpPages) : -1;
+                        int y = p.num_blocks * p.Hkv * 16;     // row past the pool: zero fill
+                        if (lane < kQpPages && 16 * v < u.ctx) {
+                            if (blk >= 0 && blk < p.num_blocks)
+                                y = (blk * p.Hkv + h) * 16;
+                            else
+                                set_status(p.dev_status, PKV_DEV_BAD_BLOCK_ID);
+                        }
+                        const int st = (int)(g & 1);
+                        uint8_t *kd = sm + Sh::OFF_K + st * Sh::CODE_TILE, *vd = sm + Sh::OFF_CODES + st * Sh::CODE_TILE;
+                        // a K slot is free once both S products of its last tile are done
+                        if (g >= 2) ok = wait_all(&bars->k_empty[st], g / 2 - 1);
+                        if (ok) {
+                            if (lane == 0) mbar_arrive_expect_tx(&bars->k_full[st], Sh::CODE_TILE);
+                            __syncwarp();
+                            if (lane < kQpPages) load_code_page(kd + lane * Sh::CODE_PAGE, &tk, y, &bars->k_full[st]);
+                        }
+                        // a slot of V's codes once they have been converted
+                        if (ok && g >= 2) ok = wait_all(&bars->codes_empty[st], g / 2 - 1);
+                        if (ok) {
+                            if (lane == 0) mbar_arrive_expect_tx(&bars->codes_full[st], Sh::CODE_TILE);
+                            __syncwarp();
+                            if (lane < kQpPages) load_code_page(vd + lane * Sh::CODE_PAGE, &tv, y, &bars->codes_full[st]);
+                        }
+                    }
+                    ++n;
+                }
+                if (!ok) break;
+                ask();
+                ok = wait_all(&bars->cancel, asked - 1);
+                if (!ok) break;
+                asking = false;
+                place = cancelled_cta(sm + Sh::OFF_CANCEL);
+                fence_proxy_async_smem();   // the answer is read before the next one is written
+                __syncwarp();
+                if (place < 0) break;
+            }
+            // no more units (after a wait that ran out the others leave by themselves)
+            if (ok && n >= 2) ok = wait_all(&bars->unit_empty[n & 1], (uint32_t)(n / 2 - 1));
+            if (ok && lane == 0) {
+                units[n & 1].tiles = 0;
+                tc::mbar_arrive_cta(&bars->unit_full[n & 1]);
+            }
+            if (!ok && lane == 0) {
+                // what is under way must land before the CTA leaves
+                if (asking) mbar_wait(&bars->cancel, (asked - 1) & 1u, kQpWaitNs / 8);
+                for (int st = 0; st < 2; ++st) {
+                    if (g > (uint32_t)st) {
+                        const uint32_t last = (g - 1 - st) / 2;
+                        mbar_wait(&bars->k_full[st], last & 1u, kQpWaitNs / 8);
+                        mbar_wait(&bars->codes_full[st], last & 1u, kQpWaitNs / 8);
+                    }
+                }
+            }
+        } else if (warp < 3) {
+            // ---------------- MMA issuer of query tile t ----------------
+            // The whole warp walks the schedule, so the waits and the
+            // descriptor arithmetic are warp-uniform; one elected lane issues
+            // each MMA and commit.
+            const int t = warp - 1;
+            const bool leader = tc::elect_one();
+            constexpr uint32_t idesc_s = tc::idesc_e4m3(kQpRows, kQpKeys);
+            constexpr uint32_t idesc_o = tc::idesc_f16(false, false, true, kQpRows, D);
+            const uint32_t d_s = tmem + t * 256, d_o = d_s + 128;
+            auto code_desc = [&](uint32_t at) { return D == 128 ? tc::smem_desc_sw128(at, 16, 1024) : tc::smem_desc_sw64(at, 16, 512); };
+            const uint64_t q_desc = code_desc(sbase + Sh::OFF_Q + t * Sh::Q_BYTES);
+            const uint64_t k_desc = code_desc(sbase + Sh::OFF_K);
+            const uint64_t v_desc = tc::smem_desc_sw128(sbase + Sh::OFF_V, 1024, Sh::GROUP);
+            uint32_t g = 0;     // key tiles done
+            // The two tiles take turns: P V of a key tile and S of the next are
+            // one turn, so that a tile's softmax runs beside the other's turn.
+            auto pass_turn = [&]() {
+                if (TILES == 2 && lane == 0) tc::mbar_arrive_cta(&bars->turn[1 - t]);
+            };
+            auto issue_s = [&](uint32_t k, bool pass) {   // S = Q K^T of key tile k
+                if (!wait_all(&bars->k_full[k & 1], k / 2)) return false;
+                tc::fence_after_sync();
+                const uint64_t kb = k_desc + (uint64_t)(((k & 1) * Sh::CODE_TILE) >> 4);
+                constexpr int STEPS = D / 32;
+#pragma unroll
+                for (int i = 0; i < Sh::TERMS * STEPS; ++i) {
+                    const uint32_t qo = ((i / STEPS) * Sh::Q_TERM + (i % STEPS) * 32) >> 4, ko = ((i % STEPS) * 32) >> 4;
+                    if (pass && i == Sh::TERMS * STEPS - 2) pass_turn();   // on its way while the rest is issued
+                    if (leader) tc::mma_f8_ss(d_s, q_desc + qo, kb + ko, idesc_s, i > 0);
+                }
+                if (leader) {
+                    tc::mma_commit(&bars->s_full[t]);
+                    tc::mma_commit(&bars->k_empty[k & 1]);
+                }
+                return true;
+            };
+            QpUnit u;
+            for (int n = 0; t < TILES; ++n) {
+                if (!take_unit(n, u)) break;
+                const int tiles = u.tiles;
+                // (S may be written: the product that read P over it was issued before)
+                bool ok = wait_all(&bars->q_full[t], (uint32_t)n) && issue_s(g, false);
+                for (int j = 0; ok && j < tiles; ++j, ++g) {
+                    const uint64_t vb = v_desc + (uint64_t)(((g & 1) * Sh::TILE) >> 4);
+                    ok = wait_all(&bars->v_full[g & 1], g / 2);
+                    if (TILES == 2 && (t == 1 || g > 0)) ok = ok && wait_all(&bars->turn[t], t == 1 ? g : g - 1);
+#pragma unroll
+                    for (int part = 0; part < 2; ++part) {
+                        // P of a unit's first tile is there only after the unit before's O was read
+                        ok = ok && wait_all(&bars->p_full[t][part], g);
+                        if (!ok) break;
+                        tc::fence_after_sync();
+#pragma unroll
+                        for (int kk = part ? 2 * Sh::FIRST_PART : 0; kk < (part ? kQpPages : 2 * Sh::FIRST_PART); ++kk) {
+                            // O (+)= P V, a page at a time
+                            const uint32_t ph = d_s + 32 * (kk >> 1) + 8 * (kk & 1);
+                            const uint64_t vp = vb + (uint32_t)(kk * Sh::PAGE >> 4);
+                            if (leader) {
+                                tc::mma_f16_ts(d_o, ph, vp, idesc_o, j > 0 || kk > 0);
+                                if (RES) tc::mma_f16_ts(d_o, ph + 16, vp, idesc_o, true);   // the weights' rounding residual
+                            }
+                        }
+                    }
+                    if (!ok) break;
+                    if (leader) {
+                        tc::mma_commit(&bars->v_empty[g & 1]);
+                        if (j + 1 == tiles) tc::mma_commit(&bars->o_done[t]);
+                    }
+                    if (j + 1 < tiles)
+                        ok = issue_s(g + 1, true);
+                    else
+                        pass_turn();
+                }
+                if (!ok) break;
+            }
+        } else {
+            // ---------------- scales of a key tile's pages ----------------
+            uint32_t g = 0;
+            bool ok = true;
+            QpUnit u;
+            for (int n = 0; ok && take_unit(n, u); ++n) {
+                auto fetch = [&](int j) {
+                    const int id = lane < kQpPages && j < u.tiles ? page_id(u, j * kQpPages + lane) : -1;
+                    if (id < 0 || id >= p.num_blocks) return make_float2(1.f, 1.f);
+                    return __ldg(reinterpret_cast<const float2 *>(p.scales) + (int64_t)id * p.Hkv + u.h);
+                };
+                float2 next = fetch(0);
+                for (int j = 0; ok && j < u.tiles; ++j, ++g) {
+                    const float2 sc = next;
+                    next = fetch(j + 1);
+                    const int st = (int)(g % kQpScaleStages);
+                    if (g >= kQpScaleStages) ok = wait_all(&bars->scales_empty[st], g / kQpScaleStages - 1);
+                    if (!ok) break;
+                    const float lb = log2_approx(sc.y);
+                    if (lane < kQpPages) page_scales[st * kQpPages + lane] = make_float4(sc.x, lb, exp2_approx(-lb), 0.f);
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive_cta(&bars->scales_full[st]);
+                }
+            }
+        }
+    } else if (warp >= 12) {
+        tc::setmaxnreg_dec<kQpConvertRegs>();
+        // ---------------- V's codes to fp16 ----------------
+        // A warp takes 32 rows, 8 rows x 4 pieces of 16 codes at a time, each lane a
+        // piece; the rows of lanes k and k + 4 differ in their lowest and third bit,
+        // so that neither the loads nor the stores meet a bank twice.
+        const int piece = lane & 3, k = lane >> 2;
+        const int row = (k >> 1) ^ ((k & 1) * 5);
+        uint32_t g = 0;
+        bool ok = true;
+        QpUnit u;
+        for (int n = 0; ok && take_unit(n, u); ++n) {
+            for (int j = 0; ok && j < u.tiles; ++j, ++g) {
+                const int st = (int)(g & 1);
+                ok = wait_all(&bars->codes_full[st], g / 2);
+                if (g >= 2) ok = ok && wait_all(&bars->v_empty[st], g / 2 - 1);
+                if (!ok) break;
+                const uint32_t from = sbase + Sh::OFF_CODES + st * Sh::CODE_TILE;
+                const uint32_t to = sbase + Sh::OFF_V + st * Sh::TILE;
+                const WpHidden hid(u, j * kQpKeys, p.sinks, kQpKeys);
+                const bool any = hid.any();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r0 = (warp - 12) * 32 + i * 8, r = r0 + row;
+                    const bool gone = any && hid.has(r);
+#pragma unroll
+                    for (int hf = 0; hf < Sh::HALVES; ++hf) {
+                        uint4 c = lds128(from + code_piece<D>(r, 4 * hf + piece));
+                        if (gone) c = make_uint4(0u, 0u, 0u, 0u);
+                        uint4 lo, hi;
+                        e4m3x4_to_f16x4(c.x, lo.x, lo.y);
+                        e4m3x4_to_f16x4(c.y, lo.z, lo.w);
+                        e4m3x4_to_f16x4(c.z, hi.x, hi.y);
+                        e4m3x4_to_f16x4(c.w, hi.z, hi.w);
+                        const uint32_t at = to + (r0 >> 3) * Sh::GROUP + hf * 1024 + row * 128;
+                        st_shared_v4(at + (((2 * piece) ^ row) << 4), lo);
+                        st_shared_v4(at + (((2 * piece + 1) ^ row) << 4), hi);
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    tc::mbar_arrive_cta(&bars->v_full[st]);
+                    tc::mbar_arrive_cta(&bars->codes_empty[st]);
+                }
+            }
+        }
+    } else {
+        tc::setmaxnreg_inc<kQpHighRegs>();
+        // ---------------- softmax: tile t, one row per thread ----------------
+        const int t = (warp - 4) >> 2;
+        const int lane_base = 32 * (warp & 3);          // tensor-memory lanes this warp may touch
+        const int r = lane_base + lane;                 // row within the tile
+        const uint32_t scol = tmem + ((uint32_t)lane_base << 16) + t * 256;   // the scores, then P
+        const uint32_t ocol = scol + 128;
+        const int tok = t * p.rtok + r / p.G, head = r % p.G;
+        // this row's query as terms; what its scores are multiplied by
+        auto split_query = [&](const QpUnit &u) {
+            uint4 x[D / 8];
+            const bool valid = r < p.G * p.rtok && tok < u.tokens;
+            const uint4 *from = reinterpret_cast<const uint4 *>(
+                static_cast<const T *>(p.q) + ((int64_t)(u.row0 + tok) * p.Hq + (int64_t)u.h * p.G + head) * D);
+            uint32_t top2 = 0;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                x[i] = valid ? __ldg(from + i) : make_uint4(0u, 0u, 0u, 0u);
+                top2 = __vmaxu2(top2, __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
+                                               __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu)));
+            }
+            const uint32_t top = max(top2 & 0xffffu, top2 >> 16);
+            const bool finite = top < (std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u);
+            const float s = block_scale(finite ? pair_to_f32<T>(top).x : 0.f, -126);
+            const float inv = 1.f / s;
+            const uint32_t to = sbase + Sh::OFF_Q + t * Sh::Q_BYTES;
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+                float v[16];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const uint4 w = x[2 * c + e];
+                    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 f = pair_to_f32<T>(ww[i]);
+                        v[8 * e + 2 * i] = f.x * inv;
+                        v[8 * e + 2 * i + 1] = f.y * inv;
+                    }
+                }
+#pragma unroll
+                for (int term = 0; term < Sh::TERMS; ++term) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        w[i] = to_e4m3x4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                        uint32_t a, b;
+                        e4m3x4_to_f16x4(w[i], a, b);
+                        const float2 fa = f16x2_to_f32(a), fb = f16x2_to_f32(b);
+                        v[4 * i] -= fa.x;
+                        v[4 * i + 1] -= fa.y;
+                        v[4 * i + 2] -= fb.x;
+                        v[4 * i + 3] -= fb.y;
+                    }
+                    st_shared_v4(to + term * Sh::Q_TERM + code_piece<D>(r, c), make_uint4(w[0], w[1], w[2], w[3]));
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive_cta(&bars->q_full[t]);
+            // (a query that is not finite has no finite output)
+            return (finite ? s : __uint_as_float(0x7fffffffu)) * p.scale_log2;
+        };
+        uint32_t g = 0;                                 // key tiles taken
+        QpUnit u;
+        bool ok = t < TILES && take_unit(0, u);
+        float rowscale = 0.f;
+        if (ok) rowscale = split_query(u);
+        for (int n = 0; ok; ++n) {
+            const bool valid = r < p.G * p.rtok && tok < u.tokens;
+            const int pos = u.first + (valid ? tok : u.tokens - 1);   // padding rows see the last row's keys
+            float m_used = -INFINITY, l = 0.f;
+            for (int j = 0; j < u.tiles; ++j, ++g) {
+                const int st = (int)(g % kQpScaleStages);
+                ok = wait_all(&bars->scales_full[st], g / kQpScaleStages) && wait_all(&bars->s_full[t], g);
+                if (!ok) break;
+                tc::fence_after_sync();
+                const int key0 = j * kQpKeys;
+                float v[kQpKeys];
+#pragma unroll
+                for (int cc = 0; cc < kQpKeys; cc += 32) tc::tmem_ld32(scol + cc, *reinterpret_cast<float(*)[32]>(v + cc));
+                tc::tmem_wait_ld();
+                // hidden: past the row's position; below its window and behind the first tokens
+                const int lim = pos - key0, low = lim - p.window + 1, sk = p.sinks - key0;
+                if (__any_sync(0xffffffffu, lim < kQpKeys - 1 || (low > 0 && sk < kQpKeys))) {
+                    auto below = [](int n) { return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u); };
+#pragma unroll
+                    for (int cc = 0; cc < kQpKeys; cc += 32) {
+                        const uint32_t see = below(lim + 1 - cc) & (~below(low - cc) | below(sk - cc));
+                        if (__any_sync(0xffffffffu, see != 0xffffffffu)) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (!(see & (1u << e))) v[cc + e] = -INFINITY;
+                        }
+                    }
+                }
+                // y = v f + lb with f, lb of the key's page; f > 0, so a page's largest y is its largest v's
+                float f[kQpPages], lb[kQpPages];
+                float mx = -INFINITY;
+#pragma unroll
+                for (int pg = 0; pg < kQpPages; ++pg) {
+                    const float4 sc = page_scales[st * kQpPages + pg];
+                    f[pg] = sc.x * rowscale;
+                    lb[pg] = sc.y;
+                    float a = fmaxf(v[16 * pg], v[16 * pg + 1]), b = fmaxf(v[16 * pg + 2], v[16 * pg + 3]);
+#pragma unroll
+                    for (int e = 4; e < 16; e += 4) {
+                        a = fmax3(a, v[16 * pg + e], v[16 * pg + e + 1]);
+                        b = fmax3(b, v[16 * pg + e + 2], v[16 * pg + e + 3]);
+                    }
+                    mx = fmaxf(mx, fmaf(fmaxf(a, b), f[pg], lb[pg]));
+                }
+                const bool first = m_used == -INFINITY;
+                const float m_new = fmaxf(m_used, mx);
+                const bool rescale = !first && m_new > m_used + 8.f;
+                const float alpha = rescale ? exp2_approx(m_used - m_new) : 1.f;
+                if (first || rescale) m_used = m_new;
+                // O was last written by the P V product before, which the tensor
+                // core finished before this tile's S (issued after it) completed
+                if (__any_sync(0xffffffffu, rescale)) {
+#pragma unroll 1
+                    for (int cc = 0; cc < D; cc += 32) {
+                        float o[32];
+                        tc::tmem_ld32(ocol + cc, o);
+                        tc::tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] *= alpha;
+                        tc::tmem_st32(ocol + cc, o);
+                    }
+                }
+                // P = 2^(y - m_used + 7) over the same columns, 32 keys at a time: 16
+                // columns of rounded pairs (then 16 of residual pairs).
+                // A row that has seen no key yet has nothing to subtract.
+                const float off = (m_used == -INFINITY ? 0.f : m_used) - 7.f;
+                l *= alpha;
+#pragma unroll
+                for (int cc = 0; cc < kQpKeys / 32; ++cc) {
+                    uint32_t hi[16], lo[16];
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const int pg = 2 * cc + half;
+                        const uint64_t f2 = f2_pack(f[pg], f[pg]), c2 = f2_pack(lb[pg] - off, lb[pg] - off);
+                        uint64_t sum2 = f2_pack(0.f, 0.f);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            float a, b;
+                            f2_unpack(f2_fma(f2_pack(v[16 * pg + 2 * e], v[16 * pg + 2 * e + 1]), f2, c2), a, b);
+                            a = exp2_approx(a);
+                            b = exp2_approx(b);
+                            const uint64_t ab = f2_pack(a, b);
+                            sum2 = f2_add(sum2, ab);
+                            if constexpr (RES)
+                                pack2_split2<__half>(ab, a, b, hi[8 * half + e], lo[8 * half + e]);
+                            else
+                                hi[8 * half + e] = pack2<__half>(a, b);
+                        }
+                        float s0, s1;
+                        f2_unpack(sum2, s0, s1);
+                        l = fmaf(s0 + s1, page_scales[st * kQpPages + pg].z, l);
+                    }
+                    tc::tmem_st16(scol + cc * 32, hi);
+                    if constexpr (RES) tc::tmem_st16(scol + cc * 32 + 16, lo);
+                    if (cc == Sh::FIRST_PART - 1 || cc == 3) {   // a part of P is ready
+                        tc::tmem_wait_st();
+                        tc::fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) tc::mbar_arrive_cta(&bars->p_full[t][cc == 3]);
+                    }
+                }
+                if (lane == 0) tc::mbar_arrive_cta(&bars->scales_empty[st]);
+            }
+            if (!ok) break;
+            // the next unit's query: this one's S products are done
+            QpUnit u_next;
+            bool more = false;
+            float rowscale_next = 0.f;
+            if constexpr (Sh::OWN_OUT) {
+                more = take_unit(n + 1, u_next);
+                if (more) rowscale_next = split_query(u_next);
+            }
+            ok = wait_all(&bars->o_done[t], (uint32_t)n);
+            if (!ok) break;
+            tc::fence_after_sync();
+            const float inv = 1.f / l;
+            // 128 bytes of each row at a time, through shared memory (see window_prefill.cu)
+            constexpr int kCols = WIDE ? 32 : 64;      // a 32-bit output or a 16-bit one
+            constexpr int kSize = WIDE ? 4 : 2;
+            const int64_t at = valid ? ((int64_t)(u.row0 + tok) * p.Hq + (int64_t)u.h * p.G + head) * D * kSize : -1;
+            uint8_t *stage = Sh::OWN_OUT ? sm + Sh::OFF_OUT + (warp - 4) * 4096
+                                         : sm + Sh::OFF_Q + t * Sh::Q_BYTES + (warp & 3) * 4096;
+            const bool box = !WIDE && p.boxes && __all_sync(0xffffffffu, valid);
+#pragma unroll 1
+            for (int cc = 0; cc < D; cc += kCols) {
+                float v[kCols];
+#pragma unroll
+                for (int e = 0; e < kCols; e += 32) tc::tmem_ld32(ocol + cc + e, *reinterpret_cast<float(*)[32]>(v + e));
+                tc::tmem_wait_ld();
+                if (lane == 0) stores_read();
+                __syncwarp();
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    uint4 w;
+                    if constexpr (WIDE)
+                        w = make_uint4(__float_as_uint(v[4 * e] * inv), __float_as_uint(v[4 * e + 1] * inv),
+                                       __float_as_uint(v[4 * e + 2] * inv), __float_as_uint(v[4 * e + 3] * inv));
+                    else
+                        w = make_uint4(pack2<T>(v[8 * e] * inv, v[8 * e + 1] * inv),
+                                       pack2<T>(v[8 * e + 2] * inv, v[8 * e + 3] * inv),
+                                       pack2<T>(v[8 * e + 4] * inv, v[8 * e + 5] * inv),
+                                       pack2<T>(v[8 * e + 6] * inv, v[8 * e + 7] * inv));
+                    *reinterpret_cast<uint4 *>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) = w;
+                }
+                if (box) {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) store_rows(&tout, stage, cc, u.h * p.G, u.row0 + tok);
+                    continue;
+                }
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int row = 4 * i + (lane >> 3);
+                    const uint4 w = *reinterpret_cast<const uint4 *>(stage + row * 128 + (((lane ^ row) & 7) << 4));
+                    const int64_t to = __shfl_sync(0xffffffffu, at, row);
+                    if (to >= 0) *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.out) + to + cc * kSize + (lane & 7) * 16) = w;
+                }
+                __syncwarp();
+            }
+            // O has been read: ordered before this unit's successor's P, whose
+            // arrival lets the tensor core write O again
+            tc::fence_before_sync();
+            if constexpr (!Sh::OWN_OUT) {
+                more = take_unit(n + 1, u_next);
+                if (lane == 0) stores_read();
+                __syncwarp();
+                if (more) rowscale_next = split_query(u_next);
+            }
+            if (!more) break;
+            u = u_next;
+            rowscale = rowscale_next;
+        }
+        if (lane == 0) stores_done();
+    }
+
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == 1) {
+        tc::fence_after_sync();
+        tc::tmem_dealloc(tmem, kQpTmemCols);
+    }
+}
+
+// A cache of codes as rows of head_dim bytes, a (block, KV head) page of 16 a box.
+// Rows past the pool read 0.
+static int encode_code_page_map(CUtensorMap *map, const void *base, int num_blocks, int num_kv_heads, int head_dim) {
+    const uint64_t dims[2] = {(uint64_t)head_dim / 2, (uint64_t)num_blocks * num_kv_heads * 16};   // in 16-bit elements
+    const uint64_t strides[1] = {(uint64_t)head_dim};
+    const uint32_t box[2] = {(uint32_t)head_dim / 2, 16};
+    return encode_tiled_map(map, base, 2, dims, strides, box, head_dim);
+}
+
+template <typename T, int D, bool WIDE, bool RES, int TILES>
+static int launch_quant_prefill(const QuantPrefillParams &prm, const CUtensorMap &tk, const CUtensorMap &tv,
+                                const CUtensorMap &tout, int grid, cudaStream_t stream) {
+    using Sh = QpShape<T, D>;
+    const auto kernel = quant_prefill_kernel<T, D, WIDE, RES, TILES>;
+    // the register split inside the kernel waits for registers that only exist
+    // if the compiled count is the one it was sized for: check it (once; the
+    // answer does not change) and refuse to launch otherwise
+    static int regs_ok = 0;   // 0 unknown, 1 as sized, -1 not
+    if (regs_ok == 0) {
+        cudaFuncAttributes fa;
+        cudaError_t e = cudaFuncGetAttributes(&fa, kernel);
+        if (e != cudaSuccess) return cuda_fail(e);
+        regs_ok = fa.numRegs == kQpLaunchRegs ? 1 : -1;
+        if (regs_ok < 0) {
+            char msg[128];
+            std::snprintf(msg, sizeof msg, "8-bit prefill kernel compiled to %d registers per thread, its split needs %d",
+                          fa.numRegs, kQpLaunchRegs);
+            set_error_message(msg);
+        }
+    }
+    if (regs_ok < 0) return PKV_ERR_UNSUPPORTED;
+    static unsigned long long attr_set = 0;   // per instantiation and device
+    if (!done_on_device(&attr_set)) {
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::SMEM_BYTES);
+        if (e != cudaSuccess) return cuda_fail(e);
+        mark_done_on_device(&attr_set);
+    }
+    cudaError_t e = launch_pdl(kernel, dim3(grid), dim3(kQpThreads), Sh::SMEM_BYTES, stream, prm, tk, tv, tout);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    return e == cudaSuccess ? PKV_OK : cuda_fail(e);
+}
+
+}  // namespace pkv
+
+extern "C" int pkv_paged_prefill_attention_e4m3(void *out, const void *q, const int32_t *cu_seqlens, int num_seqs, int max_q_len,
+                                                int total_q, const void *k_cache, const void *v_cache, const float *kv_scales,
+                                                const int32_t *block_tables, int max_blocks_per_seq,
+                                                const int32_t *context_lens, int num_blocks, int num_q_heads, int num_kv_heads,
+                                                int head_dim, int block_size, int window, int num_sinks, float scale, int dtype,
+                                                int out_dtype, int *dev_status, void *stream) {
+    pkv::NvtxRange nvtx_range("pkv_paged_prefill_attention_e4m3");
+    using namespace pkv;
+    if (max_q_len < 0 || total_q < 0) return PKV_ERR_INVALID_ARG;
+    int rc = quant_attention_refusal(num_seqs, num_blocks, num_q_heads, num_kv_heads, head_dim, block_size, max_blocks_per_seq,
+                                     window, num_sinks, scale, dtype, out_dtype);
+    if (rc != PKV_OK) return rc;
+    if (num_seqs == 0 || max_q_len == 0 || total_q == 0) return PKV_OK;
+    if (!out || !q || !cu_seqlens || !k_cache || !v_cache || !kv_scales || !block_tables || !context_lens)
+        return PKV_ERR_INVALID_ARG;
+    // query rows are read and output rows stored as 16-byte vectors
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(kv_scales, 8) ||
+        !aligned(cu_seqlens, 4) || !aligned(block_tables, 4) || !aligned(context_lens, 4))
+        return PKV_ERR_INVALID_ARG;
+    int sms = 0;
+    rc = current_sm_count(&sms);
+    if (rc != PKV_OK) return rc;
+    const int G = num_q_heads / num_kv_heads;
+    const int rtok = kQpRows / G;
+    // query tiles of a unit: two, which share every K and V tile; or one, when
+    // all units then run at once and a step of 128 keys has one tile's products
+    auto units_of = [&](int tiles) { return ((int64_t)max_q_len + tiles * rtok - 1) / (tiles * rtok); };
+    const bool one = out_dtype != PKV_DTYPE_F32 && num_seqs * units_of(1) * num_kv_heads <= sms;
+    const int qtiles = one ? 1 : 2;
+    const int64_t grid = (int64_t)num_seqs * units_of(qtiles) * num_kv_heads;
+    if (grid >= (int64_t)1 << 31) return PKV_ERR_UNSUPPORTED;
+    CUtensorMap tk, tv;
+    rc = encode_code_page_map(&tk, k_cache, num_blocks, num_kv_heads, head_dim);
+    if (rc != PKV_OK) return rc;
+    rc = encode_code_page_map(&tv, v_cache, num_blocks, num_kv_heads, head_dim);
+    if (rc != PKV_OK) return rc;
+    QuantPrefillParams prm;
+    prm.boxes = out_dtype == dtype && 32 % G == 0;
+    CUtensorMap tout = tk;
+    if (prm.boxes) {
+        const uint64_t dims[3] = {(uint64_t)head_dim, (uint64_t)num_q_heads, (uint64_t)total_q};
+        const uint64_t strides[2] = {(uint64_t)head_dim * 2, (uint64_t)num_q_heads * head_dim * 2};
+        const uint32_t rows[3] = {64, (uint32_t)G, 32u / (uint32_t)G};
+        rc = encode_tiled_map(&tout, out, 3, dims, strides, rows);
+        if (rc != PKV_OK) return rc;
+    }
+    prm.out = out;
+    prm.q = q;
+    prm.scales = kv_scales;
+    prm.cu_seqlens = cu_seqlens;
+    prm.block_tables = block_tables;
+    prm.context_lens = context_lens;
+    prm.dev_status = dev_status;
+    prm.max_blocks = max_blocks_per_seq;
+    prm.num_blocks = num_blocks;
+    prm.Hq = num_q_heads;
+    prm.Hkv = num_kv_heads;
+    prm.G = G;
+    prm.rtok = rtok;
+    prm.units_per_seq = (int)units_of(qtiles);
+    const int64_t capacity = (int64_t)max_blocks_per_seq * 16;
+    prm.window = window < capacity ? window : (int)capacity;   // no context is longer
+    prm.sinks = num_sinks < capacity ? num_sinks : (int)capacity;
+    prm.total_q = total_q;
+    prm.max_q_len = max_q_len;
+    prm.scale_log2 = scale * 1.4426950408889634f;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    auto launch = [&](auto type, auto wide, auto residual, auto tiles) {
+        using T = decltype(type);
+        constexpr bool W = decltype(wide)::value, R = decltype(residual)::value;
+        constexpr int N = decltype(tiles)::value;
+        return head_dim == 128 ? launch_quant_prefill<T, 128, W, R, N>(prm, tk, tv, tout, (int)grid, st)
+                               : launch_quant_prefill<T, 64, W, R, N>(prm, tk, tv, tout, (int)grid, st);
+    };
+    using Yes = std::true_type;
+    using No = std::false_type;
+    std::integral_constant<int, 1> tile;
+    std::integral_constant<int, 2> tiles;
+    if (dtype == PKV_DTYPE_BF16) {
+        if (out_dtype == PKV_DTYPE_F32) return launch(__nv_bfloat16(), Yes(), Yes(), tiles);
+        return one ? launch(__nv_bfloat16(), No(), No(), tile) : launch(__nv_bfloat16(), No(), No(), tiles);
+    }
+    if (out_dtype == PKV_DTYPE_F32) return launch(__half(), Yes(), Yes(), tiles);
+    return one ? launch(__half(), No(), Yes(), tile) : launch(__half(), No(), Yes(), tiles);
+}

@@ -69,6 +69,7 @@
 #include "pkv_device.cuh"
 #include "pkv_host.h"
 #include "pkv_tc.cuh"
+#include "pkv_window.cuh"
 
 namespace pkv {
 
@@ -99,30 +100,6 @@ struct WindowPrefillParams {
     int window, sinks, total_q, max_q_len;
     float scale_log2;
     bool boxes;   // a warp's 32 rows are whole tokens: tout has a box for them
-};
-
-// One unit of work, as the scheduler publishes it (tiles == 0: no more).
-// Positions count along the list of pages.
-struct WpUnit {
-    int tiles;        // key tiles walked
-    int h, row0;      // KV head; first row of q / out
-    int tokens;       // rows of the unit (tile A first)
-    int first;        // position of the first row
-    int ctx;          // end of the context
-    int wpos;         // first position of the first row's window
-    int pad;
-};
-
-// Rows [a0, a1) and [b0, b1) of the key tile at key0 that no row of the unit
-// sees, in pages that are read: past the context, and between the first tokens
-// and the window.
-struct WpHidden {
-    int a0, a1, b0, b1;
-    __device__ __forceinline__ WpHidden(const WpUnit &u, int key0, int sinks, int keys)
-        : a0(max(u.ctx - key0, 0)), a1(min(keys, ((u.ctx + 15) & ~15) - key0)), b0(max(sinks - key0, 0)),
-          b1(min(u.wpos - key0, keys)) {}
-    __device__ __forceinline__ bool any() const { return a0 < a1 || b0 < b1; }
-    __device__ __forceinline__ bool has(int r) const { return (r >= a0 && r < a1) || (r >= b0 && r < b1); }
 };
 
 struct WpBars {
@@ -167,21 +144,6 @@ __device__ __forceinline__ void load_page(void *dst, const CUtensorMap *map, int
         "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(group), "r"(smem_addr(bar))
         : "memory");
 }
-
-// 128 bytes of a warp's rows from shared memory to the output, asynchronously.
-__device__ __forceinline__ void store_rows(const CUtensorMap *map, const void *src, int column, int head, int token) {
-    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
-                     reinterpret_cast<uint64_t>(map)),
-                 "r"(column), "r"(head), "r"(token), "r"(smem_addr(src))
-                 : "memory");
-    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-}
-
-// Until what this thread's stores read may be overwritten.
-__device__ __forceinline__ void stores_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
-
-// Until this thread's stores are complete.
-__device__ __forceinline__ void stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // WIDE: a 32-bit output.  TILES: query tiles of a unit, 2, or 1 (A alone)
 template <typename T, int D, bool WIDE, int TILES>
