@@ -23,17 +23,15 @@
 // (P in e4m3 terms would take three for a bf16 output: more steps than fp16's one,
 // and a conversion of every weight three times instead of V's once a tile.)
 //
-// What is walked, the unit of work and the turns that the two query tiles take:
-// as in window_prefill.cu.  Warps (persistent; 16 of them):
-//   0       TMA and scheduler: takes units, publishes them, loads K and V tiles of
-//           codes, 8 pages of 16, a page one box
-//   1, 2    issue the MMAs of query tile A, B
-//   3       scales of a key tile's pages: a, log2 b, 1 / b
-//   4-11    softmax: a warpgroup a query tile, a row per thread; each row's terms
-//           are made by its thread, the next unit's while the last P V of this one
-//           runs
-//   12-15   V's codes to fp16, in the layout of an MN-major operand; rows that no
-//           row of the unit sees become zero (they may hold NaN codes)
+// What is walked and the unit of work: as in window_prefill.cu.  Warps (persistent;
+// 12 of them):
+//   0      TMA and scheduler: takes units, publishes them, loads K and V tiles of
+//          codes, 8 pages of 16, a page one box, and the pages' scales (a, log2 b, 1 / b)
+//   1      issues the MMAs of both query tiles, turn by turn
+//   2, 3   V's codes to fp16, in the layout of an MN-major operand; rows that no row
+//          of the unit sees become zero (they may hold NaN codes)
+//   4-11   softmax: a warpgroup a query tile, a row per thread; each row's terms are
+//          made by its thread, the next unit's while the last P V of this one runs
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -50,14 +48,13 @@
 
 namespace pkv {
 
-constexpr int kQpThreads = 512;
-// registers per thread: the launch gives every thread kQpLaunchRegs; the first and
-// the last warpgroup drop and the two softmax warpgroups rise, by no more in all
-constexpr int kQpLaunchRegs = 128;
-constexpr int kQpLowRegs = 56;
-constexpr int kQpConvertRegs = 72;
-constexpr int kQpHighRegs = 192;
-static_assert(128 * (kQpLowRegs + kQpConvertRegs + 2 * kQpHighRegs) <= kQpThreads * kQpLaunchRegs, "register split");
+constexpr int kQpThreads = 384;
+// registers per thread: the launch gives every thread kQpLaunchRegs; the first
+// warpgroup drops and the two softmax warpgroups rise, by no more in all
+constexpr int kQpLaunchRegs = 168;
+constexpr int kQpLowRegs = 88;
+constexpr int kQpHighRegs = 208;
+static_assert(128 * (kQpLowRegs + 2 * kQpHighRegs) <= kQpThreads * kQpLaunchRegs, "register split");
 constexpr int kQpRows = 128;    // MMA rows = (token, head) pairs per query tile
 constexpr int kQpKeys = 128;    // keys per K/V tile
 constexpr int kQpPages = kQpKeys / 16;
@@ -93,7 +90,6 @@ struct QpBars {
     uint64_t v_full[2], v_empty[2];                        // V in fp16
     uint64_t scales_full[kQpScaleStages], scales_empty[kQpScaleStages];
     uint64_t s_full[2], p_full[2][2], o_done[2];           // per query tile (and part of its keys)
-    uint64_t turn[2];                                      // a query tile's turn at the tensor cores
 };
 
 template <typename T, int D>
@@ -162,19 +158,18 @@ __global__ void __launch_bounds__(kQpThreads, 1)
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars->unit_full[i], 1);
-            mbar_init(&bars->unit_empty[i], 5 * TILES + 5);   // issuers and softmax of each tile, scales, converters
+            mbar_init(&bars->unit_empty[i], 4 * TILES + 3);   // softmax of each tile, issuer, converters
             mbar_init(&bars->q_full[i], 4);
             mbar_init(&bars->k_full[i], 1);
-            mbar_init(&bars->k_empty[i], TILES);
+            mbar_init(&bars->k_empty[i], 1);
             mbar_init(&bars->codes_full[i], 1);
-            mbar_init(&bars->codes_empty[i], 4);
-            mbar_init(&bars->v_full[i], 4);
-            mbar_init(&bars->v_empty[i], TILES);
+            mbar_init(&bars->codes_empty[i], 2);
+            mbar_init(&bars->v_full[i], 2);
+            mbar_init(&bars->v_empty[i], 1);
             mbar_init(&bars->s_full[i], 1);
             mbar_init(&bars->p_full[i][0], 4);
             mbar_init(&bars->p_full[i][1], 4);
             mbar_init(&bars->o_done[i], 1);
-            mbar_init(&bars->turn[i], 1);
         }
         for (int i = 0; i < kQpScaleStages; ++i) {
             mbar_init(&bars->scales_full[i], 1);
@@ -299,6 +294,10 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                             else
                                 set_status(p.dev_status, PKV_DEV_BAD_BLOCK_ID);
                         }
+                        // its scales: on their way while the slots are waited for
+                        float2 sc = make_float2(1.f, 1.f);
+                        if (lane < kQpPages && 16 * v < u.ctx && blk >= 0 && blk < p.num_blocks)
+                            sc = __ldg(reinterpret_cast<const float2 *>(p.scales) + (int64_t)blk * p.Hkv + h);
                         const int st = (int)(g & 1);
                         uint8_t *kd = sm + Sh::OFF_K + st * Sh::CODE_TILE, *vd = sm + Sh::OFF_CODES + st * Sh::CODE_TILE;
                         // a K slot is free once both S products of its last tile are done
@@ -314,6 +313,14 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                             if (lane == 0) mbar_arrive_expect_tx(&bars->codes_full[st], Sh::CODE_TILE);
                             __syncwarp();
                             if (lane < kQpPages) load_code_page(vd + lane * Sh::CODE_PAGE, &tv, y, &bars->codes_full[st]);
+                        }
+                        const int sst = (int)(g % kQpScaleStages);
+                        if (ok && g >= kQpScaleStages) ok = wait_all(&bars->scales_empty[sst], g / kQpScaleStages - 1);
+                        if (ok) {
+                            const float lb = log2_approx(sc.y);
+                            if (lane < kQpPages) page_scales[sst * kQpPages + lane] = make_float4(sc.x, lb, exp2_approx(-lb), 0.f);
+                            __syncwarp();
+                            if (lane == 0) tc::mbar_arrive_cta(&bars->scales_full[sst]);
                         }
                     }
                     ++n;
@@ -345,151 +352,125 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                     }
                 }
             }
-        } else if (warp < 3) {
-            // ---------------- MMA issuer of query tile t ----------------
+        } else if (warp == 1) {
+            // ---------------- MMA issuer ----------------
             // The whole warp walks the schedule, so the waits and the
             // descriptor arithmetic are warp-uniform; one elected lane issues
-            // each MMA and commit.
-            const int t = warp - 1;
+            // each MMA and commit.  The query tiles take turns: P V of a key tile
+            // and S of the next are one turn, so that a tile's softmax runs beside
+            // the other's turn.
             const bool leader = tc::elect_one();
             constexpr uint32_t idesc_s = tc::idesc_e4m3(kQpRows, kQpKeys);
             constexpr uint32_t idesc_o = tc::idesc_f16(false, false, true, kQpRows, D);
-            const uint32_t d_s = tmem + t * 256, d_o = d_s + 128;
             auto code_desc = [&](uint32_t at) { return D == 128 ? tc::smem_desc_sw128(at, 16, 1024) : tc::smem_desc_sw64(at, 16, 512); };
-            const uint64_t q_desc = code_desc(sbase + Sh::OFF_Q + t * Sh::Q_BYTES);
+            const uint64_t q_desc = code_desc(sbase + Sh::OFF_Q);
             const uint64_t k_desc = code_desc(sbase + Sh::OFF_K);
             const uint64_t v_desc = tc::smem_desc_sw128(sbase + Sh::OFF_V, 1024, Sh::GROUP);
             uint32_t g = 0;     // key tiles done
-            // The two tiles take turns: P V of a key tile and S of the next are
-            // one turn, so that a tile's softmax runs beside the other's turn.
-            auto pass_turn = [&]() {
-                if (TILES == 2 && lane == 0) tc::mbar_arrive_cta(&bars->turn[1 - t]);
-            };
-            auto issue_s = [&](uint32_t k, bool pass) {   // S = Q K^T of key tile k
-                if (!wait_all(&bars->k_full[k & 1], k / 2)) return false;
+            auto issue_s = [&](int t, uint32_t k) {   // S = Q K^T of query tile t and key tile k
+                if (t == 0 && !wait_all(&bars->k_full[k & 1], k / 2)) return false;
                 tc::fence_after_sync();
+                const uint64_t qb = q_desc + (uint64_t)((t * Sh::Q_BYTES) >> 4);
                 const uint64_t kb = k_desc + (uint64_t)(((k & 1) * Sh::CODE_TILE) >> 4);
                 constexpr int STEPS = D / 32;
-#pragma unroll
-                for (int i = 0; i < Sh::TERMS * STEPS; ++i) {
-                    const uint32_t qo = ((i / STEPS) * Sh::Q_TERM + (i % STEPS) * 32) >> 4, ko = ((i % STEPS) * 32) >> 4;
-                    if (pass && i == Sh::TERMS * STEPS - 2) pass_turn();   // on its way while the rest is issued
-                    if (leader) tc::mma_f8_ss(d_s, q_desc + qo, kb + ko, idesc_s, i > 0);
-                }
                 if (leader) {
+#pragma unroll
+                    for (int i = 0; i < Sh::TERMS * STEPS; ++i) {
+                        const uint32_t qo = ((i / STEPS) * Sh::Q_TERM + (i % STEPS) * 32) >> 4, ko = ((i % STEPS) * 32) >> 4;
+                        tc::mma_f8_ss(tmem + t * 256, qb + qo, kb + ko, idesc_s, i > 0);
+                    }
                     tc::mma_commit(&bars->s_full[t]);
-                    tc::mma_commit(&bars->k_empty[k & 1]);
+                    if (t == TILES - 1) tc::mma_commit(&bars->k_empty[k & 1]);
                 }
+                __syncwarp();
                 return true;
             };
             QpUnit u;
-            for (int n = 0; t < TILES; ++n) {
-                if (!take_unit(n, u)) break;
+            for (int n = 0; take_unit(n, u); ++n) {
                 const int tiles = u.tiles;
+                bool ok = true;
                 // (S may be written: the product that read P over it was issued before)
-                bool ok = wait_all(&bars->q_full[t], (uint32_t)n) && issue_s(g, false);
+#pragma unroll
+                for (int t = 0; t < TILES; ++t) ok = ok && wait_all(&bars->q_full[t], (uint32_t)n) && issue_s(t, g);
                 for (int j = 0; ok && j < tiles; ++j, ++g) {
                     const uint64_t vb = v_desc + (uint64_t)(((g & 1) * Sh::TILE) >> 4);
                     ok = wait_all(&bars->v_full[g & 1], g / 2);
-                    if (TILES == 2 && (t == 1 || g > 0)) ok = ok && wait_all(&bars->turn[t], t == 1 ? g : g - 1);
 #pragma unroll
-                    for (int part = 0; part < 2; ++part) {
-                        // P of a unit's first tile is there only after the unit before's O was read
-                        ok = ok && wait_all(&bars->p_full[t][part], g);
-                        if (!ok) break;
-                        tc::fence_after_sync();
+                    for (int t = 0; t < TILES; ++t) {
+                        const uint32_t d_s = tmem + t * 256, d_o = d_s + 128;
 #pragma unroll
-                        for (int kk = part ? 2 * Sh::FIRST_PART : 0; kk < (part ? kQpPages : 2 * Sh::FIRST_PART); ++kk) {
-                            // O (+)= P V, a page at a time
-                            const uint32_t ph = d_s + 32 * (kk >> 1) + 8 * (kk & 1);
-                            const uint64_t vp = vb + (uint32_t)(kk * Sh::PAGE >> 4);
+                        for (int part = 0; part < 2; ++part) {
+                            // P of a unit's first tile is there only after the unit before's O was read
+                            ok = ok && wait_all(&bars->p_full[t][part], g);
+                            if (!ok) break;
+                            tc::fence_after_sync();
                             if (leader) {
-                                tc::mma_f16_ts(d_o, ph, vp, idesc_o, j > 0 || kk > 0);
-                                if (RES) tc::mma_f16_ts(d_o, ph + 16, vp, idesc_o, true);   // the weights' rounding residual
+#pragma unroll
+                                for (int kk = part ? 2 * Sh::FIRST_PART : 0; kk < (part ? kQpPages : 2 * Sh::FIRST_PART); ++kk) {
+                                    // O (+)= P V, a page at a time
+                                    const uint32_t ph = d_s + 32 * (kk >> 1) + 8 * (kk & 1);
+                                    const uint64_t vp = vb + (uint32_t)(kk * Sh::PAGE >> 4);
+                                    tc::mma_f16_ts(d_o, ph, vp, idesc_o, j > 0 || kk > 0);
+                                    if (RES) tc::mma_f16_ts(d_o, ph + 16, vp, idesc_o, true);   // the weights' rounding residual
+                                }
                             }
+                            __syncwarp();
                         }
+                        if (!ok) break;
+                        if (leader) {
+                            if (t == TILES - 1) tc::mma_commit(&bars->v_empty[g & 1]);
+                            if (j + 1 == tiles) tc::mma_commit(&bars->o_done[t]);
+                        }
+                        __syncwarp();
+                        if (j + 1 < tiles) ok = issue_s(t, g + 1);
                     }
-                    if (!ok) break;
-                    if (leader) {
-                        tc::mma_commit(&bars->v_empty[g & 1]);
-                        if (j + 1 == tiles) tc::mma_commit(&bars->o_done[t]);
-                    }
-                    if (j + 1 < tiles)
-                        ok = issue_s(g + 1, true);
-                    else
-                        pass_turn();
                 }
                 if (!ok) break;
             }
         } else {
-            // ---------------- scales of a key tile's pages ----------------
+            // ---------------- V's codes to fp16 ----------------
+            // A warp takes 64 rows, 8 rows x 4 pieces of 16 codes at a time, each lane a
+            // piece; the rows of lanes k and k + 4 differ in their lowest and third bit,
+            // so that neither the loads nor the stores meet a bank twice.
+            const int piece = lane & 3, k = lane >> 2;
+            const int row = (k >> 1) ^ ((k & 1) * 5);
             uint32_t g = 0;
             bool ok = true;
             QpUnit u;
             for (int n = 0; ok && take_unit(n, u); ++n) {
-                auto fetch = [&](int j) {
-                    const int id = lane < kQpPages && j < u.tiles ? page_id(u, j * kQpPages + lane) : -1;
-                    if (id < 0 || id >= p.num_blocks) return make_float2(1.f, 1.f);
-                    return __ldg(reinterpret_cast<const float2 *>(p.scales) + (int64_t)id * p.Hkv + u.h);
-                };
-                float2 next = fetch(0);
                 for (int j = 0; ok && j < u.tiles; ++j, ++g) {
-                    const float2 sc = next;
-                    next = fetch(j + 1);
-                    const int st = (int)(g % kQpScaleStages);
-                    if (g >= kQpScaleStages) ok = wait_all(&bars->scales_empty[st], g / kQpScaleStages - 1);
+                    const int st = (int)(g & 1);
+                    ok = wait_all(&bars->codes_full[st], g / 2);
+                    if (g >= 2) ok = ok && wait_all(&bars->v_empty[st], g / 2 - 1);
                     if (!ok) break;
-                    const float lb = log2_approx(sc.y);
-                    if (lane < kQpPages) page_scales[st * kQpPages + lane] = make_float4(sc.x, lb, exp2_approx(-lb), 0.f);
-                    __syncwarp();
-                    if (lane == 0) tc::mbar_arrive_cta(&bars->scales_full[st]);
-                }
-            }
-        }
-    } else if (warp >= 12) {
-        tc::setmaxnreg_dec<kQpConvertRegs>();
-        // ---------------- V's codes to fp16 ----------------
-        // A warp takes 32 rows, 8 rows x 4 pieces of 16 codes at a time, each lane a
-        // piece; the rows of lanes k and k + 4 differ in their lowest and third bit,
-        // so that neither the loads nor the stores meet a bank twice.
-        const int piece = lane & 3, k = lane >> 2;
-        const int row = (k >> 1) ^ ((k & 1) * 5);
-        uint32_t g = 0;
-        bool ok = true;
-        QpUnit u;
-        for (int n = 0; ok && take_unit(n, u); ++n) {
-            for (int j = 0; ok && j < u.tiles; ++j, ++g) {
-                const int st = (int)(g & 1);
-                ok = wait_all(&bars->codes_full[st], g / 2);
-                if (g >= 2) ok = ok && wait_all(&bars->v_empty[st], g / 2 - 1);
-                if (!ok) break;
-                const uint32_t from = sbase + Sh::OFF_CODES + st * Sh::CODE_TILE;
-                const uint32_t to = sbase + Sh::OFF_V + st * Sh::TILE;
-                const WpHidden hid(u, j * kQpKeys, p.sinks, kQpKeys);
-                const bool any = hid.any();
+                    const uint32_t from = sbase + Sh::OFF_CODES + st * Sh::CODE_TILE;
+                    const uint32_t to = sbase + Sh::OFF_V + st * Sh::TILE;
+                    const WpHidden hid(u, j * kQpKeys, p.sinks, kQpKeys);
+                    const bool any = hid.any();
+#pragma unroll 4
+                    for (int i = 0; i < 8; ++i) {
+                        const int r0 = (warp - 2) * 64 + i * 8, r = r0 + row;
+                        const bool gone = any && hid.has(r);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r0 = (warp - 12) * 32 + i * 8, r = r0 + row;
-                    const bool gone = any && hid.has(r);
-#pragma unroll
-                    for (int hf = 0; hf < Sh::HALVES; ++hf) {
-                        uint4 c = lds128(from + code_piece<D>(r, 4 * hf + piece));
-                        if (gone) c = make_uint4(0u, 0u, 0u, 0u);
-                        uint4 lo, hi;
-                        e4m3x4_to_f16x4(c.x, lo.x, lo.y);
-                        e4m3x4_to_f16x4(c.y, lo.z, lo.w);
-                        e4m3x4_to_f16x4(c.z, hi.x, hi.y);
-                        e4m3x4_to_f16x4(c.w, hi.z, hi.w);
-                        const uint32_t at = to + (r0 >> 3) * Sh::GROUP + hf * 1024 + row * 128;
-                        st_shared_v4(at + (((2 * piece) ^ row) << 4), lo);
-                        st_shared_v4(at + (((2 * piece + 1) ^ row) << 4), hi);
+                        for (int hf = 0; hf < Sh::HALVES; ++hf) {
+                            uint4 c = lds128(from + code_piece<D>(r, 4 * hf + piece));
+                            if (gone) c = make_uint4(0u, 0u, 0u, 0u);
+                            uint4 lo, hi;
+                            e4m3x4_to_f16x4(c.x, lo.x, lo.y);
+                            e4m3x4_to_f16x4(c.y, lo.z, lo.w);
+                            e4m3x4_to_f16x4(c.z, hi.x, hi.y);
+                            e4m3x4_to_f16x4(c.w, hi.z, hi.w);
+                            const uint32_t at = to + (r0 >> 3) * Sh::GROUP + hf * 1024 + row * 128;
+                            st_shared_v4(at + (((2 * piece) ^ row) << 4), lo);
+                            st_shared_v4(at + (((2 * piece + 1) ^ row) << 4), hi);
+                        }
                     }
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    tc::mbar_arrive_cta(&bars->v_full[st]);
-                    tc::mbar_arrive_cta(&bars->codes_empty[st]);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tc::mbar_arrive_cta(&bars->v_full[st]);
+                        tc::mbar_arrive_cta(&bars->codes_empty[st]);
+                    }
                 }
             }
         }
@@ -591,20 +572,17 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                     }
                 }
                 // y = v f + lb with f, lb of the key's page; f > 0, so a page's largest y is its largest v's
-                float f[kQpPages], lb[kQpPages];
                 float mx = -INFINITY;
 #pragma unroll
                 for (int pg = 0; pg < kQpPages; ++pg) {
                     const float4 sc = page_scales[st * kQpPages + pg];
-                    f[pg] = sc.x * rowscale;
-                    lb[pg] = sc.y;
                     float a = fmaxf(v[16 * pg], v[16 * pg + 1]), b = fmaxf(v[16 * pg + 2], v[16 * pg + 3]);
 #pragma unroll
                     for (int e = 4; e < 16; e += 4) {
                         a = fmax3(a, v[16 * pg + e], v[16 * pg + e + 1]);
                         b = fmax3(b, v[16 * pg + e + 2], v[16 * pg + e + 3]);
                     }
-                    mx = fmaxf(mx, fmaf(fmaxf(a, b), f[pg], lb[pg]));
+                    mx = fmaxf(mx, fmaf(fmaxf(a, b), sc.x * rowscale, sc.y));
                 }
                 const bool first = m_used == -INFINITY;
                 const float m_new = fmaxf(m_used, mx);
@@ -635,7 +613,9 @@ __global__ void __launch_bounds__(kQpThreads, 1)
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         const int pg = 2 * cc + half;
-                        const uint64_t f2 = f2_pack(f[pg], f[pg]), c2 = f2_pack(lb[pg] - off, lb[pg] - off);
+                        const float4 sc = page_scales[st * kQpPages + pg];
+                        const float f = sc.x * rowscale, c = sc.y - off;
+                        const uint64_t f2 = f2_pack(f, f), c2 = f2_pack(c, c);
                         uint64_t sum2 = f2_pack(0.f, 0.f);
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
@@ -652,7 +632,7 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                         }
                         float s0, s1;
                         f2_unpack(sum2, s0, s1);
-                        l = fmaf(s0 + s1, page_scales[st * kQpPages + pg].z, l);
+                        l = fmaf(s0 + s1, sc.z, l);
                     }
                     tc::tmem_st16(scol + cc * 32, hi);
                     if constexpr (RES) tc::tmem_st16(scol + cc * 32 + 16, lo);
