@@ -26,7 +26,7 @@
 // What is walked and the unit of work: as in window_prefill.cu.  Warps (persistent;
 // 12 of them):
 //   0      TMA and scheduler: takes units, publishes them, loads K and V tiles of
-//          codes, 8 pages of 16, a page one box, and the pages' scales (a, log2 b, 1 / b)
+//          codes, 8 pages of 16, a page one box, and the pages' scales (a, log2 b)
 //   1      issues the MMAs of both query tiles, turn by turn
 //   2, 3   V's codes to fp16, in the layout of an MN-major operand; rows that no row
 //          of the unit sees become zero (they may hold NaN codes)
@@ -115,7 +115,7 @@ struct QpShape {
     // take them, and the next unit's terms are made behind them
     static constexpr bool OWN_OUT = !(TERMS == 3 && D == 128);
     static constexpr int OFF_SCALES = OFF_OUT + (OWN_OUT ? 8 * 4096 : 0);
-    static constexpr int OFF_CANCEL = OFF_SCALES + kQpScaleStages * kQpPages * 16;
+    static constexpr int OFF_CANCEL = OFF_SCALES + kQpScaleStages * kQpPages * 8;
     static constexpr int OFF_UNIT = OFF_CANCEL + 16;
     static constexpr int OFF_BAR = (OFF_UNIT + 2 * (int)sizeof(QpUnit) + 7) & ~7;
     static constexpr int SMEM_BYTES = 1024 + OFF_BAR + (int)sizeof(QpBars) + 16;
@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(kQpThreads, 1)
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     QpBars *bars = reinterpret_cast<QpBars *>(sm + Sh::OFF_BAR);
     QpUnit *units = reinterpret_cast<QpUnit *>(sm + Sh::OFF_UNIT);
-    float4 *page_scales = reinterpret_cast<float4 *>(sm + Sh::OFF_SCALES);   // [stage][page] a, log2 b, 1 / b
+    float2 *page_scales = reinterpret_cast<float2 *>(sm + Sh::OFF_SCALES);   // [stage][page] a, log2 b
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 1);
     volatile int *gave_up = reinterpret_cast<volatile int *>(tmem_slot + 1);   // a wait of this CTA ran out
 
@@ -317,8 +317,7 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                         const int sst = (int)(g % kQpScaleStages);
                         if (ok && g >= kQpScaleStages) ok = wait_all(&bars->scales_empty[sst], g / kQpScaleStages - 1);
                         if (ok) {
-                            const float lb = log2_approx(sc.y);
-                            if (lane < kQpPages) page_scales[sst * kQpPages + lane] = make_float4(sc.x, lb, exp2_approx(-lb), 0.f);
+                            if (lane < kQpPages) page_scales[sst * kQpPages + lane] = make_float2(sc.x, log2_approx(sc.y));
                             __syncwarp();
                             if (lane == 0) tc::mbar_arrive_cta(&bars->scales_full[sst]);
                         }
@@ -447,22 +446,36 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                     const uint32_t to = sbase + Sh::OFF_V + st * Sh::TILE;
                     const WpHidden hid(u, j * kQpKeys, p.sinks, kQpKeys);
                     const bool any = hid.any();
-#pragma unroll 4
-                    for (int i = 0; i < 8; ++i) {
-                        const int r0 = (warp - 2) * 64 + i * 8, r = r0 + row;
-                        const bool gone = any && hid.has(r);
+                    // two groups of 8 rows at a time, the next ones' codes on their way
+                    uint4 codes[2][2][Sh::HALVES];
+                    auto load = [&](int i) {
 #pragma unroll
-                        for (int hf = 0; hf < Sh::HALVES; ++hf) {
-                            uint4 c = lds128(from + code_piece<D>(r, 4 * hf + piece));
-                            if (gone) c = make_uint4(0u, 0u, 0u, 0u);
-                            uint4 lo, hi;
-                            e4m3x4_to_f16x4(c.x, lo.x, lo.y);
-                            e4m3x4_to_f16x4(c.y, lo.z, lo.w);
-                            e4m3x4_to_f16x4(c.z, hi.x, hi.y);
-                            e4m3x4_to_f16x4(c.w, hi.z, hi.w);
-                            const uint32_t at = to + (r0 >> 3) * Sh::GROUP + hf * 1024 + row * 128;
-                            st_shared_v4(at + (((2 * piece) ^ row) << 4), lo);
-                            st_shared_v4(at + (((2 * piece + 1) ^ row) << 4), hi);
+                        for (int e = 0; e < 2; ++e)
+#pragma unroll
+                            for (int hf = 0; hf < Sh::HALVES; ++hf)
+                                codes[i & 1][e][hf] = lds128(from + code_piece<D>((warp - 2) * 64 + (2 * i + e) * 8 + row, 4 * hf + piece));
+                    };
+                    load(0);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (i < 3) load(i + 1);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int r0 = (warp - 2) * 64 + (2 * i + e) * 8;
+                            const bool gone = any && hid.has(r0 + row);
+#pragma unroll
+                            for (int hf = 0; hf < Sh::HALVES; ++hf) {
+                                uint4 c = codes[i & 1][e][hf];
+                                if (gone) c = make_uint4(0u, 0u, 0u, 0u);
+                                uint4 lo, hi;
+                                e4m3x4_to_f16x4(c.x, lo.x, lo.y);
+                                e4m3x4_to_f16x4(c.y, lo.z, lo.w);
+                                e4m3x4_to_f16x4(c.z, hi.x, hi.y);
+                                e4m3x4_to_f16x4(c.w, hi.z, hi.w);
+                                const uint32_t at = to + (r0 >> 3) * Sh::GROUP + hf * 1024 + row * 128;
+                                st_shared_v4(at + (((2 * piece) ^ row) << 4), lo);
+                                st_shared_v4(at + (((2 * piece + 1) ^ row) << 4), hi);
+                            }
                         }
                     }
                     fence_proxy_async_smem();
@@ -483,60 +496,68 @@ __global__ void __launch_bounds__(kQpThreads, 1)
         const uint32_t scol = tmem + ((uint32_t)lane_base << 16) + t * 256;   // the scores, then P
         const uint32_t ocol = scol + 128;
         const int tok = t * p.rtok + r / p.G, head = r % p.G;
-        // this row's query as terms; what its scores are multiplied by
+        // This warp's rows of the query as terms; what this thread's row has its scores
+        // multiplied by.  LANES lanes take a row, eight elements each.
         auto split_query = [&](const QpUnit &u) {
-            uint4 x[D / 8];
-            const bool valid = r < p.G * p.rtok && tok < u.tokens;
-            const uint4 *from = reinterpret_cast<const uint4 *>(
-                static_cast<const T *>(p.q) + ((int64_t)(u.row0 + tok) * p.Hq + (int64_t)u.h * p.G + head) * D);
-            uint32_t top2 = 0;
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
-                x[i] = valid ? __ldg(from + i) : make_uint4(0u, 0u, 0u, 0u);
-                top2 = __vmaxu2(top2, __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
-                                               __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu)));
-            }
-            const uint32_t top = max(top2 & 0xffffu, top2 >> 16);
-            const bool finite = top < (std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u);
-            const float s = block_scale(finite ? pair_to_f32<T>(top).x : 0.f, -126);
-            const float inv = 1.f / s;
+            constexpr int LANES = D / 8, ROWS = 32 / LANES;    // rows at a time
+            constexpr int N = 32 / ROWS;
+            const int sub = lane / LANES, piece = lane % LANES;
             const uint32_t to = sbase + Sh::OFF_Q + t * Sh::Q_BYTES;
+            uint4 x[N];
 #pragma unroll
-            for (int c = 0; c < D / 16; ++c) {
-                float v[16];
+            for (int i = 0; i < N; ++i) {
+                const int rr = lane_base + i * ROWS + sub, tk = t * p.rtok + rr / p.G;
+                x[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (rr < p.G * p.rtok && tk < u.tokens)
+                    x[i] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(p.q) +
+                                                                 ((int64_t)(u.row0 + tk) * p.Hq + (int64_t)u.h * p.G + rr % p.G) * D) +
+                                 piece);
+            }
+            float scale = 0.f;
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const uint4 w = x[2 * c + e];
-                    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+            for (int i = 0; i < N; ++i) {
+                const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                const uint32_t top2 = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
+                                               __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+                uint32_t top = max(top2 & 0xffffu, top2 >> 16);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 f = pair_to_f32<T>(ww[i]);
-                        v[8 * e + 2 * i] = f.x * inv;
-                        v[8 * e + 2 * i + 1] = f.y * inv;
-                    }
+                for (int m = 1; m < LANES; m *= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, m));
+                const bool finite = top < (std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u);
+                const float s = block_scale(finite ? pair_to_f32<T>(top).x : 0.f, -126);
+                const float inv = __uint_as_float((254u << 23) - __float_as_uint(s));   // (s is a power of two)
+                // (a query that is not finite has no finite output)
+                const float mine = __shfl_sync(0xffffffffu, finite ? s : __uint_as_float(0x7fffffffu), (lane % ROWS) * LANES);
+                if (lane / ROWS == i) scale = mine;
+                float v[8];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 f = pair_to_f32<T>(w[e]);
+                    v[2 * e] = f.x * inv;
+                    v[2 * e + 1] = f.y * inv;
                 }
+                const int rr = lane_base + i * ROWS + sub;
+                const uint32_t at = to + code_piece<D>(rr, piece >> 1) + (piece & 1) * 8;
 #pragma unroll
                 for (int term = 0; term < Sh::TERMS; ++term) {
-                    uint32_t w[4];
+                    uint32_t c[2];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        w[i] = to_e4m3x4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-                        uint32_t a, b;
-                        e4m3x4_to_f16x4(w[i], a, b);
-                        const float2 fa = f16x2_to_f32(a), fb = f16x2_to_f32(b);
-                        v[4 * i] -= fa.x;
-                        v[4 * i + 1] -= fa.y;
-                        v[4 * i + 2] -= fb.x;
-                        v[4 * i + 3] -= fb.y;
+                    for (int e = 0; e < 2; ++e) {
+                        c[e] = to_e4m3x4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                        uint32_t lo, hi;
+                        e4m3x4_to_f16x4(c[e], lo, hi);
+                        const float2 fl = f16x2_to_f32(lo), fh = f16x2_to_f32(hi);
+                        v[4 * e] -= fl.x;
+                        v[4 * e + 1] -= fl.y;
+                        v[4 * e + 2] -= fh.x;
+                        v[4 * e + 3] -= fh.y;
                     }
-                    st_shared_v4(to + term * Sh::Q_TERM + code_piece<D>(r, c), make_uint4(w[0], w[1], w[2], w[3]));
+                    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + term * Sh::Q_TERM), "r"(c[0]), "r"(c[1]) : "memory");
                 }
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive_cta(&bars->q_full[t]);
-            // (a query that is not finite has no finite output)
-            return (finite ? s : __uint_as_float(0x7fffffffu)) * p.scale_log2;
+            return scale * p.scale_log2;
         };
         uint32_t g = 0;                                 // key tiles taken
         QpUnit u;
@@ -572,17 +593,22 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                     }
                 }
                 // y = v f + lb with f, lb of the key's page; f > 0, so a page's largest y is its largest v's
+                // (read once: a load that all lanes make of one address costs shared
+                // memory, which the products keep busy, as much as any other)
+                float f[kQpPages], lb[kQpPages];
                 float mx = -INFINITY;
 #pragma unroll
                 for (int pg = 0; pg < kQpPages; ++pg) {
-                    const float4 sc = page_scales[st * kQpPages + pg];
+                    const float2 sc = page_scales[st * kQpPages + pg];
+                    f[pg] = sc.x * rowscale;
+                    lb[pg] = sc.y;
                     float a = fmaxf(v[16 * pg], v[16 * pg + 1]), b = fmaxf(v[16 * pg + 2], v[16 * pg + 3]);
 #pragma unroll
                     for (int e = 4; e < 16; e += 4) {
                         a = fmax3(a, v[16 * pg + e], v[16 * pg + e + 1]);
                         b = fmax3(b, v[16 * pg + e + 2], v[16 * pg + e + 3]);
                     }
-                    mx = fmaxf(mx, fmaf(fmaxf(a, b), sc.x * rowscale, sc.y));
+                    mx = fmaxf(mx, fmaf(fmaxf(a, b), f[pg], lb[pg]));
                 }
                 const bool first = m_used == -INFINITY;
                 const float m_new = fmaxf(m_used, mx);
@@ -602,45 +628,46 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                         tc::tmem_st32(ocol + cc, o);
                     }
                 }
-                // P = 2^(y - m_used + 7) over the same columns, 32 keys at a time: 16
-                // columns of rounded pairs (then 16 of residual pairs).
+                // P = 2^(y - m_used + 7) over the same columns, a page at a time: 8 columns
+                // of rounded pairs (and 16 further 8 of residual pairs).
                 // A row that has seen no key yet has nothing to subtract.
                 const float off = (m_used == -INFINITY ? 0.f : m_used) - 7.f;
                 l *= alpha;
 #pragma unroll
-                for (int cc = 0; cc < kQpKeys / 32; ++cc) {
-                    uint32_t hi[16], lo[16];
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const int pg = 2 * cc + half;
-                        const float4 sc = page_scales[st * kQpPages + pg];
-                        const float f = sc.x * rowscale, c = sc.y - off;
-                        const uint64_t f2 = f2_pack(f, f), c2 = f2_pack(c, c);
-                        uint64_t sum2 = f2_pack(0.f, 0.f);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            float a, b;
-                            f2_unpack(f2_fma(f2_pack(v[16 * pg + 2 * e], v[16 * pg + 2 * e + 1]), f2, c2), a, b);
-                            a = exp2_approx(a);
-                            b = exp2_approx(b);
-                            const uint64_t ab = f2_pack(a, b);
-                            sum2 = f2_add(sum2, ab);
-                            if constexpr (RES)
-                                pack2_split2<__half>(ab, a, b, hi[8 * half + e], lo[8 * half + e]);
-                            else
-                                hi[8 * half + e] = pack2<__half>(a, b);
-                        }
-                        float s0, s1;
-                        f2_unpack(sum2, s0, s1);
-                        l = fmaf(s0 + s1, sc.z, l);
+                for (int pg = 0; pg < kQpPages; ++pg) {
+                    float2 sc = make_float2(f[pg], lb[pg]);
+                    if constexpr (RES) {   // (registers are short: read again)
+                        sc = page_scales[st * kQpPages + pg];
+                        sc.x *= rowscale;
                     }
-                    tc::tmem_st16(scol + cc * 32, hi);
-                    if constexpr (RES) tc::tmem_st16(scol + cc * 32 + 16, lo);
-                    if (cc == Sh::FIRST_PART - 1 || cc == 3) {   // a part of P is ready
+                    const float c = sc.y - off;
+                    const uint64_t f2 = f2_pack(sc.x, sc.x), c2 = f2_pack(c, c);
+                    uint64_t sum2 = f2_pack(0.f, 0.f);
+                    uint32_t hi[8], lo[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        float a, b;
+                        f2_unpack(f2_fma(f2_pack(v[16 * pg + 2 * e], v[16 * pg + 2 * e + 1]), f2, c2), a, b);
+                        a = exp2_approx(a);
+                        b = exp2_approx(b);
+                        const uint64_t ab = f2_pack(a, b);
+                        sum2 = f2_add(sum2, ab);
+                        if constexpr (RES)
+                            pack2_split2<__half>(ab, a, b, hi[e], lo[e]);
+                        else
+                            hi[e] = pack2<__half>(a, b);
+                    }
+                    float s0, s1;
+                    f2_unpack(sum2, s0, s1);
+                    l = fmaf(s0 + s1, exp2_approx(-sc.y), l);
+                    const uint32_t to = scol + 32 * (pg >> 1) + 8 * (pg & 1);
+                    tc::tmem_st8(to, hi);
+                    if constexpr (RES) tc::tmem_st8(to + 16, lo);
+                    if (pg == 2 * Sh::FIRST_PART - 1 || pg == kQpPages - 1) {   // a part of P is ready
                         tc::tmem_wait_st();
                         tc::fence_before_sync();
                         __syncwarp();
-                        if (lane == 0) tc::mbar_arrive_cta(&bars->p_full[t][cc == 3]);
+                        if (lane == 0) tc::mbar_arrive_cta(&bars->p_full[t][pg == kQpPages - 1]);
                     }
                 }
                 if (lane == 0) tc::mbar_arrive_cta(&bars->scales_empty[st]);
