@@ -89,7 +89,7 @@ struct QpBars {
     uint64_t codes_full[2], codes_empty[2];                // V's codes
     uint64_t v_full[2], v_empty[2];                        // V in fp16
     uint64_t scales_full[kQpScaleStages], scales_empty[kQpScaleStages];
-    uint64_t s_full[2], p_full[2][2], o_done[2];           // per query tile (and part of its keys)
+    uint64_t s_full[2], p_full[2][2], half_done[2], o_done[2];   // per query tile (and half of its keys)
 };
 
 template <typename T, int D>
@@ -105,7 +105,6 @@ struct QpShape {
     static constexpr int GROUP = HALVES * 1024;            // 8 rows
     static constexpr int PAGE = 2 * GROUP;
     static constexpr int TILE = kQpPages * PAGE;
-    static constexpr int FIRST_PART = 2;                   // 32-key groups of P after which P V may start
     static constexpr int OFF_Q = 0;                        // tile A, then tile B
     static constexpr int OFF_K = 2 * Q_BYTES;
     static constexpr int OFF_CODES = OFF_K + 2 * CODE_TILE;
@@ -169,6 +168,7 @@ __global__ void __launch_bounds__(kQpThreads, 1)
             mbar_init(&bars->s_full[i], 1);
             mbar_init(&bars->p_full[i][0], 4);
             mbar_init(&bars->p_full[i][1], 4);
+            mbar_init(&bars->half_done[i], 1);
             mbar_init(&bars->o_done[i], 1);
         }
         for (int i = 0; i < kQpScaleStages; ++i) {
@@ -405,13 +405,14 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                             tc::fence_after_sync();
                             if (leader) {
 #pragma unroll
-                                for (int kk = part ? 2 * Sh::FIRST_PART : 0; kk < (part ? kQpPages : 2 * Sh::FIRST_PART); ++kk) {
+                                for (int kk = part * kQpPages / 2; kk < (part + 1) * kQpPages / 2; ++kk) {
                                     // O (+)= P V, a page at a time
                                     const uint32_t ph = d_s + 32 * (kk >> 1) + 8 * (kk & 1);
                                     const uint64_t vp = vb + (uint32_t)(kk * Sh::PAGE >> 4);
                                     tc::mma_f16_ts(d_o, ph, vp, idesc_o, j > 0 || kk > 0);
                                     if (RES) tc::mma_f16_ts(d_o, ph + 16, vp, idesc_o, true);   // the weights' rounding residual
                                 }
+                                if (RES && part == 0) tc::mma_commit(&bars->half_done[t]);
                             }
                             __syncwarp();
                         }
@@ -466,7 +467,7 @@ __global__ void __launch_bounds__(kQpThreads, 1)
 #pragma unroll
                             for (int hf = 0; hf < Sh::HALVES; ++hf) {
                                 uint4 c = codes[i & 1][e][hf];
-                                if (gone) c = make_uint4(0u, 0u, 0u, 0u);
+                                if (any && gone) c = make_uint4(0u, 0u, 0u, 0u);
                                 uint4 lo, hi;
                                 e4m3x4_to_f16x4(c.x, lo.x, lo.y);
                                 e4m3x4_to_f16x4(c.y, lo.z, lo.w);
@@ -573,103 +574,213 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                 ok = wait_all(&bars->scales_full[st], g / kQpScaleStages) && wait_all(&bars->s_full[t], g);
                 if (!ok) break;
                 tc::fence_after_sync();
-                const int key0 = j * kQpKeys;
-                float v[kQpKeys];
+                if constexpr (!RES) {
+                    const int key0 = j * kQpKeys;
+                    float v[kQpKeys];
 #pragma unroll
-                for (int cc = 0; cc < kQpKeys; cc += 32) tc::tmem_ld32(scol + cc, *reinterpret_cast<float(*)[32]>(v + cc));
-                tc::tmem_wait_ld();
-                // hidden: past the row's position; below its window and behind the first tokens
-                const int lim = pos - key0, low = lim - p.window + 1, sk = p.sinks - key0;
-                if (__any_sync(0xffffffffu, lim < kQpKeys - 1 || (low > 0 && sk < kQpKeys))) {
-                    auto below = [](int n) { return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u); };
+                    for (int cc = 0; cc < kQpKeys; cc += 32) tc::tmem_ld32(scol + cc, *reinterpret_cast<float(*)[32]>(v + cc));
+                    tc::tmem_wait_ld();
+                    // hidden: past the row's position; below its window and behind the first tokens
+                    const int lim = pos - key0, low = lim - p.window + 1, sk = p.sinks - key0;
+                    if (__any_sync(0xffffffffu, lim < kQpKeys - 1 || (low > 0 && sk < kQpKeys))) {
+                        auto below = [](int n) { return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u); };
 #pragma unroll
-                    for (int cc = 0; cc < kQpKeys; cc += 32) {
-                        const uint32_t see = below(lim + 1 - cc) & (~below(low - cc) | below(sk - cc));
-                        if (__any_sync(0xffffffffu, see != 0xffffffffu)) {
+                        for (int cc = 0; cc < kQpKeys; cc += 32) {
+                            const uint32_t see = below(lim + 1 - cc) & (~below(low - cc) | below(sk - cc));
+                            if (__any_sync(0xffffffffu, see != 0xffffffffu)) {
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (!(see & (1u << e))) v[cc + e] = -INFINITY;
+                                for (int e = 0; e < 32; ++e)
+                                    if (!(see & (1u << e))) v[cc + e] = -INFINITY;
+                            }
                         }
                     }
-                }
-                // y = v f + lb with f, lb of the key's page; f > 0, so a page's largest y is its largest v's
-                // (read once: a load that all lanes make of one address costs shared
-                // memory, which the products keep busy, as much as any other)
-                float f[kQpPages], lb[kQpPages];
-                float mx = -INFINITY;
+                    // y = v f + lb with f, lb of the key's page; f > 0, so a page's largest y is its largest v's
+                    // (read once: a load that all lanes make of one address costs shared
+                    // memory, which the products keep busy, as much as any other)
+                    float f[kQpPages], lb[kQpPages];
+                    float mx = -INFINITY;
 #pragma unroll
-                for (int pg = 0; pg < kQpPages; ++pg) {
-                    const float2 sc = page_scales[st * kQpPages + pg];
-                    f[pg] = sc.x * rowscale;
-                    lb[pg] = sc.y;
-                    float a = fmaxf(v[16 * pg], v[16 * pg + 1]), b = fmaxf(v[16 * pg + 2], v[16 * pg + 3]);
+                    for (int pg = 0; pg < kQpPages; ++pg) {
+                        const float2 sc = page_scales[st * kQpPages + pg];
+                        f[pg] = sc.x * rowscale;
+                        lb[pg] = sc.y;
+                        float a = fmaxf(v[16 * pg], v[16 * pg + 1]), b = fmaxf(v[16 * pg + 2], v[16 * pg + 3]);
 #pragma unroll
-                    for (int e = 4; e < 16; e += 4) {
-                        a = fmax3(a, v[16 * pg + e], v[16 * pg + e + 1]);
-                        b = fmax3(b, v[16 * pg + e + 2], v[16 * pg + e + 3]);
+                        for (int e = 4; e < 16; e += 4) {
+                            a = fmax3(a, v[16 * pg + e], v[16 * pg + e + 1]);
+                            b = fmax3(b, v[16 * pg + e + 2], v[16 * pg + e + 3]);
+                        }
+                        mx = fmaxf(mx, fmaf(fmaxf(a, b), f[pg], lb[pg]));
                     }
-                    mx = fmaxf(mx, fmaf(fmaxf(a, b), f[pg], lb[pg]));
-                }
-                const bool first = m_used == -INFINITY;
-                const float m_new = fmaxf(m_used, mx);
-                const bool rescale = !first && m_new > m_used + 8.f;
-                const float alpha = rescale ? exp2_approx(m_used - m_new) : 1.f;
-                if (first || rescale) m_used = m_new;
-                // O was last written by the P V product before, which the tensor
-                // core finished before this tile's S (issued after it) completed
-                if (__any_sync(0xffffffffu, rescale)) {
+                    const bool first = m_used == -INFINITY;
+                    const float m_new = fmaxf(m_used, mx);
+                    const bool rescale = !first && m_new > m_used + 8.f;
+                    const float alpha = rescale ? exp2_approx(m_used - m_new) : 1.f;
+                    if (first || rescale) m_used = m_new;
+                    // O was last written by the P V product before, which the tensor
+                    // core finished before this tile's S (issued after it) completed
+                    if (__any_sync(0xffffffffu, rescale)) {
 #pragma unroll 1
-                    for (int cc = 0; cc < D; cc += 32) {
-                        float o[32];
-                        tc::tmem_ld32(ocol + cc, o);
-                        tc::tmem_wait_ld();
+                        for (int cc = 0; cc < D; cc += 32) {
+                            float o[32];
+                            tc::tmem_ld32(ocol + cc, o);
+                            tc::tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] *= alpha;
-                        tc::tmem_st32(ocol + cc, o);
+                            for (int e = 0; e < 32; ++e) o[e] *= alpha;
+                            tc::tmem_st32(ocol + cc, o);
+                        }
                     }
-                }
-                // P = 2^(y - m_used + 7) over the same columns, a page at a time: 8 columns
-                // of rounded pairs (and 16 further 8 of residual pairs).
-                // A row that has seen no key yet has nothing to subtract.
-                const float off = (m_used == -INFINITY ? 0.f : m_used) - 7.f;
-                l *= alpha;
+                    // P = 2^(y - m_used + 7) over the same columns, a page at a time: 8 columns
+                    // of rounded pairs.
+                    // A row that has seen no key yet has nothing to subtract.
+                    const float off = (m_used == -INFINITY ? 0.f : m_used) - 7.f;
+                    l *= alpha;
 #pragma unroll
-                for (int pg = 0; pg < kQpPages; ++pg) {
-                    float2 sc = make_float2(f[pg], lb[pg]);
-                    if constexpr (RES) {   // (registers are short: read again)
-                        sc = page_scales[st * kQpPages + pg];
-                        sc.x *= rowscale;
-                    }
-                    const float c = sc.y - off;
-                    const uint64_t f2 = f2_pack(sc.x, sc.x), c2 = f2_pack(c, c);
-                    uint64_t sum2 = f2_pack(0.f, 0.f);
-                    uint32_t hi[8], lo[8];
+                    for (int pg = 0; pg < kQpPages; ++pg) {
+                        const float c = lb[pg] - off;
+                        const uint64_t f2 = f2_pack(f[pg], f[pg]), c2 = f2_pack(c, c);
+                        uint64_t sum2 = f2_pack(0.f, 0.f);
+                        uint32_t hi[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        float a, b;
-                        f2_unpack(f2_fma(f2_pack(v[16 * pg + 2 * e], v[16 * pg + 2 * e + 1]), f2, c2), a, b);
-                        a = exp2_approx(a);
-                        b = exp2_approx(b);
-                        const uint64_t ab = f2_pack(a, b);
-                        sum2 = f2_add(sum2, ab);
-                        if constexpr (RES)
-                            pack2_split2<__half>(ab, a, b, hi[e], lo[e]);
-                        else
+                        for (int e = 0; e < 8; ++e) {
+                            float a, b;
+                            f2_unpack(f2_fma(f2_pack(v[16 * pg + 2 * e], v[16 * pg + 2 * e + 1]), f2, c2), a, b);
+                            a = exp2_approx(a);
+                            b = exp2_approx(b);
+                            const uint64_t ab = f2_pack(a, b);
+                            sum2 = f2_add(sum2, ab);
                             hi[e] = pack2<__half>(a, b);
+                        }
+                        float s0, s1;
+                        f2_unpack(sum2, s0, s1);
+                        l = fmaf(s0 + s1, exp2_approx(-lb[pg]), l);
+                        const uint32_t to = scol + 32 * (pg >> 1) + 8 * (pg & 1);
+                        tc::tmem_st8(to, hi);
+                        if (pg == kQpPages / 2 - 1 || pg == kQpPages - 1) {   // a part of P is ready
+                            tc::tmem_wait_st();
+                            tc::fence_before_sync();
+                            __syncwarp();
+                            if (lane == 0) tc::mbar_arrive_cta(&bars->p_full[t][pg == kQpPages - 1]);
+                        }
                     }
-                    float s0, s1;
-                    f2_unpack(sum2, s0, s1);
-                    l = fmaf(s0 + s1, exp2_approx(-sc.y), l);
-                    const uint32_t to = scol + 32 * (pg >> 1) + 8 * (pg & 1);
-                    tc::tmem_st8(to, hi);
-                    if constexpr (RES) tc::tmem_st8(to + 16, lo);
-                    if (pg == 2 * Sh::FIRST_PART - 1 || pg == kQpPages - 1) {   // a part of P is ready
-                        tc::tmem_wait_st();
+                } else {
+                    // Half of the keys at a time, and no look for the largest y first: twice
+                    // the work on a weight, and code that, unrolled for 128 keys, does not
+                    // stay in the instruction cache (3 x 4,000 rows in fp16 794 us, 725 so;
+                    // rounded once, the loop takes 590 us for 545).
+#pragma unroll 1
+                    for (int part = 0; part < 2; ++part) {
+                        constexpr int kHalf = kQpKeys / 2;
+                        float v[kHalf];
+                        tc::tmem_ld32(scol + part * kHalf, *reinterpret_cast<float(*)[32]>(v));
+                        tc::tmem_ld32(scol + part * kHalf + 32, *reinterpret_cast<float(*)[32]>(v + 32));
+                        // y = v f + lb with f, lb of the key's page
+                        float f[kHalf / 16], lb[kHalf / 16];
+#pragma unroll
+                        for (int pg = 0; pg < kHalf / 16; ++pg) {
+                            const float2 sc = page_scales[(st * 2 + part) * (kHalf / 16) + pg];
+                            f[pg] = sc.x * rowscale;
+                            lb[pg] = sc.y;
+                        }
+                        tc::tmem_wait_ld();
+                        // hidden: past the row's position; below its window and behind the first tokens
+                        const int key0 = j * kQpKeys + part * kHalf;
+                        const int lim = pos - key0, low = lim - p.window + 1, sk = p.sinks - key0;
+                        if (__any_sync(0xffffffffu, lim < kHalf - 1 || (low > 0 && sk < kHalf))) {
+                            auto below = [](int n) { return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u); };
+#pragma unroll
+                            for (int cc = 0; cc < kHalf; cc += 32) {
+                                const uint32_t see = below(lim + 1 - cc) & (~below(low - cc) | below(sk - cc));
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    if (!(see & (1u << e))) v[cc + e] = -INFINITY;
+                            }
+                        }
+                        // A row that has no maximum yet takes this half's (O has not been
+                        // written for it, or only with weights of 0).  Others go on with the
+                        // one they have, and look whether it still serves by the sums of P: a
+                        // page's sum of at most 2^15 has no weight above.
+                        bool raise = m_used == -INFINITY;
+                        float sum = 0.f;
+#pragma unroll 1
+                        for (int go = 0; go < 2; ++go) {   // (raised to the largest y there is, it serves)
+                            if (__any_sync(0xffffffffu, raise)) {
+                                // m_used becomes the largest y so far; O and l follow.  O was last
+                                // written by the P V product of the tile before, which the tensor
+                                // core finished before this tile's S (issued after it) completed,
+                                // or by the first half's
+                                if (part == 1) ok = wait_all(&bars->half_done[t], g);
+                                if (!ok) break;
+                                tc::fence_after_sync();
+                                float mx = m_used;
+#pragma unroll
+                                for (int pg = 0; pg < kHalf / 16; ++pg) {
+                                    float a = fmaxf(v[16 * pg], v[16 * pg + 1]), b = fmaxf(v[16 * pg + 2], v[16 * pg + 3]);
+#pragma unroll
+                                    for (int e = 4; e < 16; e += 4) {
+                                        a = fmax3(a, v[16 * pg + e], v[16 * pg + e + 1]);
+                                        b = fmax3(b, v[16 * pg + e + 2], v[16 * pg + e + 3]);
+                                    }
+                                    mx = fmaxf(mx, fmaf(fmaxf(a, b), f[pg], lb[pg]));   // (f > 0)
+                                }
+                                const float alpha = raise && m_used > -INFINITY ? exp2_approx(m_used - mx) : 1.f;
+                                if (raise) m_used = mx;
+                                l *= alpha;
+                                if (__any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+                                    for (int cc = 0; cc < D; cc += 32) {
+                                        float o[32];
+                                        tc::tmem_ld32(ocol + cc, o);
+                                        tc::tmem_wait_ld();
+#pragma unroll
+                                        for (int e = 0; e < 32; ++e) o[e] *= alpha;
+                                        tc::tmem_st32(ocol + cc, o);
+                                    }
+                                }
+                            }
+                            // P = 2^(y - m_used + 7) over the same columns, a page at a time: 8
+                            // columns of rounded pairs (and 16 further 8 of residual pairs).
+                            // (A row that has seen no key yet has nothing to subtract.)
+                            const float off = (m_used == -INFINITY ? 0.f : m_used) - 7.f;
+                            float top = 0.f;
+                            sum = 0.f;
+#pragma unroll
+                            for (int pg = 0; pg < kHalf / 16; ++pg) {
+                                const float c = lb[pg] - off;
+                                const uint64_t f2 = f2_pack(f[pg], f[pg]), c2 = f2_pack(c, c);
+                                uint64_t sum2 = f2_pack(0.f, 0.f);
+                                uint32_t hi[8], lo[8];
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) {
+                                    float a, b;
+                                    f2_unpack(f2_fma(f2_pack(v[16 * pg + 2 * e], v[16 * pg + 2 * e + 1]), f2, c2), a, b);
+                                    a = exp2_approx(a);
+                                    b = exp2_approx(b);
+                                    const uint64_t ab = f2_pack(a, b);
+                                    sum2 = f2_add(sum2, ab);
+                                    pack2_split2<__half>(ab, a, b, hi[e], lo[e]);
+                                }
+                                float s0, s1;
+                                f2_unpack(sum2, s0, s1);
+                                s0 += s1;
+                                top = fmaxf(top, s0);
+                                sum = fmaf(s0, exp2_approx(-lb[pg]), sum);
+                                const uint32_t to = scol + part * kHalf + 32 * (pg >> 1) + 8 * (pg & 1);
+                                tc::tmem_st8(to, hi);
+                                tc::tmem_st8(to + 16, lo);
+                            }
+                            raise = top > 32768.f;
+                            if (!__any_sync(0xffffffffu, raise)) break;
+                        }
+                        if (!ok) break;
+                        l += sum;
+                        tc::tmem_wait_st();   // a part of P is ready
                         tc::fence_before_sync();
                         __syncwarp();
-                        if (lane == 0) tc::mbar_arrive_cta(&bars->p_full[t][pg == kQpPages - 1]);
+                        if (lane == 0) tc::mbar_arrive_cta(&bars->p_full[t][part]);
                     }
                 }
+                if (!ok) break;
                 if (lane == 0) tc::mbar_arrive_cta(&bars->scales_empty[st]);
             }
             if (!ok) break;
