@@ -17,9 +17,10 @@
 //                two terms hold bf16's 8 bits, three fp16's 11, down to 2^-10 (2^-18
 //                of the largest element at most).  As many steps as in 16 bits, or
 //                one and a half times for fp16.
-//   O += P v     in fp16: v is converted on the way (exact).  P for a bf16 output
-//                is rounded once (2^-11 of a weight, an eighth of what the output's
-//                own rounding may be), else value and residual, two products.
+//   O += P v     in fp16: v is converted on the way (exact).  P for a 16-bit output
+//                is rounded once (2^-11 of a weight: an eighth of what the output's
+//                own rounding may be in bf16, and as much in fp16), for a 32-bit one
+//                value and residual, two products.
 // (P in e4m3 terms would take three for a bf16 output: more steps than fp16's one,
 // and a conversion of every weight three times instead of V's once a tile.)
 //
@@ -72,9 +73,10 @@ struct QuantPrefillParams {
     const int32_t *context_lens;
     int *dev_status;
     int max_blocks, num_blocks, Hq, Hkv, G;
-    int rtok, units_per_seq;
+    int rtok, num_seqs, units_per_seq;
     int window, sinks, total_q, max_q_len;
     float scale_log2;
+    bool sorted;  // units by length, longest first
     bool boxes;   // a warp's 32 rows are whole tokens: tout has a box for them
 };
 
@@ -242,29 +244,74 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                 asked += !asking;
                 asking = true;
             };
-            while (ok) {
-                // place -> unit; chunk by chunk, the last pair of tiles first, the KV heads side by side
-                const int h = place % p.Hkv;
-                const int rest = place / p.Hkv;
-                const int unit = p.units_per_seq - 1 - rest % p.units_per_seq;
-                const int c = rest / p.units_per_seq;
-                const int q0 = __ldg(p.cu_seqlens + c);
-                const int q_len = __ldg(p.cu_seqlens + c + 1) - q0;
-                const int ctx = __ldg(p.context_lens + c);
-                const int i0 = unit * TILES * p.rtok;
+            const int R = TILES * p.rtok;   // tokens of a unit
+            // a chunk's rows, tokens (none of one that is refused) and context; why it is refused
+            auto chunk_of = [&](int c, int &q0, int &q_len, int &ctx) {
+                q0 = __ldg(p.cu_seqlens + c);
+                q_len = __ldg(p.cu_seqlens + c + 1) - q0;
+                ctx = __ldg(p.context_lens + c);
                 int bad = 0;
                 // (rows past max_q_len have no unit)
                 if (q_len < 0 || q_len > ctx || q_len > p.max_q_len || q0 < 0 || q_len > p.total_q - q0)
                     bad = PKV_DEV_BAD_CHUNK;
                 else if (ctx > p.max_blocks * 16)
                     bad = PKV_DEV_BAD_CONTEXT;
-                if (bad && unit == 0 && lane == 0) set_status(p.dev_status, bad);
-                if (!bad && i0 < q_len) {
+                if (bad) q_len = 0;
+                return bad;
+            };
+            // Units in order of their contexts, longest first, where a lane can hold a chunk
+            // each: a unit's level is the number of units' lengths before it in its context,
+            // so a chunk has one unit in each of `count` levels from `level` on.
+            const bool sorted = p.sorted;
+            int my_q0 = 0, my_q_len = 0, my_ctx = 0, level = 0, count = 0;
+            if (sorted && lane < p.num_seqs) {
+                const int bad = chunk_of(lane, my_q0, my_q_len, my_ctx);
+                if (bad && blockIdx.x == 0) set_status(p.dev_status, bad);
+                level = (my_ctx - my_q_len) / R;
+                count = (my_q_len + R - 1) / R;
+            }
+            __syncwarp();
+            while (ok) {
+                // place -> unit; the KV heads side by side
+                const int h = place % p.Hkv;
+                const int rest = place / p.Hkv;
+                int c, unit, q0, q_len, ctx;
+                if (sorted) {
+                    // the lowest level that at most `rest` units are above, and of its units the
+                    // one that is left
+                    auto above = [&](int x) { return (int)__reduce_add_sync(0xffffffffu, min(max(level + count - x, 0), count)); };
+                    int lo = 0, hi = (int)__reduce_max_sync(0xffffffffu, level + count);
+                    while (lo < hi) {
+                        const int mid = (lo + hi) >> 1;
+                        if (above(mid + 1) <= rest)
+                            hi = mid;
+                        else
+                            lo = mid + 1;
+                    }
+                    const bool has = lane < p.num_seqs && lo >= level && lo < level + count;
+                    const uint32_t with = __ballot_sync(0xffffffffu, has);
+                    const int nth = rest - above(lo + 1);
+                    const uint32_t hit = __ballot_sync(0xffffffffu, has && __popc(with & ((1u << lane) - 1u)) == nth);
+                    c = hit ? __ffs(hit) - 1 : 0;
+                    unit = lo - __shfl_sync(0xffffffffu, level, c);
+                    q0 = __shfl_sync(0xffffffffu, my_q0, c);
+                    q_len = __shfl_sync(0xffffffffu, my_q_len, c);
+                    ctx = __shfl_sync(0xffffffffu, my_ctx, c);
+                    if (!hit) unit = q_len = 0;   // a place behind the last unit
+                } else {
+                    // chunk by chunk, the last unit first
+                    unit = p.units_per_seq - 1 - rest % p.units_per_seq;
+                    c = rest / p.units_per_seq;
+                    const int bad = chunk_of(c, q0, q_len, ctx);
+                    if (bad && unit == 0 && lane == 0) set_status(p.dev_status, bad);
+                }
+                const int i0 = unit * R;
+                if (i0 < q_len) {
                     QpUnit u = {};
                     u.h = h;
                     u.chunk = c;
                     u.row0 = q0 + i0;
-                    u.tokens = min(TILES * p.rtok, q_len - i0);
+                    u.tokens = min(R, q_len - i0);
                     u.first = ctx - q_len + i0;
                     u.wpos = max(u.first - p.window + 1, 0);
                     u.sink_pages = min((p.sinks + 15) / 16, (ctx + 15) / 16);
@@ -504,20 +551,25 @@ __global__ void __launch_bounds__(kQpThreads, 1)
             constexpr int N = 32 / ROWS;
             const int sub = lane / LANES, piece = lane % LANES;
             const uint32_t to = sbase + Sh::OFF_Q + t * Sh::Q_BYTES;
+            const uint4 *from = reinterpret_cast<const uint4 *>(static_cast<const T *>(p.q) +
+                                                                ((int64_t)u.row0 * p.Hq + (int64_t)u.h * p.G) * D) + piece;
+            const int mine_at = r < p.G * p.rtok && tok < u.tokens ? (tok * p.Hq + head) * LANES : -1;
             uint4 x[N];
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                const int rr = lane_base + i * ROWS + sub, tk = t * p.rtok + rr / p.G;
+                const int at = __shfl_sync(0xffffffffu, mine_at, i * ROWS + sub);
                 x[i] = make_uint4(0u, 0u, 0u, 0u);
-                if (rr < p.G * p.rtok && tk < u.tokens)
-                    x[i] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(p.q) +
-                                                                 ((int64_t)(u.row0 + tk) * p.Hq + (int64_t)u.h * p.G + rr % p.G) * D) +
-                                 piece);
+                if (at >= 0) x[i] = __ldg(from + at);
             }
             float scale = 0.f;
+            // (a loop, and the rows moved up in it: unrolled, this code, which runs once a
+            // unit, takes longer to come from memory than to run)
+#pragma unroll 1
+            for (int i0 = 0; i0 < N; i0 += 2) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+              for (int i2 = 0; i2 < 2; ++i2) {
+                const int i = i0 + i2;
+                const uint32_t w[4] = {x[i2].x, x[i2].y, x[i2].z, x[i2].w};
                 const uint32_t top2 = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
                                                __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
                 uint32_t top = max(top2 & 0xffffu, top2 >> 16);
@@ -554,6 +606,9 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                     }
                     asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + term * Sh::Q_TERM), "r"(c[0]), "r"(c[1]) : "memory");
                 }
+              }
+#pragma unroll
+              for (int k = 2; k < N; ++k) x[k - 2] = x[k];
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -967,7 +1022,9 @@ extern "C" int pkv_paged_prefill_attention_e4m3(void *out, const void *q, const 
     prm.Hkv = num_kv_heads;
     prm.G = G;
     prm.rtok = rtok;
+    prm.num_seqs = num_seqs;
     prm.units_per_seq = (int)units_of(qtiles);
+    prm.sorted = num_seqs <= 32 && grid > sms;
     const int64_t capacity = (int64_t)max_blocks_per_seq * 16;
     prm.window = window < capacity ? window : (int)capacity;   // no context is longer
     prm.sinks = num_sinks < capacity ? num_sinks : (int)capacity;
@@ -991,5 +1048,5 @@ extern "C" int pkv_paged_prefill_attention_e4m3(void *out, const void *q, const 
         return one ? launch(__nv_bfloat16(), No(), No(), tile) : launch(__nv_bfloat16(), No(), No(), tiles);
     }
     if (out_dtype == PKV_DTYPE_F32) return launch(__half(), Yes(), Yes(), tiles);
-    return one ? launch(__half(), No(), Yes(), tile) : launch(__half(), No(), Yes(), tiles);
+    return one ? launch(__half(), No(), No(), tile) : launch(__half(), No(), No(), tiles);
 }

@@ -99,6 +99,27 @@ def test_prefill_of_many_units(cuda_lib, dtype, out_dtype, d, window, sinks):
     assert torch.equal(got, st.prefill(out_dtype)) and st.status.item() == 0
 
 
+@pytest.mark.parametrize("chunks,extra", [(3, 0), (32, 300), (33, 0), (60, 77)])
+@pytest.mark.parametrize("Hq,Hkv,d,out_dtype", [(16, 16, 64, BF16), (30, 10, 128, F32)])
+def test_prefill_takes_every_unit_once(cuda_lib, chunks, extra, Hq, Hkv, d, out_dtype):
+    """Chunks of no row, of one and of many, behind contexts of their own, with a max_q_len that none reaches; some that
+    are refused among them: the rows of those stay as they were, every other has its output."""
+    qn = [[170, 0, 1, 64, 65, 130][i % 6] + (i if i % 6 == 0 else 0) for i in range(chunks)]
+    ctx = [n + [900, 3, 400, 0, 64, 31][(i // 2) % 6] for i, n in enumerate(qn)]
+    st = Step(ctx, qn, Hq, Hkv, d, BF16, 500, 3, seed=chunks, poison=False)
+    want, bound = st.reference(out_dtype)
+    got = st.prefill(out_dtype, max_q=max(qn) + extra)
+    ref.assert_within(got, want, bound)
+    assert st.status.item() == 0 and torch.equal(got, st.prefill(out_dtype))
+    st.dev["ctx"][0] = qn[0] - 1              # fewer positions than rows
+    st.dev["ctx"][2] = st.dev["table"].shape[1] * 16 + 1
+    got = st.prefill(out_dtype, max_q=max(qn) + extra).cpu()
+    rows = torch.arange(sum(qn))
+    bad = (rows < qn[0]) | (rows == qn[0])    # chunk 2 is the row behind chunk 0's
+    assert got[bad].isnan().all() and st.status.item() == BAD_CHUNK | BAD_CONTEXT
+    ref.assert_within(got[~bad], want[~bad], bound[~bad])
+
+
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("spread", [3.0, 10.0])
 def test_scales_far_apart(cuda_lib, d, spread):
