@@ -81,6 +81,7 @@ struct QuantPrefillParams {
 };
 
 struct QpUnit : WpUnit {
+    int tile0;                     // the CTA's first key tile of them (u.tiles: its own)
     int chunk, sink_pages, skip;   // page v of the list is logical page v, or v + skip from sink_pages on
 };
 
@@ -140,9 +141,9 @@ __device__ __forceinline__ uint32_t code_piece(int r, int c) {
     return D == 128 ? (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)) : (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
 }
 
-// WIDE: a 32-bit output.  RES: weights as value and residual.  TILES: query tiles
-// of a unit, 2, or 1 (A alone)
-template <typename T, int D, bool WIDE, bool RES, int TILES>
+// WIDE: a 32-bit output, and weights as value and residual.  TILES: query tiles of
+// a unit, 2, or 1 (A alone; the CTAs of a cluster share its keys)
+template <typename T, int D, bool WIDE, int TILES>
 __global__ void __launch_bounds__(kQpThreads, 1)
     quant_prefill_kernel(const QuantPrefillParams p, const __grid_constant__ CUtensorMap tk,
                          const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tout) {
@@ -153,6 +154,10 @@ __global__ void __launch_bounds__(kQpThreads, 1)
     QpUnit *units = reinterpret_cast<QpUnit *>(sm + Sh::OFF_UNIT);
     float2 *page_scales = reinterpret_cast<float2 *>(sm + Sh::OFF_SCALES);   // [stage][page] a, log2 b
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 1);
+    // What the CTAs of a cluster that share a unit tell one another: a row's m and l,
+    // where the query was; its O, by weight, where V was.
+    float2 *stats = reinterpret_cast<float2 *>(sm + Sh::OFF_Q);
+    const int rank = TILES == 1 ? (int)cluster_ctarank() : 0, ranks = TILES == 1 ? (int)cluster_nctarank() : 1;
     volatile int *gave_up = reinterpret_cast<volatile int *>(tmem_slot + 1);   // a wait of this CTA ran out
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -179,6 +184,7 @@ __global__ void __launch_bounds__(kQpThreads, 1)
         }
         mbar_init(&bars->cancel, 1);
         *gave_up = 0;
+        units[0].tokens = 0;
         fence_mbar_init();
         prefetch_tensormap(&tk);
         prefetch_tensormap(&tv);
@@ -220,6 +226,7 @@ __global__ void __launch_bounds__(kQpThreads, 1)
         if (lane == 0) tc::mbar_arrive_cta(&bars->unit_empty[n & 1]);
         return u.tiles > 0;
     };
+    auto tile0 = [](const QpUnit &u) { return TILES == 1 ? u.tile0 : 0; };
     // the block id of page v of a unit's list; -1: none is wanted there
     auto page_id = [&](const QpUnit &u, int v) {
         if (16 * v >= u.ctx) return -1;
@@ -230,7 +237,7 @@ __global__ void __launch_bounds__(kQpThreads, 1)
         tc::setmaxnreg_dec<kQpLowRegs>();
         if (warp == 0) {
             // ---------------- scheduler and TMA producer ----------------
-            int place = blockIdx.x;
+            int place = blockIdx.x / ranks;
             int n = 0;              // units published
             uint32_t g = 0;         // key tiles loaded
             uint32_t asked = 0;     // places asked for
@@ -262,7 +269,7 @@ __global__ void __launch_bounds__(kQpThreads, 1)
             // Units in order of their contexts, longest first, where a lane can hold a chunk
             // each: a unit's level is the number of units' lengths before it in its context,
             // so a chunk has one unit in each of `count` levels from `level` on.
-            const bool sorted = p.sorted;
+            const bool sorted = TILES == 2 && p.sorted;
             int my_q0 = 0, my_q_len = 0, my_ctx = 0, level = 0, count = 0;
             if (sorted && lane < p.num_seqs) {
                 const int bad = chunk_of(lane, my_q0, my_q_len, my_ctx);
@@ -320,6 +327,15 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                     u.wpos -= 16 * u.skip;
                     u.ctx = ctx - 16 * u.skip;
                     u.tiles = (u.first + u.tokens - 1) / kQpKeys + 1;
+                    if constexpr (TILES == 1) {   // the CTA's part of the key tiles: none, where there are few
+                        const int all = u.tiles;
+                        u.tile0 = all * rank / ranks;   // (fewer than 2^27 tiles)
+                        u.tiles = all * (rank + 1) / ranks - u.tile0;
+                        if (u.tiles == 0) {
+                            if (lane == 0) units[0] = u;
+                            break;
+                        }
+                    }
                     if (n >= 2) ok = wait_all(&bars->unit_empty[n & 1], (uint32_t)(n / 2 - 1));
                     if (!ok) break;
                     if (lane == 0) {
@@ -327,12 +343,12 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                         tc::mbar_arrive_cta(&bars->unit_full[n & 1]);
                     }
                     // lane i < 8 reads the block id of page i of the tile, one tile ahead
-                    int blk_next = lane < kQpPages ? page_id(u, lane) : -1;
+                    int blk_next = lane < kQpPages ? page_id(u, tile0(u) * kQpPages + lane) : -1;
                     for (int j = 0; ok && j < u.tiles; ++j, ++g) {
                         // the next place is asked for near the unit's end (see window_prefill.cu)
-                        if (j + 2 >= u.tiles) ask();
+                        if (TILES == 2 && j + 2 >= u.tiles) ask();
                         const int blk = blk_next;
-                        const int v = j * kQpPages + lane;
+                        const int v = (tile0(u) + j) * kQpPages + lane;
                         if (j + 1 < u.tiles) blk_next = lane < kQpPages ? page_id(u, v + kQpPages) : -1;
                         int y = p.num_blocks * p.Hkv * 16;     // row past the pool: zero fill
                         if (lane < kQpPages && 16 * v < u.ctx) {
@@ -371,7 +387,7 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                     }
                     ++n;
                 }
-                if (!ok) break;
+                if (TILES == 1 || !ok) break;   // (one query tile: every unit has its CTAs)
                 ask();
                 ok = wait_all(&bars->cancel, asked - 1);
                 if (!ok) break;
@@ -457,9 +473,9 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                                     const uint32_t ph = d_s + 32 * (kk >> 1) + 8 * (kk & 1);
                                     const uint64_t vp = vb + (uint32_t)(kk * Sh::PAGE >> 4);
                                     tc::mma_f16_ts(d_o, ph, vp, idesc_o, j > 0 || kk > 0);
-                                    if (RES) tc::mma_f16_ts(d_o, ph + 16, vp, idesc_o, true);   // the weights' rounding residual
+                                    if (WIDE) tc::mma_f16_ts(d_o, ph + 16, vp, idesc_o, true);   // the weights' rounding residual
                                 }
-                                if (RES && part == 0) tc::mma_commit(&bars->half_done[t]);
+                                if (WIDE && part == 0) tc::mma_commit(&bars->half_done[t]);
                             }
                             __syncwarp();
                         }
@@ -492,7 +508,7 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                     if (!ok) break;
                     const uint32_t from = sbase + Sh::OFF_CODES + st * Sh::CODE_TILE;
                     const uint32_t to = sbase + Sh::OFF_V + st * Sh::TILE;
-                    const WpHidden hid(u, j * kQpKeys, p.sinks, kQpKeys);
+                    const WpHidden hid(u, (tile0(u) + j) * kQpKeys, p.sinks, kQpKeys);
                     const bool any = hid.any();
                     // two groups of 8 rows at a time, the next ones' codes on their way
                     uint4 codes[2][2][Sh::HALVES];
@@ -618,6 +634,7 @@ __global__ void __launch_bounds__(kQpThreads, 1)
         uint32_t g = 0;                                 // key tiles taken
         QpUnit u;
         bool ok = t < TILES && take_unit(0, u);
+        if (TILES == 1 && t == 0 && !ok) stats[r] = make_float2(-INFINITY, 0.f);   // no key of this CTA's
         float rowscale = 0.f;
         if (ok) rowscale = split_query(u);
         for (int n = 0; ok; ++n) {
@@ -629,8 +646,8 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                 ok = wait_all(&bars->scales_full[st], g / kQpScaleStages) && wait_all(&bars->s_full[t], g);
                 if (!ok) break;
                 tc::fence_after_sync();
-                if constexpr (!RES) {
-                    const int key0 = j * kQpKeys;
+                if constexpr (!WIDE) {
+                    const int key0 = (tile0(u) + j) * kQpKeys;
                     float v[kQpKeys];
 #pragma unroll
                     for (int cc = 0; cc < kQpKeys; cc += 32) tc::tmem_ld32(scol + cc, *reinterpret_cast<float(*)[32]>(v + cc));
@@ -739,7 +756,7 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                         }
                         tc::tmem_wait_ld();
                         // hidden: past the row's position; below its window and behind the first tokens
-                        const int key0 = j * kQpKeys + part * kHalf;
+                        const int key0 = (tile0(u) + j) * kQpKeys + part * kHalf;
                         const int lim = pos - key0, low = lim - p.window + 1, sk = p.sinks - key0;
                         if (__any_sync(0xffffffffu, lim < kHalf - 1 || (low > 0 && sk < kHalf))) {
                             auto below = [](int n) { return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u); };
@@ -850,6 +867,10 @@ __global__ void __launch_bounds__(kQpThreads, 1)
             ok = wait_all(&bars->o_done[t], (uint32_t)n);
             if (!ok) break;
             tc::fence_after_sync();
+            if (TILES == 1 && ranks > 1) {
+                stats[r] = make_float2(m_used, l);
+                break;
+            }
             const float inv = 1.f / l;
             // 128 bytes of each row at a time, through shared memory (see window_prefill.cu)
             constexpr int kCols = WIDE ? 32 : 64;      // a 32-bit output or a 16-bit one
@@ -909,6 +930,73 @@ __global__ void __launch_bounds__(kQpThreads, 1)
             rowscale = rowscale_next;
         }
         if (lane == 0) stores_done();
+        if constexpr (TILES == 1) {
+            if (ranks > 1) {
+                // ---- the parts of a unit: each CTA brings its O to the row's largest m and
+                // total l, and sums a slice of the rows over the CTAs, in their order ----
+                __syncwarp();
+                cluster_sync();
+                const int tokens = units[0].tokens, row0 = units[0].row0, h = units[0].h;
+                float *part = reinterpret_cast<float *>(sm + Sh::OFF_V);
+                if (t == 0 && units[0].tiles > 0) {
+                    float m = -INFINITY, total = 0.f;
+                    for (int c = 0; c < ranks; ++c) m = fmaxf(m, ld_cluster_f32x2(cluster_addr(stats + r, c)).x);
+                    for (int c = 0; c < ranks; ++c) {
+                        const float2 s = ld_cluster_f32x2(cluster_addr(stats + r, c));
+                        total = fmaf(s.y, exp2_approx(s.x - m), total);
+                    }
+                    // (a query that is not finite has no m, and NaN for its weight)
+                    const float w = exp2_approx(stats[r].x - m) / total;
+#pragma unroll 1
+                    for (int cc = 0; cc < D; cc += 32) {
+                        float o[32];
+                        tc::tmem_ld32(ocol + cc, o);
+                        tc::tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            *reinterpret_cast<float4 *>(part + r * D + (((cc / 4 + e) ^ (r & 7)) << 2)) =
+                                make_float4(o[4 * e] * w, o[4 * e + 1] * w, o[4 * e + 2] * w, o[4 * e + 3] * w);
+                    }
+                }
+                __syncwarp();
+                cluster_sync();
+                constexpr int LANES = D / 4, ROWS = 32 / LANES;   // lanes a row, rows a warp at a time
+                const int end = kQpRows * (rank + 1) / ranks;
+#pragma unroll 1
+                for (int row = kQpRows * rank / ranks + (warp - 4) * ROWS + lane / LANES; row < end; row += 8 * ROWS) {
+                    const int tk = row / p.G, col = (lane % LANES) * 4;
+                    if (row >= p.G * p.rtok || tk >= tokens) continue;
+                    float m = -INFINITY;
+                    for (int c = 0; c < ranks; ++c) m = fmaxf(m, ld_cluster_f32x2(cluster_addr(stats + row, c)).x);
+                    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int c = 0; c < ranks; ++c) {
+                        // (where a CTA saw no key of the row's, nothing may be there)
+                        if (ld_cluster_f32x2(cluster_addr(stats + row, c)).x == -INFINITY && m > -INFINITY) continue;
+                        const float4 x = ld_cluster_f32x4(cluster_addr(part + row * D + (((col >> 2) ^ (row & 7)) << 2), c));
+                        sum.x += x.x;
+                        sum.y += x.y;
+                        sum.z += x.z;
+                        sum.w += x.w;
+                    }
+                    const int64_t at = ((int64_t)(row0 + tk) * p.Hq + (int64_t)h * p.G + row % p.G) * D + col;
+                    if constexpr (WIDE)
+                        *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at) = sum;
+                    else
+                        *reinterpret_cast<uint2 *>(static_cast<T *>(p.out) + at) = make_uint2(pack2<T>(sum.x, sum.y), pack2<T>(sum.z, sum.w));
+                }
+            }
+        }
+    }
+    if constexpr (TILES == 1) {
+        // (and a CTA's shared memory outlives its readers)
+        __syncwarp();
+        if (ranks > 1) {
+            if (warp < 4) {
+                cluster_sync();
+                cluster_sync();
+            }
+            cluster_sync();
+        }
     }
 
     tc::fence_before_sync();
@@ -928,11 +1016,11 @@ static int encode_code_page_map(CUtensorMap *map, const void *base, int num_bloc
     return encode_tiled_map(map, base, 2, dims, strides, box, head_dim);
 }
 
-template <typename T, int D, bool WIDE, bool RES, int TILES>
+template <typename T, int D, bool WIDE, int TILES>
 static int launch_quant_prefill(const QuantPrefillParams &prm, const CUtensorMap &tk, const CUtensorMap &tv,
-                                const CUtensorMap &tout, int grid, cudaStream_t stream) {
+                                const CUtensorMap &tout, int grid, int ranks, cudaStream_t stream) {
     using Sh = QpShape<T, D>;
-    const auto kernel = quant_prefill_kernel<T, D, WIDE, RES, TILES>;
+    const auto kernel = quant_prefill_kernel<T, D, WIDE, TILES>;
     // the register split inside the kernel waits for registers that only exist
     // if the compiled count is the one it was sized for: check it (once; the
     // answer does not change) and refuse to launch otherwise
@@ -956,7 +1044,11 @@ static int launch_quant_prefill(const QuantPrefillParams &prm, const CUtensorMap
         if (e != cudaSuccess) return cuda_fail(e);
         mark_done_on_device(&attr_set);
     }
-    cudaError_t e = launch_pdl(kernel, dim3(grid), dim3(kQpThreads), Sh::SMEM_BYTES, stream, prm, tk, tv, tout);
+    cudaError_t e;
+    if constexpr (TILES == 1)
+        e = launch_cluster(kernel, grid * ranks, ranks, kQpThreads, Sh::SMEM_BYTES, stream, prm, tk, tv, tout);
+    else
+        e = launch_pdl(kernel, dim3(grid), dim3(kQpThreads), Sh::SMEM_BYTES, stream, prm, tk, tv, tout);
     if (e == cudaSuccess) e = cudaGetLastError();
     return e == cudaSuccess ? PKV_OK : cuda_fail(e);
 }
@@ -990,10 +1082,16 @@ extern "C" int pkv_paged_prefill_attention_e4m3(void *out, const void *q, const 
     // query tiles of a unit: two, which share every K and V tile; or one, when
     // all units then run at once and a step of 128 keys has one tile's products
     auto units_of = [&](int tiles) { return ((int64_t)max_q_len + tiles * rtok - 1) / (tiles * rtok); };
-    const bool one = out_dtype != PKV_DTYPE_F32 && num_seqs * units_of(1) * num_kv_heads <= sms;
+    const bool one = num_seqs * units_of(1) * num_kv_heads <= sms;
     const int qtiles = one ? 1 : 2;
     const int64_t grid = (int64_t)num_seqs * units_of(qtiles) * num_kv_heads;
     if (grid >= (int64_t)1 << 31) return PKV_ERR_UNSUPPORTED;
+    // where most SMs would have none, a unit's keys go to the CTAs of a cluster,
+    // two key tiles each or more if contexts fill their tables
+    const int64_t capacity = (int64_t)max_blocks_per_seq * 16;
+    const int64_t keys = window < capacity && num_sinks < capacity - window ? (int64_t)window + num_sinks + max_q_len : capacity;
+    int ranks = 1;
+    while (one && ranks < 8 && grid * ranks * 2 <= sms && ranks * 2 * 2 * kQpKeys <= keys) ranks *= 2;
     CUtensorMap tk, tv;
     rc = encode_code_page_map(&tk, k_cache, num_blocks, num_kv_heads, head_dim);
     if (rc != PKV_OK) return rc;
@@ -1025,28 +1123,24 @@ extern "C" int pkv_paged_prefill_attention_e4m3(void *out, const void *q, const 
     prm.num_seqs = num_seqs;
     prm.units_per_seq = (int)units_of(qtiles);
     prm.sorted = num_seqs <= 32 && grid > sms;
-    const int64_t capacity = (int64_t)max_blocks_per_seq * 16;
     prm.window = window < capacity ? window : (int)capacity;   // no context is longer
     prm.sinks = num_sinks < capacity ? num_sinks : (int)capacity;
     prm.total_q = total_q;
     prm.max_q_len = max_q_len;
     prm.scale_log2 = scale * 1.4426950408889634f;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    auto launch = [&](auto type, auto wide, auto residual, auto tiles) {
+    auto launch = [&](auto type, auto wide, auto tiles) {
         using T = decltype(type);
-        constexpr bool W = decltype(wide)::value, R = decltype(residual)::value;
+        constexpr bool W = decltype(wide)::value;
         constexpr int N = decltype(tiles)::value;
-        return head_dim == 128 ? launch_quant_prefill<T, 128, W, R, N>(prm, tk, tv, tout, (int)grid, st)
-                               : launch_quant_prefill<T, 64, W, R, N>(prm, tk, tv, tout, (int)grid, st);
+        return head_dim == 128 ? launch_quant_prefill<T, 128, W, N>(prm, tk, tv, tout, (int)grid, ranks, st)
+                               : launch_quant_prefill<T, 64, W, N>(prm, tk, tv, tout, (int)grid, ranks, st);
     };
-    using Yes = std::true_type;
-    using No = std::false_type;
-    std::integral_constant<int, 1> tile;
-    std::integral_constant<int, 2> tiles;
-    if (dtype == PKV_DTYPE_BF16) {
-        if (out_dtype == PKV_DTYPE_F32) return launch(__nv_bfloat16(), Yes(), Yes(), tiles);
-        return one ? launch(__nv_bfloat16(), No(), No(), tile) : launch(__nv_bfloat16(), No(), No(), tiles);
-    }
-    if (out_dtype == PKV_DTYPE_F32) return launch(__half(), Yes(), Yes(), tiles);
-    return one ? launch(__half(), No(), No(), tile) : launch(__half(), No(), No(), tiles);
+    auto typed = [&](auto type) {
+        std::integral_constant<int, 1> tile;
+        std::integral_constant<int, 2> tiles;
+        if (out_dtype == PKV_DTYPE_F32) return one ? launch(type, std::true_type(), tile) : launch(type, std::true_type(), tiles);
+        return one ? launch(type, std::false_type(), tile) : launch(type, std::false_type(), tiles);
+    };
+    return dtype == PKV_DTYPE_BF16 ? typed(__nv_bfloat16()) : typed(__half());
 }

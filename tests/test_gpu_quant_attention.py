@@ -99,6 +99,20 @@ def test_prefill_of_many_units(cuda_lib, dtype, out_dtype, d, window, sinks):
     assert torch.equal(got, st.prefill(out_dtype)) and st.status.item() == 0
 
 
+@pytest.mark.parametrize("ctx,qn", [([9000], [3]), ([5000], [200]), ([4097, 1, 40], [1, 1, 33]), ([300, 2600, 0, 128], [32, 64, 0, 128]),
+                                    ([129], [129]), ([1300, 700], [64, 64])])
+@pytest.mark.parametrize("window,sinks", [(WHOLE, 0), (700, 33), (20, 0)])
+@pytest.mark.parametrize("Hq,Hkv,d,dtype,out_dtype", [(4, 1, 128, BF16, BF16), (10, 2, 64, F16, F32), (8, 1, 128, F16, F16),
+                                                      (3, 1, 64, BF16, F32)])
+def test_prefill_of_few_rows(cuda_lib, ctx, qn, window, sinks, Hq, Hkv, d, dtype, out_dtype):
+    """A unit's keys over several CTAs, some without a key; the same bits at every call."""
+    st = Step(ctx, qn, Hq, Hkv, d, dtype, window, sinks, seed=ctx[0] % 89, heavy=d == 64)
+    want, bound = st.reference(out_dtype)
+    got = st.prefill(out_dtype)
+    ref.assert_within(got, want, bound)
+    assert st.status.item() == 0 and torch.equal(got, st.prefill(out_dtype))
+
+
 @pytest.mark.parametrize("chunks,extra", [(3, 0), (32, 300), (33, 0), (60, 77)])
 @pytest.mark.parametrize("Hq,Hkv,d,out_dtype", [(16, 16, 64, BF16), (30, 10, 128, F32)])
 def test_prefill_takes_every_unit_once(cuda_lib, chunks, extra, Hq, Hkv, d, out_dtype):
