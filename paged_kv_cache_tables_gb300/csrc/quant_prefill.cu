@@ -416,80 +416,76 @@ __global__ void __launch_bounds__(kQpThreads, 1)
             }
         } else if (warp == 1) {
             // ---------------- MMA issuer ----------------
-            // The whole warp walks the schedule, so the waits and the
-            // descriptor arithmetic are warp-uniform; one elected lane issues
-            // each MMA and commit.  The query tiles take turns: P V of a key tile
-            // and S of the next are one turn, so that a tile's softmax runs beside
-            // the other's turn.
-            const bool leader = tc::elect_one();
-            constexpr uint32_t idesc_s = tc::idesc_e4m3(kQpRows, kQpKeys);
-            constexpr uint32_t idesc_o = tc::idesc_f16(false, false, true, kQpRows, D);
-            auto code_desc = [&](uint32_t at) { return D == 128 ? tc::smem_desc_sw128(at, 16, 1024) : tc::smem_desc_sw64(at, 16, 512); };
-            const uint64_t q_desc = code_desc(sbase + Sh::OFF_Q);
-            const uint64_t k_desc = code_desc(sbase + Sh::OFF_K);
-            const uint64_t v_desc = tc::smem_desc_sw128(sbase + Sh::OFF_V, 1024, Sh::GROUP);
-            uint32_t g = 0;     // key tiles done
-            auto issue_s = [&](int t, uint32_t k) {   // S = Q K^T of query tile t and key tile k
-                if (t == 0 && !wait_all(&bars->k_full[k & 1], k / 2)) return false;
-                tc::fence_after_sync();
-                const uint64_t qb = q_desc + (uint64_t)((t * Sh::Q_BYTES) >> 4);
-                const uint64_t kb = k_desc + (uint64_t)(((k & 1) * Sh::CODE_TILE) >> 4);
-                constexpr int STEPS = D / 32;
-                if (leader) {
+            // One thread, which is the tensor cores' bottleneck unless it is quick: it
+            // waits alone (a wait of the whole warp costs a vote and two meetings, and
+            // there are six a key tile).  The query tiles take turns: P V of a key tile
+            // and S of the next are one turn, so that a tile's softmax runs beside the
+            // other's turn.
+            if (tc::elect_one()) {
+                constexpr uint32_t idesc_s = tc::idesc_e4m3(kQpRows, kQpKeys);
+                constexpr uint32_t idesc_o = tc::idesc_f16(false, false, true, kQpRows, D);
+                auto code_desc = [&](uint32_t at) { return D == 128 ? tc::smem_desc_sw128(at, 16, 1024) : tc::smem_desc_sw64(at, 16, 512); };
+                // descriptors: the upper half, and the lower one of each operand's first byte
+                const uint32_t code_high = (uint32_t)(code_desc(0) >> 32);
+                const uint32_t q_low = (uint32_t)code_desc(sbase + Sh::OFF_Q), k_low = (uint32_t)code_desc(sbase + Sh::OFF_K);
+                const uint64_t v_desc = tc::smem_desc_sw128(sbase + Sh::OFF_V, 1024, Sh::GROUP);
+                const uint32_t v_high = (uint32_t)(v_desc >> 32), v_low = (uint32_t)v_desc;
+                uint32_t g = 0;     // key tiles done
+                auto issue_s = [&](int t, uint32_t k) {   // S = Q K^T of query tile t and key tile k
+                    if (t == 0 && !wait(&bars->k_full[k & 1], k / 2)) return false;
+                    tc::fence_after_sync();
+                    const uint32_t qb = q_low + ((t * Sh::Q_BYTES) >> 4), kb = k_low + (((k & 1) * Sh::CODE_TILE) >> 4);
+                    constexpr int STEPS = D / 32;
 #pragma unroll
                     for (int i = 0; i < Sh::TERMS * STEPS; ++i) {
                         const uint32_t qo = ((i / STEPS) * Sh::Q_TERM + (i % STEPS) * 32) >> 4, ko = ((i % STEPS) * 32) >> 4;
-                        tc::mma_f8_ss(tmem + t * 256, qb + qo, kb + ko, idesc_s, i > 0);
+                        tc::mma_f8_ss(tmem + t * 256, qb + qo, kb + ko, code_high, idesc_s, i > 0);
                     }
                     tc::mma_commit(&bars->s_full[t]);
                     if (t == TILES - 1) tc::mma_commit(&bars->k_empty[k & 1]);
-                }
-                __syncwarp();
-                return true;
-            };
-            QpUnit u;
-            for (int n = 0; take_unit(n, u); ++n) {
-                const int tiles = u.tiles;
-                bool ok = true;
-                // (S may be written: the product that read P over it was issued before)
+                    return true;
+                };
+                for (int n = 0;; ++n) {
+                    if (!wait(&bars->unit_full[n & 1], (uint32_t)(n / 2))) break;
+                    const int tiles = units[n & 1].tiles;
+                    tc::mbar_arrive_cta(&bars->unit_empty[n & 1]);
+                    if (tiles == 0) break;
+                    bool ok = true;
+                    // (S may be written: the product that read P over it was issued before)
 #pragma unroll
-                for (int t = 0; t < TILES; ++t) ok = ok && wait_all(&bars->q_full[t], (uint32_t)n) && issue_s(t, g);
-                for (int j = 0; ok && j < tiles; ++j, ++g) {
-                    const uint64_t vb = v_desc + (uint64_t)(((g & 1) * Sh::TILE) >> 4);
-                    ok = wait_all(&bars->v_full[g & 1], g / 2);
+                    for (int t = 0; t < TILES; ++t) ok = ok && wait(&bars->q_full[t], (uint32_t)n) && issue_s(t, g);
+                    for (int j = 0; ok && j < tiles; ++j, ++g) {
+                        const uint32_t vb = v_low + (((g & 1) * Sh::TILE) >> 4);
+                        ok = wait(&bars->v_full[g & 1], g / 2);
 #pragma unroll
-                    for (int t = 0; t < TILES; ++t) {
-                        const uint32_t d_s = tmem + t * 256, d_o = d_s + 128;
+                        for (int t = 0; t < TILES; ++t) {
+                            const uint32_t d_s = tmem + t * 256, d_o = d_s + 128;
 #pragma unroll
-                        for (int part = 0; part < 2; ++part) {
-                            // P of a unit's first tile is there only after the unit before's O was read
-                            ok = ok && wait_all(&bars->p_full[t][part], g);
-                            if (!ok) break;
-                            tc::fence_after_sync();
-                            if (leader) {
+                            for (int part = 0; part < 2; ++part) {
+                                // P of a unit's first tile is there only after the unit before's O was read
+                                ok = ok && wait(&bars->p_full[t][part], g);
+                                if (!ok) break;
+                                tc::fence_after_sync();
 #pragma unroll
                                 for (int kk = part * kQpPages / 2; kk < (part + 1) * kQpPages / 2; ++kk) {
                                     // O (+)= P V, a page at a time
                                     const uint32_t ph = d_s + 32 * (kk >> 1) + 8 * (kk & 1);
-                                    const uint64_t vp = vb + (uint32_t)(kk * Sh::PAGE >> 4);
-                                    tc::mma_f16_ts(d_o, ph, vp, idesc_o, j > 0 || kk > 0);
-                                    if (WIDE) tc::mma_f16_ts(d_o, ph + 16, vp, idesc_o, true);   // the weights' rounding residual
+                                    const uint32_t vp = vb + (uint32_t)(kk * Sh::PAGE >> 4);
+                                    tc::mma_f16_ts(d_o, ph, vp, v_high, idesc_o, j > 0 || kk > 0);
+                                    if (WIDE) tc::mma_f16_ts(d_o, ph + 16, vp, v_high, idesc_o, true);   // the weights' rounding residual
                                 }
                                 if (WIDE && part == 0) tc::mma_commit(&bars->half_done[t]);
                             }
-                            __syncwarp();
-                        }
-                        if (!ok) break;
-                        if (leader) {
+                            if (!ok) break;
                             if (t == TILES - 1) tc::mma_commit(&bars->v_empty[g & 1]);
                             if (j + 1 == tiles) tc::mma_commit(&bars->o_done[t]);
+                            else ok = issue_s(t, g + 1);
                         }
-                        __syncwarp();
-                        if (j + 1 < tiles) ok = issue_s(t, g + 1);
                     }
+                    if (!ok) break;
                 }
-                if (!ok) break;
             }
+            __syncwarp();
         } else {
             // ---------------- V's codes to fp16 ----------------
             // A warp takes 64 rows, 8 rows x 4 pieces of 16 codes at a time, each lane a
