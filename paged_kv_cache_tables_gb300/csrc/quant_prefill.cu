@@ -17,10 +17,11 @@
 //                two terms hold bf16's 8 bits, three fp16's 11, down to 2^-10 (2^-18
 //                of the largest element at most).  As many steps as in 16 bits, or
 //                one and a half times for fp16.
-//   O += P v     in fp16: v is converted on the way (exact).  P for a 16-bit output
-//                is rounded once (2^-11 of a weight: an eighth of what the output's
-//                own rounding may be in bf16, and as much in fp16), for a 32-bit one
-//                value and residual, two products.
+//   O += P v     in fp16: v is converted on the way (exact).  P for a bf16 output
+//                is rounded once (2^-11 of a weight, an eighth of what the output's
+//                own rounding may be), else value and residual, two products (an
+//                fp16 output from P rounded once would be off by 1.25 times its own
+//                rounding, and take 81 us instead of 100 for 5 x 2,000 rows of head_dim 64).
 // (P in e4m3 terms would take three for a bf16 output: more steps than fp16's one,
 // and a conversion of every weight three times instead of V's once a tile.)
 //
@@ -141,13 +142,14 @@ __device__ __forceinline__ uint32_t code_piece(int r, int c) {
     return D == 128 ? (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)) : (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
 }
 
-// WIDE: a 32-bit output, and weights as value and residual.  TILES: query tiles of
+// WIDE: a 32-bit output.  TILES: query tiles of
 // a unit, 2, or 1 (A alone; the CTAs of a cluster share its keys)
 template <typename T, int D, bool WIDE, int TILES>
 __global__ void __launch_bounds__(kQpThreads, 1)
     quant_prefill_kernel(const QuantPrefillParams p, const __grid_constant__ CUtensorMap tk,
                          const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tout) {
     using Sh = QpShape<T, D>;
+    constexpr bool RES = WIDE || std::is_same<T, __half>::value;   // weights as value and residual (an fp16 or 32-bit output)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     QpBars *bars = reinterpret_cast<QpBars *>(sm + Sh::OFF_BAR);
@@ -472,9 +474,9 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                                     const uint32_t ph = d_s + 32 * (kk >> 1) + 8 * (kk & 1);
                                     const uint32_t vp = vb + (uint32_t)(kk * Sh::PAGE >> 4);
                                     tc::mma_f16_ts(d_o, ph, vp, v_high, idesc_o, j > 0 || kk > 0);
-                                    if (WIDE) tc::mma_f16_ts(d_o, ph + 16, vp, v_high, idesc_o, true);   // the weights' rounding residual
+                                    if (RES) tc::mma_f16_ts(d_o, ph + 16, vp, v_high, idesc_o, true);   // the weights' rounding residual
                                 }
-                                if (WIDE && part == 0) tc::mma_commit(&bars->half_done[t]);
+                                if (RES && part == 0) tc::mma_commit(&bars->half_done[t]);
                             }
                             if (!ok) break;
                             if (t == TILES - 1) tc::mma_commit(&bars->v_empty[g & 1]);
@@ -642,7 +644,7 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                 ok = wait_all(&bars->scales_full[st], g / kQpScaleStages) && wait_all(&bars->s_full[t], g);
                 if (!ok) break;
                 tc::fence_after_sync();
-                if constexpr (!WIDE) {
+                if constexpr (!RES) {
                     const int key0 = (tile0(u) + j) * kQpKeys;
                     float v[kQpKeys];
 #pragma unroll

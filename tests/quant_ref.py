@@ -7,12 +7,11 @@ found among the table's midpoints, so no conversion of torch's is relied on.
 Bounds.  A row is read back as code times scale, rounded once to the output's
 type: half a step.  Attention: as in window_ref for scores, exp2 and the fp32
 sums; the softmax weights, times the block's scale and at least 2^6 where the
-largest of a row stands, meet the codes as fp16 values: with a 16-bit output
+largest of a row stands, meet the codes as fp16 values: with a bf16 output
 rounded once, half a step of fp16 (2^-11 relative), or of its subnormals (2^-25,
 against weights of which one is at least 2^6: 2^-31 times the largest |v| the
 scales can hold, for each position); else value and residual, which is inside
-window_ref's 2^-16 and the subnormals' half step again (decode takes both for
-every output, and is well inside).  log2 of a V scale off by
+window_ref's 2^-16 and the subnormals' half step again.  log2 of a V scale off by
 half a step of fp32 at up to 2^7 (2^-18, in the exponent, so 2^-18 of the weight
 in the products but not in the sum), the scale's reciprocal by 2^-23.
 """
@@ -109,7 +108,7 @@ def attention_bound(out, spread, mass, d, scale, out_dtype, largest_v, n):
     """largest_v: the largest |v| that the scales of the visible blocks can hold (448 s); n: positions."""
     ds = d * 2.0 ** -23 * mass * scale
     err = (2 * ds + 2.0 ** -16 + 2.0 ** -18 + 2.0 ** -22 + 2.0 ** -14) * spread + 2.0 ** -31 * largest_v * n
-    if out_dtype != F32:
+    if out_dtype == BF16:
         err = err + 2.0 ** -11 * spread
     return err + ref.rounding(out, err, out_dtype)
 
