@@ -472,7 +472,8 @@ int pkv_kv_append_e4m3(const void *k, int64_t k_stride, const void *v, int64_t v
  *                 cu[s] + i receives position first[s] + i of sequence s, its
  *                 codes times their scale, rounded once
  *   first         device int32 [num_seqs], or NULL: 0 for all
- * Rows from cu[num_seqs] on are left as they were.  A position outside the table
+ * Rows from cu[num_seqs] on, and from `total` on, are left as they were.
+ * num_kv_heads <= 65,536 (PKV_ERR_UNSUPPORTED).  A position outside the table
  * (PKV_DEV_BAD_CONTEXT) or a block id outside the pool (PKV_DEV_BAD_BLOCK_ID)
  * gives zeros.
  */

@@ -29,11 +29,31 @@
 // 12 of them):
 //   0      TMA and scheduler: takes units, publishes them, loads K and V tiles of
 //          codes, 8 pages of 16, a page one box, and the pages' scales (a, log2 b)
-//   1      issues the MMAs of both query tiles, turn by turn
+//   1      one thread issues the MMAs of both query tiles, turn by turn
 //   2, 3   V's codes to fp16, in the layout of an MN-major operand; rows that no row
 //          of the unit sees become zero (they may hold NaN codes)
 //   4-11   softmax: a warpgroup a query tile, a row per thread; each row's terms are
 //          made by its thread, the next unit's while the last P V of this one runs
+// Units go out longest first, found by bisection over up to 32 chunks a lane each
+// (8 x 512 behind 0 to 4,096 tokens 131 us chunk by chunk, 114).  Where one query
+// tile a unit leaves SMs without one, the unit's keys go to the CTAs of a cluster,
+// and the parts are joined through its shared memory (16 rows behind 4,096: 54 us
+// in 8 CTAs, 19 in 64).
+//
+// What bounds it: a key tile for two query tiles of head_dim 128 is 2,048 cycles of
+// products, and its shared memory 2,440 (1,536 of operands, 650 of conversion,
+// scales and barriers, 256 of TMA), of about 3,000 that it takes; the rest is a
+// chain, S, softmax, P V, of which two run at a time.  8 chunks of 512 rows: 114 us, 72
+// % of the products' floor (over a 16-bit cache 160); 3 x 4,000 rows, window 4,096: 545
+// to 555 us, 74 % (641 to 684); 5 prompts of 2,000, head_dim 64, fp16: 100 us, 23
+// % (102), bound by the softmax and the issue of products that are half as long.
+// Measured and left (3 x 4,000 unless stated): a fourth warpgroup for V and the scales,
+// an issuer each for the query tiles, 632; scores' maximum not looked for in a
+// bf16 output's loop either, 580 to 595; two threads a row, both warpgroups on one
+// query tile, 555; a suspended wait, 568; P V from a third of P, as from half; P in
+// columns of its own (head_dim 64), S ahead of the softmax: the query tiles fall
+// into step, 524 for 456.  Without V's conversion, for timing, 2 x 2,048 rows take 160
+// us instead of 169.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -142,8 +162,8 @@ __device__ __forceinline__ uint32_t code_piece(int r, int c) {
     return D == 128 ? (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)) : (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
 }
 
-// WIDE: a 32-bit output.  TILES: query tiles of
-// a unit, 2, or 1 (A alone; the CTAs of a cluster share its keys)
+// WIDE: a 32-bit output.  TILES: query tiles of a unit, 2, or 1 (A alone; the CTAs
+// of a cluster share its keys)
 template <typename T, int D, bool WIDE, int TILES>
 __global__ void __launch_bounds__(kQpThreads, 1)
     quant_prefill_kernel(const QuantPrefillParams p, const __grid_constant__ CUtensorMap tk,
@@ -418,9 +438,9 @@ __global__ void __launch_bounds__(kQpThreads, 1)
             }
         } else if (warp == 1) {
             // ---------------- MMA issuer ----------------
-            // One thread, which is the tensor cores' bottleneck unless it is quick: it
-            // waits alone (a wait of the whole warp costs a vote and two meetings, and
-            // there are six a key tile).  The query tiles take turns: P V of a key tile
+            // One thread: it waits alone (a wait of the whole warp costs a vote and two
+            // meetings, there are six a key tile, and with them this loop, not the
+            // products, was what products of head_dim 64 waited for: 91 us for 81).  The query tiles take turns: P V of a key tile
             // and S of the next are one turn, so that a tile's softmax runs beside the
             // other's turn.
             if (tc::elect_one()) {
