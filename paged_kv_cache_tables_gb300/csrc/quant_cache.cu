@@ -37,18 +37,43 @@ struct QuantAppendParams {
     int T, num_blocks, Hkv, span;
 };
 
-// Largest of the finite magnitudes among eight 16-bit values, as bits.
 template <typename T>
-__device__ __forceinline__ uint32_t finite_max8(uint4 x) {
-    constexpr uint32_t inf = std::is_same<T, __nv_bfloat16>::value ? 0x7f80u : 0x7c00u;
+constexpr uint32_t kInfBits = std::is_same<T, __nv_bfloat16>::value ? 0x7f80u : 0x7c00u;
+
+// Largest magnitudes among pairs of 16-bit values so far, with eight more.
+__device__ __forceinline__ uint32_t max_pair(uint32_t top, uint4 x) {
+    return __vmaxu2(__vmaxu2(__vmaxu2(top, x.x & 0x7fff7fffu), __vmaxu2(x.y & 0x7fff7fffu, x.z & 0x7fff7fffu)), x.w & 0x7fff7fffu);
+}
+
+// The same of the finite ones only: four times the instructions, for rows that
+// turn out to hold others.
+template <typename T>
+__device__ __forceinline__ uint32_t finite_max_pair(uint32_t top, uint4 x) {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t lo = w[i] & 0x7fffu, hi = (w[i] >> 16) & 0x7fffu;
-        m = max(m, max(lo < inf ? lo : 0u, hi < inf ? hi : 0u));
+        uint32_t lo = w[i] & 0x7fffu, hi = (w[i] >> 16) & 0x7fffu;
+        lo = lo < kInfBits<T> ? lo : 0u;
+        hi = hi < kInfBits<T> ? hi : 0u;
+        top = __vmaxu2(top, lo | hi << 16);
     }
-    return m;
+    return top;
+}
+
+// The largest finite magnitude that the lanes of `group` hold in their N pieces, as bits.
+template <typename T, int N>
+__device__ __forceinline__ uint32_t group_max(uint32_t group, const uint4 (&x)[N]) {
+    uint32_t top = 0u;
+#pragma unroll
+    for (int e = 0; e < N; ++e) top = max_pair(top, x[e]);
+    top = __reduce_max_sync(group, max(top & 0xffffu, top >> 16));
+    if (top >= kInfBits<T>) {
+        top = 0u;
+#pragma unroll
+        for (int e = 0; e < N; ++e) top = finite_max_pair<T>(top, x[e]);
+        top = __reduce_max_sync(group, max(top & 0xffffu, top >> 16));
+    }
+    return top;
 }
 
 // Four codes times r, as codes.
@@ -62,8 +87,15 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t codes, float r) {
 // Eight values times f as codes.
 template <typename T>
 __device__ __forceinline__ uint2 codes8(uint4 x, float f) {
-    const float2 a = pair_to_f32<T>(x.x), b = pair_to_f32<T>(x.y), c = pair_to_f32<T>(x.z), d = pair_to_f32<T>(x.w);
-    return make_uint2(to_e4m3x4(a.x * f, a.y * f, b.x * f, b.y * f), to_e4m3x4(c.x * f, c.y * f, d.x * f, d.y * f));
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    const uint64_t f2 = f2_pack(f, f);
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 a = pair_to_f32<T>(w[i]);
+        f2_unpack(f2_mul(f2_pack(a.x, a.y), f2), v[2 * i], v[2 * i + 1]);
+    }
+    return make_uint2(to_e4m3x4(v[0], v[1], v[2], v[3]), to_e4m3x4(v[4], v[5], v[6], v[7]));
 }
 
 // The scale of a tile from that before (none where the block starts anew) and the
@@ -124,8 +156,8 @@ __global__ void __launch_bounds__(256, 4) kv_append_e4m3_kernel(const QuantAppen
             float2 *scales = reinterpret_cast<float2 *>(p.scales) + tile;
             const float2 was = *scales;
             const float2 old = off ? make_float2(was.x > 0.f ? was.x : 0.f, was.y > 0.f ? was.y : 0.f) : make_float2(0.f, 0.f);
-            const float2 now = make_float2(new_scale<T>(old.x, __reduce_max_sync(group, finite_max8<T>(xk))),
-                                           new_scale<T>(old.y, __reduce_max_sync(group, finite_max8<T>(xv))));
+            const uint4 ks[1] = {xk}, vs[1] = {xv};
+            const float2 now = make_float2(new_scale<T>(old.x, group_max<T>(group, ks)), new_scale<T>(old.y, group_max<T>(group, vs)));
             const float2 inv = make_float2(1.f / now.x, 1.f / now.y);
             uint8_t *ck = p.k_cache + tile * 16 * D, *cv = p.v_cache + tile * 16 * D;
             *reinterpret_cast<uint2 *>(ck + off * D + col * 8) = codes8<T>(xk, inv.x);
@@ -163,17 +195,14 @@ __global__ void __launch_bounds__(256, 4) kv_append_e4m3_kernel(const QuantAppen
             const int64_t stride = kv ? p.v_stride : p.k_stride;
             const T *rows = (kv ? v : k) + (t0 + i - 1) * stride + h * D;
             uint4 x[16 / ROWS];
-            uint32_t top = 0;
 #pragma unroll
             for (int e = 0; e < 16 / ROWS; ++e) {
                 const int r = e * ROWS + sub;
                 x[e] = r < n ? __ldg(reinterpret_cast<const uint4 *>(rows + r * stride) + col) : make_uint4(0u, 0u, 0u, 0u);
             }
-#pragma unroll
-            for (int e = 0; e < 16 / ROWS; ++e) top = max(top, finite_max8<T>(x[e]));
             const bool anew = written & 1u;
             const float old = !anew && was > 0.f ? was : 0.f;
-            const float now = new_scale<T>(old, __reduce_max_sync(0xffffffffu, top));
+            const float now = new_scale<T>(old, group_max<T>(0xffffffffu, x));
             const float inv = 1.f / now;
             uint8_t *out = (kv ? p.v_cache : p.k_cache) + tile * 16 * D;
 #pragma unroll

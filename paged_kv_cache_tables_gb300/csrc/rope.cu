@@ -92,12 +92,6 @@ __device__ __forceinline__ uint4 pack8(const uint64_t (&f)[4]) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-
 template <typename T>
 __device__ __forceinline__ void load_weight8(const void *w, int f32, int at, uint64_t (&f)[4]) {
     if (f32) {
