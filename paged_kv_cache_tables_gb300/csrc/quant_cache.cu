@@ -9,9 +9,9 @@
 // scale(a) the least power of two with a <= 448 scale(a).
 //
 // What bounds them: HBM, and for few rows the chain slot, row and scale, maximum,
-// store.  Append of 256 decodes (8 heads of 128, bf16) 2.4 us, 4,327 mixed rows 8.9
-// us (44 % of the measured copy rate), a prompt of 16,383 rows (16 heads of 64,
-// fp16) 21.8 us (68 %); with a warp for every (token, head, K or V), most of which
+// store.  Append of 256 decodes (8 heads of 128, bf16) 2.4 us, 4,327 mixed rows 7.6
+// us (52 % of the measured copy rate), a prompt of 16,383 rows (16 heads of 64,
+// fp16) 20 us (74 %; 8 heads of 128 18.7, 80 %); with a warp for every (token, head, K or V), most of which
 // found another one to do their work, 4.9, 16 and 78 us.  Read back: 64 sequences
 // of up to 8,000 tokens (742 MB) 114 us, 96 %; 32-bit rows 190 us, 96 %; 777 rows 4.5
 // us.  With 16 codes and 32 bytes of output a thread, halves of whose sectors were
@@ -363,10 +363,13 @@ extern "C" int pkv_kv_append_e4m3(const void *k, int64_t k_stride, const void *v
         !aligned(kv_scales, 8) || k_stride < 0 || v_stride < 0 || k_stride % 8 != 0 || v_stride % 8 != 0)
         return PKV_ERR_INVALID_ARG;
     // Tokens a CTA, and CTAs that share them: few where the rows are few (256 decodes
-    // 2.4 us in spans of 8 shared by four CTAs, 4.9 of 16 by two; one chunk of 512 4.2
-    // and 3.1), else 16 by two (a prompt of 16,383 rows 21.8 us, 27.5 in spans of 8 by
-    // four; 4,327 mixed rows 8.9 and 8.9).
-    const int span = num_tokens <= 1024 ? 8 : 16, slices = num_tokens <= 1024 ? 4 : 2;
+    // 2.4 us in spans of 8 shared by four CTAs, 4.9 of 16 by two; one chunk of 512 3.4
+    // and 3.1), else 16, by as many as leave a warp 8 KB of a block's rows (a prompt of
+    // 16,383 rows, 16 heads of 64, 20 us in spans of 16 by two, 27.5 in spans of 8 by
+    // four; 6,000 rows of 32 heads of 128 25.1 us by eight, 30.7 by two; 16,383 of one
+    // head 5.2 by one, 6.0 by two).
+    const int span = num_tokens <= 1024 ? 8 : 16;
+    const int slices = num_tokens <= 1024 ? 4 : std::max(1, std::min(8, num_kv_heads * head_dim / 512));
     const QuantAppendParams prm = {k, v, k_stride, v_stride, slot_mapping, static_cast<uint8_t *>(k_cache),
                                    static_cast<uint8_t *>(v_cache), kv_scales, dev_status, num_tokens, num_blocks,
                                    num_kv_heads, span};
