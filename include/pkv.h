@@ -450,7 +450,8 @@ int pkv_paged_window_prefill_attention(void *out, const void *q, const int32_t *
  *     s' = r(a) where the call writes offset 0 of the block (the block starts
  *     anew: what it held is gone), else max(s, r(a));
  * each row is stored as the codes next to x / s' (ties to even; infinities as
- * +-448, NaN as NaN), and where s' > s the block's other rows as those next to
+ * +-448, NaN as NaN; x times 1 / s' where an s that was there is no power of
+ * two), and where s' > s the block's other rows as those next to
  * their code times s / s' (exact, short of e4m3's subnormals).  A scale s that is
  * not above 0 counts as 0.
  * The rows of one block must stand next to one another in the call, as the
@@ -485,7 +486,8 @@ int pkv_kv_gather_e4m3(void *k, void *v, const void *k_cache, const void *v_cach
 /*
  * pkv_paged_decode_attention_e4m3 -- pkv_paged_window_decode_attention over a
  * cache held in 8 bits; a window of at least max_blocks_per_seq * block_size is
- * the whole context.  Arguments, limits and guarantees as there.  kv_scales of
+ * the whole context.  Arguments, limits and guarantees as there; num_q_heads <=
+ * 65,536 (PKV_ERR_UNSUPPORTED).  kv_scales of
  * blocks that are read must be positive and finite (any such value will do, not
  * just powers of two).  A block id outside the pool reads zeros.
  */
@@ -498,7 +500,9 @@ int pkv_paged_decode_attention_e4m3(void *out, const void *q, const void *k_cach
 /*
  * pkv_paged_prefill_attention_e4m3 -- pkv_paged_window_prefill_attention over a
  * cache held in 8 bits, with the window and kv_scales of
- * pkv_paged_decode_attention_e4m3.
+ * pkv_paged_decode_attention_e4m3, and its limit.  Scores times log2 e, plus the
+ * log2 of V's scale, are to stay below 2^22 in magnitude: of larger ones fp32
+ * holds too few bits behind the point for weights relative to a maximum.
  */
 int pkv_paged_prefill_attention_e4m3(void *out, const void *q, const int32_t *cu_seqlens, int num_seqs, int max_q_len,
                                      int total_q, const void *k_cache, const void *v_cache, const float *kv_scales,

@@ -88,6 +88,7 @@ inline int quant_attention_refusal(int num_seqs, int num_blocks, int num_q_heads
         num_sinks < 0)
         return PKV_ERR_INVALID_ARG;
     if (num_q_heads % num_kv_heads != 0) return PKV_ERR_INVALID_ARG;
+    if (num_q_heads > 1 << 16) return PKV_ERR_UNSUPPORTED;   // (offsets in a unit's rows of queries are 32-bit)
     if (num_q_heads / num_kv_heads > 16 || block_size != 16 || (head_dim != 64 && head_dim != 128)) return PKV_ERR_UNSUPPORTED;
     if (dtype != PKV_DTYPE_F16 && dtype != PKV_DTYPE_BF16) return PKV_ERR_UNSUPPORTED;
     if (out_dtype != dtype && out_dtype != PKV_DTYPE_F32) return PKV_ERR_UNSUPPORTED;

@@ -78,7 +78,7 @@ PREFILL = dict(out=FAKE, q=FAKE, cu=FAKE, num_seqs=1, max_q=16, total_q=16, k_ca
 ATTENTION = [
     (dict(window=0), INVALID), (dict(window=-1), INVALID), (dict(sinks=-1), INVALID), (dict(scale=0.0), INVALID),
     (dict(scale=-1.0), INVALID), (dict(scale=math.nan), INVALID), (dict(scale=math.inf), INVALID), (dict(hq=6, hkv=4), INVALID),
-    (dict(hq=34, hkv=2), UNSUPPORTED), (dict(d=96), UNSUPPORTED), (dict(bs=32), UNSUPPORTED), (dict(dtype=2), UNSUPPORTED),
+    (dict(hq=34, hkv=2), UNSUPPORTED), (dict(hq=(1 << 16) + 16, hkv=(1 << 12) + 1), UNSUPPORTED), (dict(d=96), UNSUPPORTED), (dict(bs=32), UNSUPPORTED), (dict(dtype=2), UNSUPPORTED),
     (dict(out_dtype=0), UNSUPPORTED), (dict(num_blocks=0), INVALID), (dict(hkv=0), INVALID), (dict(max_blocks=0), INVALID),
     (dict(num_seqs=-1), INVALID), (dict(num_blocks=1 << 27), UNSUPPORTED), (dict(max_blocks=(1 << 26) + 1), UNSUPPORTED),
     (dict(out=None), INVALID), (dict(q=None), INVALID), (dict(k_cache=None), INVALID), (dict(v_cache=None), INVALID),
