@@ -82,7 +82,10 @@ struct QuantDecodeParams {
 // where what counts is how many are under way.  us, PAIRS / not (with TMA): 256
 // sequences x 8 of 32 to 8,192 tokens 127 / 144, 40 x 8 of 2,048 30.6 / 35.4; 1,000
 // x 8 of 100 to 600 117 / 108, 256 x 8 of 30 to 130 22.5 / 19.0, 64 x 8 of 1,000 (512
-// CTAs: one wave of four an SM, or two of three) 31.5 / 25.3.  More heads (NT ==
+// CTAs: one wave of four an SM, or two of three) 31.5 / 25.3.  With heads of 64 pairs
+// leave registers for four CTAs, and are for split ranges too (64 x 8 of 64 to 4,096
+// 21.6 / 23.3, 128 x 8 of 2,000 48 / 52 in three CTAs; with heads of 128 split ranges
+// take longer, 16 x 8 of 8,000 57 / 47).  More heads (NT ==
 // 2, up to 8, larger groups in parts) have one form: their accumulators leave
 // registers for one block a step and three CTAs (two, with pairs: 81 us for 79).
 template <int D, int NT, bool PAIRS>
@@ -91,7 +94,7 @@ struct QuantShape {
     static constexpr int BLOCK_BYTES = 2 * TILE_BYTES;  // K then V
     static constexpr int STEP = PAIRS ? 2 : 1;          // blocks a warp takes at a time: a slot of its ring
     static constexpr int SLOT_BYTES = STEP * BLOCK_BYTES;
-    static constexpr int PER_SM = PAIRS || NT > 1 ? 3 : 4;
+    static constexpr int PER_SM = (PAIRS && D == 128) || NT > 1 ? 3 : 4;
     static constexpr int SLOTS = (PER_SM == 3 ? 16 : 12) * 1024 / SLOT_BYTES;
     static constexpr int RING_BYTES = kQdWarps * SLOTS * SLOT_BYTES;
     // behind the ring: scales of 32 blocks a warp, then (m, l) of each warp and of the CTA
@@ -663,7 +666,7 @@ static int quant_decode(QuantDecodeParams &prm, int64_t blocks, int sms, cudaStr
     // blocks a CTA, while there are fewer than 12 CTAs an SM then: its length may
     // be far above the others', and an SM takes 2 MB no faster than in 45 us (24 x 8
     // of 500 to 30,000 tokens 73 us in 8 CTAs a range, 158 in one; 64 x 8 of 64 to
-    // 4,096 23 and 27; 16 x 8 of 8,000 45 and 52).  More CTAs than that cost more
+    // 4,096, heads of 64, 23 and 27; 16 x 8 of 8,000 45 and 52).  More CTAs than that cost more
     // than they even out (256 x 8 of 1,400: 132 us in two a range for 112).
     const int ranks = std::max(power_below(std::min<int64_t>(sms / ranges, blocks / kQdWarps)),
                                power_below(std::min<int64_t>(12 * sms / ranges, blocks / 96)));
@@ -673,7 +676,8 @@ static int quant_decode(QuantDecodeParams &prm, int64_t blocks, int sms, cudaStr
     // 1,400 each 112 and 116).
     prm.ordered = ctas > 3 * sms && blocks > ctas / 13 && prm.num_seqs <= kQdMaxOrdered;
     if (prm.G > 4) return launch_quant_decode<T, D, 2, false>(prm, (int)ctas, ranks, stream);
-    const bool pairs = ranks == 1 && blocks > 48 && !(blocks <= 128 && ctas <= 4 * sms && ctas > 3 * sms);
+    const bool pairs = D == 64 ? blocks > 48 * ranks
+                               : ranks == 1 && blocks > 48 && !(blocks <= 128 && ctas <= 4 * sms && ctas > 3 * sms);
     if (pairs) return launch_quant_decode<T, D, 1, true>(prm, (int)ctas, ranks, stream);
     return launch_quant_decode<T, D, 1, false>(prm, (int)ctas, ranks, stream);
 }
