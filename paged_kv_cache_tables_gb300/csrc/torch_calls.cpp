@@ -22,6 +22,15 @@
 
 #include "pkv.h"
 
+// The 8-bit cache's entry points may be missing from the libpkv.so that the module
+// is loaded with: the others' calls work all the same.
+extern "C" {
+extern decltype(pkv_kv_append_e4m3) pkv_kv_append_e4m3 __attribute__((weak));
+extern decltype(pkv_kv_gather_e4m3) pkv_kv_gather_e4m3 __attribute__((weak));
+extern decltype(pkv_paged_decode_attention_e4m3) pkv_paged_decode_attention_e4m3 __attribute__((weak));
+extern decltype(pkv_paged_prefill_attention_e4m3) pkv_paged_prefill_attention_e4m3 __attribute__((weak));
+}
+
 namespace {
 
 // A Python exception on its way to the interpreter.
@@ -265,6 +274,11 @@ PyObject *window_prefill(PyObject *, Args a, Py_ssize_t n) {
 
 constexpr at::ScalarType kCode = at::kFloat8_e4m3fn;
 
+template <typename F>
+void needs(F *entry, const char *name) {
+    if (!entry) refuse(PyExc_RuntimeError, std::string("libpkv.so has no ") + name + ": rebuild it");
+}
+
 float *scales_arg(PyObject *o, int64_t NB, int64_t Hkv, int device) {
     return static_cast<float *>(ptr(o, "kv_scales", at::kFloat, {NB, Hkv, 2}, device));
 }
@@ -272,6 +286,7 @@ float *scales_arg(PyObject *o, int64_t NB, int64_t Hkv, int device) {
 // (out, q, k_cache, v_cache, kv_scales, block_tables, context_lens, window, num_sinks, scale, dev_status, stream)
 PyObject *decode_e4m3(PyObject *, Args a, Py_ssize_t n) {
     return guarded("decode_e4m3", n, 12, [&] {
+        needs(&pkv_paged_decode_attention_e4m3, "pkv_paged_decode_attention_e4m3");
         const Attention t(a[0], a[1], a[2], a[3], kCode);
         const float *scales = scales_arg(a[4], t.NB, t.Hkv, t.device);
         const int64_t S = t.q_shape[0], MB = dims(tensor(a[5], "block_tables"), "block_tables", 2)[1];
@@ -295,6 +310,7 @@ PyObject *decode_e4m3(PyObject *, Args a, Py_ssize_t n) {
 //  dev_status, stream)
 PyObject *prefill_e4m3(PyObject *, Args a, Py_ssize_t n) {
     return guarded("prefill_e4m3", n, 14, [&] {
+        needs(&pkv_paged_prefill_attention_e4m3, "pkv_paged_prefill_attention_e4m3");
         const Attention t(a[0], a[1], a[4], a[5], kCode);
         const float *scales = scales_arg(a[6], t.NB, t.Hkv, t.device);
         const auto tb = dims(tensor(a[7], "block_tables"), "block_tables", 2);
@@ -320,6 +336,7 @@ PyObject *prefill_e4m3(PyObject *, Args a, Py_ssize_t n) {
 // (k, v, slot_mapping, k_cache, v_cache, kv_scales, dev_status, stream)
 PyObject *append_e4m3(PyObject *, Args a, Py_ssize_t n) {
     return guarded("append_e4m3", n, 8, [&] {
+        needs(&pkv_kv_append_e4m3, "pkv_kv_append_e4m3");
         const at::Tensor &tk = tensor(a[0], "k");
         const int dev = device_of(tk, "k");
         const auto ks = dims(tk, "k", 3);
@@ -346,6 +363,7 @@ PyObject *append_e4m3(PyObject *, Args a, Py_ssize_t n) {
 // (k, v, k_cache, v_cache, kv_scales, block_tables, cu_seqlens, first, dev_status, stream)
 PyObject *gather_e4m3(PyObject *, Args a, Py_ssize_t n) {
     return guarded("gather_e4m3", n, 10, [&] {
+        needs(&pkv_kv_gather_e4m3, "pkv_kv_gather_e4m3");
         const at::Tensor &tk = tensor(a[0], "k");
         const int dev = device_of(tk, "k");
         const auto ks = dims(tk, "k", 3);

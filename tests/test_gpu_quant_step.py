@@ -6,12 +6,17 @@ memory and in again.  And the calls that a loop makes around that: two at once o
 two streams, caches past 4 GB, batches padded to a capacity.  Codes and scales are
 held to the definition exactly, outputs to it within the derived bounds."""
 import math
+import os
+import shutil
+import subprocess
+import sys
 
 import pytest
 import torch
 
 import quant_ref as qr
 import window_ref as ref
+from paged_kv_cache_tables_gb300 import _binding as B
 from paged_kv_cache_tables_gb300 import (copy_blocks, kv_append_e4m3, kv_gather_e4m3, paged_decode_attention_e4m3,
                                          paged_prefill_attention_e4m3, qk_rope, release_blocks, rope_frequencies,
                                          step_tables)
@@ -345,3 +350,63 @@ def test_queries_that_are_not_finite_stay_apart(cuda_lib, d, dtype, out_dtype):
         assert got.cpu()[bad].isnan().any(-1).all()
         ref.assert_within(got.cpu()[~bad], want[~bad], bound[~bad])
         assert st.status.item() == 0
+
+
+# ---- the calls from Python ------------------------------------------------------------------------------------------
+OLDER = """
+#include <stddef.h>
+int PyGILState_Check(void);
+#define HELD(name) int name(void) { return PyGILState_Check(); }
+HELD(pkv_paged_window_decode_attention)
+HELD(pkv_paged_window_prefill_attention)
+HELD(pkv_qk_rope)
+HELD(pkv_qk_rope_append)
+HELD(pkv_step_tables)
+HELD(pkv_release_blocks)
+size_t pkv_release_workspace_size(int n) { return 4 * (size_t)n; }
+"""
+
+WHOLE_LIBRARY = OLDER + """
+HELD(pkv_kv_append_e4m3)
+HELD(pkv_kv_gather_e4m3)
+HELD(pkv_paged_decode_attention_e4m3)
+HELD(pkv_paged_prefill_attention_e4m3)
+"""
+
+CALLS = """
+import importlib.util, sys, torch
+spec = importlib.util.spec_from_file_location("_torch_calls", sys.argv[1])
+m = importlib.util.module_from_spec(spec)
+spec.loader.exec_module(m)
+x = torch.zeros(2, 2, 64, dtype=torch.float16, device="cuda")
+c = torch.zeros(4, 2, 16, 64, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+k = torch.zeros(4, 2, 2, device="cuda")
+i = torch.zeros(2, dtype=torch.int32, device="cuda")
+t = torch.zeros(2, 4, dtype=torch.int32, device="cuda")
+cu = torch.zeros(3, dtype=torch.int32, device="cuda")
+calls = [lambda: m.append_e4m3(x, x, i.long(), c, c, k, None, None),
+         lambda: m.gather_e4m3(x, x, c, c, k, t, cu, None, None, None),
+         lambda: m.decode_e4m3(x, x, c, c, k, t, i, 16, 0, None, None, None),
+         lambda: m.prefill_e4m3(x, x, cu, 1, c, c, k, t, i, 16, 0, None, None, None)]
+def outcome(f):
+    try:
+        return f()
+    except RuntimeError as e:
+        assert "rebuild" in str(e), e
+        return "missing"
+print([outcome(f) for f in calls])
+"""
+
+
+@pytest.mark.parametrize("library,want", [(WHOLE_LIBRARY, [0] * 4), (OLDER, ["missing"] * 4)], ids=["whole", "older"])
+def test_python_calls_against_other_libraries(cuda_lib, tmp_path, library, want):
+    """The interpreter is free while an entry point runs (it returns whether it is held); a library that has none of the
+    four is named, and serves the module's other calls."""
+    (tmp_path / "fake.c").write_text(library)
+    subprocess.run(["gcc", "-shared", "-fPIC", "-o", str(tmp_path / "libpkv.so"), str(tmp_path / "fake.c")], check=True)
+    shutil.copy(B.CALLS_PATH, tmp_path / "_torch_calls.so")
+    (tmp_path / "calls.py").write_text(CALLS)
+    res = subprocess.run([sys.executable, "calls.py", str(tmp_path / "_torch_calls.so")], cwd=tmp_path, capture_output=True,
+                         text=True, timeout=300, env=dict(os.environ, PYTHONPATH=""))
+    assert res.returncode == 0, res.stderr
+    assert res.stdout.strip() == str(want)
