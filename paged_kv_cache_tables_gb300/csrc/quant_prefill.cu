@@ -35,7 +35,7 @@
 //   4-11   softmax: a warpgroup a query tile, a row per thread; each row's terms are
 //          made by its thread, the next unit's while the last P V of this one runs
 // Units go out longest first, found by bisection over up to 32 chunks a lane each
-// (8 x 512 behind 0 to 4,096 tokens 131 us chunk by chunk, 114).  Where one query
+// (8 x 512 behind 0 to 4,096 tokens 131 us chunk by chunk, 114 so).  Where one query
 // tile a unit leaves SMs without one, the unit's keys go to the CTAs of a cluster,
 // and the parts are joined through its shared memory (16 rows behind 4,096: 54 us
 // in 8 CTAs, 19 in 64).
@@ -43,9 +43,9 @@
 // What bounds it: a key tile for two query tiles of head_dim 128 is 2,048 cycles of
 // products, and its shared memory 2,440 (1,536 of operands, 650 of conversion,
 // scales and barriers, 256 of TMA), of about 3,000 that it takes; the rest is a
-// chain, S, softmax, P V, of which two run at a time.  8 chunks of 512 rows: 114 us, 72
-// % of the products' floor (over a 16-bit cache 160); 3 x 4,000 rows, window 4,096: 545
-// to 555 us, 74 % (641 to 684); 5 prompts of 2,000, head_dim 64, fp16: 100 us, 23
+// chain, S, softmax, P V, of which two run at a time.  8 chunks of 512 rows: 111 us, 74
+// % of the products' floor (over a 16-bit cache 160); 3 x 4,000 rows, window 4,096: 526
+// to 535 us, 77 % (641 to 684); 5 prompts of 2,000, head_dim 64, fp16: 100 us, 23
 // % (102), bound by the softmax and the issue of products that are half as long.
 // Measured and left (3 x 4,000 unless stated): a fourth warpgroup for V and the scales,
 // an issuer each for the query tiles, 632; scores' maximum not looked for in a
@@ -363,6 +363,17 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                     if (lane == 0) {
                         units[n & 1] = u;
                         tc::mbar_arrive_cta(&bars->unit_full[n & 1]);
+                    }
+                    // its query rows on their way to L2: they are read when the unit before is
+                    // done (3 x 4,000 rows 551 us without, 530; 8 x 512 114 and 111; fp16 of
+                    // head_dim 64, whose units are long, 100 without and 102)
+                    if constexpr (!(RES && D == 64)) {
+                        const int lines = p.G * (D / 64);   // of 128 bytes, of a token
+                        const uint8_t *rows = static_cast<const uint8_t *>(p.q) + ((int64_t)u.row0 * p.Hq + (int64_t)h * p.G) * (D * 2);
+                        for (int i = lane; i < u.tokens * lines; i += 32) {
+                            const int tk = i / lines;
+                            asm volatile("prefetch.global.L2 [%0];" ::"l"(rows + (int64_t)tk * p.Hq * (D * 2) + (i - tk * lines) * 128));
+                        }
                     }
                     // lane i < 8 reads the block id of page i of the tile, one tile ahead
                     int blk_next = lane < kQpPages ? page_id(u, tile0(u) * kQpPages + lane) : -1;
