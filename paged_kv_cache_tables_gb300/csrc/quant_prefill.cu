@@ -43,7 +43,7 @@
 // What bounds it: a key tile for two query tiles of head_dim 128 is 2,048 cycles of
 // products, and its shared memory 2,440 (1,536 of operands, 650 of conversion,
 // scales and barriers, 256 of TMA), of about 3,000 that it takes; the rest is a
-// chain, S, softmax, P V, of which two run at a time.  8 chunks of 512 rows: 111 us, 74
+// chain, S, softmax, P V, of which two run at a time.  8 chunks of 512 rows: 108 us, 75
 // % of the products' floor (over a 16-bit cache 160); 3 x 4,000 rows, window 4,096: 526
 // to 535 us, 77 % (641 to 684); 5 prompts of 2,000, head_dim 64, fp16: 100 us, 23
 // % (102), bound by the softmax and the issue of products that are half as long.
@@ -608,52 +608,55 @@ __global__ void __launch_bounds__(kQpThreads, 1)
             }
             float scale = 0.f;
             // (a loop, and the rows moved up in it: unrolled, this code, which runs once a
-            // unit, takes longer to come from memory than to run)
+            // unit, takes longer to come from memory than to run.  8 x 512 rows 134 us
+            // unrolled, 111 two rows at a time, 108.5 four; where a CTA has one unit, 1 x 512
+            // 60 two at a time, 66 four)
+            constexpr int PER = TILES == 2 ? 4 : 2;
 #pragma unroll 1
-            for (int i0 = 0; i0 < N; i0 += 2) {
+            for (int i0 = 0; i0 < N; i0 += PER) {
 #pragma unroll
-              for (int i2 = 0; i2 < 2; ++i2) {
-                const int i = i0 + i2;
-                const uint32_t w[4] = {x[i2].x, x[i2].y, x[i2].z, x[i2].w};
-                const uint32_t top2 = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
-                                               __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
-                uint32_t top = max(top2 & 0xffffu, top2 >> 16);
+                for (int i2 = 0; i2 < PER; ++i2) {
+                    const int i = i0 + i2;
+                    const uint32_t w[4] = {x[i2].x, x[i2].y, x[i2].z, x[i2].w};
+                    const uint32_t top2 = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
+                                                   __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+                    uint32_t top = max(top2 & 0xffffu, top2 >> 16);
 #pragma unroll
-                for (int m = 1; m < LANES; m *= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, m));
-                const bool finite = top < (std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u);
-                const float s = block_scale(finite ? pair_to_f32<T>(top).x : 0.f, -126);
-                const float inv = __uint_as_float((254u << 23) - __float_as_uint(s));   // (s is a power of two)
-                // (a query that is not finite has no finite output)
-                const float mine = __shfl_sync(0xffffffffu, finite ? s : __uint_as_float(0x7fffffffu), (lane % ROWS) * LANES);
-                if (lane / ROWS == i) scale = mine;
-                float v[8];
+                    for (int m = 1; m < LANES; m *= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, m));
+                    const bool finite = top < (std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u);
+                    const float s = block_scale(finite ? pair_to_f32<T>(top).x : 0.f, -126);
+                    const float inv = __uint_as_float((254u << 23) - __float_as_uint(s));   // (s is a power of two)
+                    // (a query that is not finite has no finite output)
+                    const float mine = __shfl_sync(0xffffffffu, finite ? s : __uint_as_float(0x7fffffffu), (lane % ROWS) * LANES);
+                    if (lane / ROWS == i) scale = mine;
+                    float v[8];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 f = pair_to_f32<T>(w[e]);
-                    v[2 * e] = f.x * inv;
-                    v[2 * e + 1] = f.y * inv;
-                }
-                const int rr = lane_base + i * ROWS + sub;
-                const uint32_t at = to + code_piece<D>(rr, piece >> 1) + (piece & 1) * 8;
-#pragma unroll
-                for (int term = 0; term < Sh::TERMS; ++term) {
-                    uint32_t c[2];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        c[e] = to_e4m3x4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
-                        uint32_t lo, hi;
-                        e4m3x4_to_f16x4(c[e], lo, hi);
-                        const float2 fl = f16x2_to_f32(lo), fh = f16x2_to_f32(hi);
-                        v[4 * e] -= fl.x;
-                        v[4 * e + 1] -= fl.y;
-                        v[4 * e + 2] -= fh.x;
-                        v[4 * e + 3] -= fh.y;
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 f = pair_to_f32<T>(w[e]);
+                        v[2 * e] = f.x * inv;
+                        v[2 * e + 1] = f.y * inv;
                     }
-                    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + term * Sh::Q_TERM), "r"(c[0]), "r"(c[1]) : "memory");
-                }
-              }
+                    const int rr = lane_base + i * ROWS + sub;
+                    const uint32_t at = to + code_piece<D>(rr, piece >> 1) + (piece & 1) * 8;
 #pragma unroll
-              for (int k = 2; k < N; ++k) x[k - 2] = x[k];
+                    for (int term = 0; term < Sh::TERMS; ++term) {
+                        uint32_t c[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            c[e] = to_e4m3x4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                            uint32_t lo, hi;
+                            e4m3x4_to_f16x4(c[e], lo, hi);
+                            const float2 fl = f16x2_to_f32(lo), fh = f16x2_to_f32(hi);
+                            v[4 * e] -= fl.x;
+                            v[4 * e + 1] -= fl.y;
+                            v[4 * e + 2] -= fh.x;
+                            v[4 * e + 3] -= fh.y;
+                        }
+                        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + term * Sh::Q_TERM), "r"(c[0]), "r"(c[1]) : "memory");
+                    }
+                }
+#pragma unroll
+                for (int k = PER; k < N; ++k) x[k - PER] = x[k];
             }
             fence_proxy_async_smem();
             __syncwarp();
