@@ -56,6 +56,7 @@
 // us instead of 169.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdio>
 #include <type_traits>
@@ -1113,10 +1114,11 @@ extern "C" int pkv_paged_prefill_attention_e4m3(void *out, const void *q, const 
     const int rtok = kQpRows / G;
     // query tiles of a unit: two, which share every K and V tile; or one, when
     // all units then run at once and a step of 128 keys has one tile's products
-    auto units_of = [&](int tiles) { return ((int64_t)max_q_len + tiles * rtok - 1) / (tiles * rtok); };
+    const int most_q = std::min(max_q_len, total_q);   // rows that a chunk can have
+    auto units_of = [&](int tiles) { return ((int64_t)most_q + tiles * rtok - 1) / (tiles * rtok); };
     const bool one = num_seqs * units_of(1) * num_kv_heads <= sms;
     const int qtiles = one ? 1 : 2;
-    const int64_t grid = (int64_t)num_seqs * units_of(qtiles) * num_kv_heads;
+    int64_t grid = (int64_t)num_seqs * units_of(qtiles) * num_kv_heads;
     if (grid >= (int64_t)1 << 31) return PKV_ERR_UNSUPPORTED;
     // where most SMs would have none, a unit's keys go to the CTAs of a cluster,
     // two key tiles each or more if contexts fill their tables
@@ -1155,6 +1157,9 @@ extern "C" int pkv_paged_prefill_attention_e4m3(void *out, const void *q, const 
     prm.num_seqs = num_seqs;
     prm.units_per_seq = (int)units_of(qtiles);
     prm.sorted = num_seqs <= 32 && grid > sms;
+    // sorted units leave no place empty between them: as many places as total_q rows
+    // in num_seqs chunks can make units
+    if (prm.sorted) grid = std::min(grid, ((int64_t)total_q / (qtiles * rtok) + num_seqs) * num_kv_heads);
     prm.window = window < capacity ? window : (int)capacity;   // no context is longer
     prm.sinks = num_sinks < capacity ? num_sinks : (int)capacity;
     prm.total_q = total_q;

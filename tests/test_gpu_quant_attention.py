@@ -113,7 +113,7 @@ def test_prefill_of_few_rows(cuda_lib, ctx, qn, window, sinks, Hq, Hkv, d, dtype
     assert st.status.item() == 0 and torch.equal(got, st.prefill(out_dtype))
 
 
-@pytest.mark.parametrize("chunks,extra", [(3, 0), (32, 300), (33, 0), (60, 77)])
+@pytest.mark.parametrize("chunks,extra", [(3, 0), (32, 300), (33, 0), (60, 77), (5, 2 ** 31 - 1 - 194)])
 @pytest.mark.parametrize("Hq,Hkv,d,out_dtype", [(16, 16, 64, BF16), (30, 10, 128, F32)])
 def test_prefill_takes_every_unit_once(cuda_lib, chunks, extra, Hq, Hkv, d, out_dtype):
     """Chunks of no row, of one and of many, behind contexts of their own, with a max_q_len that none reaches; some that
