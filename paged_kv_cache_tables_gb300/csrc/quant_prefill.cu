@@ -452,9 +452,9 @@ __global__ void __launch_bounds__(kQpThreads, 1)
             // ---------------- MMA issuer ----------------
             // One thread: it waits alone (a wait of the whole warp costs a vote and two
             // meetings, there are six a key tile, and with them this loop, not the
-            // products, was what products of head_dim 64 waited for: 91 us for 81).  The query tiles take turns: P V of a key tile
-            // and S of the next are one turn, so that a tile's softmax runs beside the
-            // other's turn.
+            // products, was what products of head_dim 64 waited for: 91 us for 81, 5
+            // prompts of 2,000).  The query tiles take turns: P V of a key tile and S of
+            // the next are one turn, so that a tile's softmax runs beside the other's turn.
             if (tc::elect_one()) {
                 constexpr uint32_t idesc_s = tc::idesc_e4m3(kQpRows, kQpKeys);
                 constexpr uint32_t idesc_o = tc::idesc_f16(false, false, true, kQpRows, D);
