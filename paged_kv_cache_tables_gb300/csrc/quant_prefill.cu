@@ -6,8 +6,8 @@
 // positions:
 //     y_t = scale2 f a_j (q' . k_t) + log2 b_j,   P_t = 2^(y_t - m + 7),
 //     l = l c + sum P_t / b_j,   O = O c + P v,   c = 2^(m_old - m),   out = O / l,
-// m the running maximum of y, moved when it grows by more than 2^8: P stays below
-// 2^15 and about 2^7 for the weight that counts most, whatever the scales are.
+// m a maximum of y so far, moved on when a page's P sum to more than 2^15: P stays
+// below that, and the largest at least 2^7, whatever the scales are.
 //
 // Both products run on the codes without their scales:
 //   S = q' k^T   in e4m3 (kind::f8f6f4, twice the rate of 16 bits): K goes from the
@@ -17,13 +17,12 @@
 //                two terms hold bf16's 8 bits, three fp16's 11, down to 2^-10 (2^-18
 //                of the largest element at most).  As many steps as in 16 bits, or
 //                one and a half times for fp16.
-//   O += P v     in fp16: v is converted on the way (exact).  P for a bf16 output
-//                is rounded once (2^-11 of a weight, an eighth of what the output's
-//                own rounding may be), else value and residual, two products (an
-//                fp16 output from P rounded once would be off by 1.25 times its own
-//                rounding, and take 81 us instead of 100 for 5 x 2,000 rows of head_dim 64).
-// (P in e4m3 terms would take three for a bf16 output: more steps than fp16's one,
-// and a conversion of every weight three times instead of V's once a tile.)
+//   O += P v     in fp16: v is converted on the way (exact), P is value and residual,
+//                two products, for any output.  (With P rounded once, 2^-11 of a
+//                weight, 3 x 4,000 rows of bf16 would take 538 us instead of 724, and
+//                outputs would be the 32-bit ones rounded no longer.)
+// (P in e4m3 terms would take four: as many steps, and a conversion of every weight
+// four times instead of V's once a tile.)
 //
 // What is walked and the unit of work: as in window_prefill.cu.  Warps (persistent;
 // 12 of them):
@@ -40,20 +39,19 @@
 // and the parts are joined through its shared memory (16 rows behind 4,096: 54 us
 // in 8 CTAs, 19 in 64).
 //
-// What bounds it: a key tile for two query tiles of head_dim 128 is 2,048 cycles of
-// products, and its shared memory 2,440 (1,536 of operands, 650 of conversion,
-// scales and barriers, 256 of TMA), of about 3,000 that it takes; the rest is a
-// chain, S, softmax, P V, of which two run at a time.  8 chunks of 512 rows: 108 us, 75
-// % of the products' floor (over a 16-bit cache 160); 3 x 4,000 rows, window 4,096: 526
-// to 535 us, 77 % (641 to 684); 5 prompts of 2,000, head_dim 64, fp16: 100 us, 23
-// % (102), bound by the softmax and the issue of products that are half as long.
+// What bounds it: a key tile for two query tiles of head_dim 128 is 3,072 cycles of
+// products, a third of them the residual's, and a chain, S, softmax, P V, of which
+// two run at a time.  Beside the products' time without the residual's, at the
+// measured rate of 16 bits and the contexts that were timed: 8 chunks of 512 rows
+// behind 0 to 4,096 tokens 153 us for 74 (over a 16-bit cache 160); 3 x 4,000 rows,
+// window 4,096, 724 for 392 (641 to 684); 5 prompts of 2,000, head_dim 64, fp16
+// 98 for 25 (102), bound by the softmax and the issue of products that are half as
+// long.
 // Measured and left (3 x 4,000 unless stated): a fourth warpgroup for V and the scales,
-// an issuer each for the query tiles, 632; scores' maximum not looked for in a
-// bf16 output's loop either, 580 to 595; two threads a row, both warpgroups on one
-// query tile, 555; a suspended wait, 568; P V from a third of P, as from half; P in
-// columns of its own (head_dim 64), S ahead of the softmax: the query tiles fall
-// into step, 524 for 456.  Without V's conversion, for timing, 2 x 2,048 rows take 160
-// us instead of 169.
+// an issuer each for the query tiles; two threads a row, both warpgroups on one
+// query tile; a suspended wait; P V from a third of P: none faster.  P in columns of
+// its own (head_dim 64), S ahead of the softmax: the query tiles fall into step, 15 %
+// slower.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -170,7 +168,6 @@ __global__ void __launch_bounds__(kQpThreads, 1)
     quant_prefill_kernel(const QuantPrefillParams p, const __grid_constant__ CUtensorMap tk,
                          const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tout) {
     using Sh = QpShape<T, D>;
-    constexpr bool RES = WIDE || std::is_same<T, __half>::value;   // weights as value and residual (an fp16 or 32-bit output)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     QpBars *bars = reinterpret_cast<QpBars *>(sm + Sh::OFF_BAR);
@@ -368,7 +365,7 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                     // its query rows on their way to L2: they are read when the unit before is
                     // done (3 x 4,000 rows 551 us without, 530; 8 x 512 114 and 111; fp16 of
                     // head_dim 64, whose units are long, 100 without and 102)
-                    if constexpr (!(RES && D == 64)) {
+                    if constexpr (D == 128) {
                         const int lines = p.G * (D / 64);   // of 128 bytes, of a token
                         const uint8_t *rows = static_cast<const uint8_t *>(p.q) + ((int64_t)u.row0 * p.Hq + (int64_t)h * p.G) * (D * 2);
                         for (int i = lane; i < u.tokens * lines; i += 32) {
@@ -506,9 +503,9 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                                     const uint32_t ph = d_s + 32 * (kk >> 1) + 8 * (kk & 1);
                                     const uint32_t vp = vb + (uint32_t)(kk * Sh::PAGE >> 4);
                                     tc::mma_f16_ts(d_o, ph, vp, v_high, idesc_o, j > 0 || kk > 0);
-                                    if (RES) tc::mma_f16_ts(d_o, ph + 16, vp, v_high, idesc_o, true);   // the weights' rounding residual
+                                    tc::mma_f16_ts(d_o, ph + 16, vp, v_high, idesc_o, true);   // the weights' rounding residual
                                 }
-                                if (RES && part == 0) tc::mma_commit(&bars->half_done[t]);
+                                if (part == 0) tc::mma_commit(&bars->half_done[t]);
                             }
                             if (!ok) break;
                             if (t == TILES - 1) tc::mma_commit(&bars->v_empty[g & 1]);
@@ -679,211 +676,119 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                 ok = wait_all(&bars->scales_full[st], g / kQpScaleStages) && wait_all(&bars->s_full[t], g);
                 if (!ok) break;
                 tc::fence_after_sync();
-                if constexpr (!RES) {
-                    const int key0 = (tile0(u) + j) * kQpKeys;
-                    float v[kQpKeys];
+                // Half of the keys at a time, and no look for the largest y first: the code,
+                // unrolled for 128 keys, does not stay in the instruction cache (3 x 4,000
+                // rows in fp16 794 us, 725 so).
+#pragma unroll 1
+                for (int part = 0; part < 2; ++part) {
+                    constexpr int kHalf = kQpKeys / 2;
+                    float v[kHalf];
+                    tc::tmem_ld32(scol + part * kHalf, *reinterpret_cast<float(*)[32]>(v));
+                    tc::tmem_ld32(scol + part * kHalf + 32, *reinterpret_cast<float(*)[32]>(v + 32));
+                    // y = v f + lb with f, lb of the key's page
+                    float f[kHalf / 16], lb[kHalf / 16];
 #pragma unroll
-                    for (int cc = 0; cc < kQpKeys; cc += 32) tc::tmem_ld32(scol + cc, *reinterpret_cast<float(*)[32]>(v + cc));
-                    tc::tmem_wait_ld();
-                    // hidden: past the row's position; below its window and behind the first tokens
-                    const int lim = pos - key0, low = lim - p.window + 1, sk = p.sinks - key0;
-                    if (__any_sync(0xffffffffu, lim < kQpKeys - 1 || (low > 0 && sk < kQpKeys))) {
-                        auto below = [](int n) { return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u); };
-#pragma unroll
-                        for (int cc = 0; cc < kQpKeys; cc += 32) {
-                            const uint32_t see = below(lim + 1 - cc) & (~below(low - cc) | below(sk - cc));
-                            if (__any_sync(0xffffffffu, see != 0xffffffffu)) {
-#pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    if (!(see & (1u << e))) v[cc + e] = -INFINITY;
-                            }
-                        }
-                    }
-                    // y = v f + lb with f, lb of the key's page; f > 0, so a page's largest y is its largest v's
-                    // (read once: a load that all lanes make of one address costs shared
-                    // memory, which the products keep busy, as much as any other)
-                    float f[kQpPages], lb[kQpPages];
-                    float mx = -INFINITY;
-#pragma unroll
-                    for (int pg = 0; pg < kQpPages; ++pg) {
-                        const float2 sc = page_scales[st * kQpPages + pg];
+                    for (int pg = 0; pg < kHalf / 16; ++pg) {
+                        const float2 sc = page_scales[(st * 2 + part) * (kHalf / 16) + pg];
                         f[pg] = sc.x * rowscale;
                         lb[pg] = sc.y;
-                        float a = fmaxf(v[16 * pg], v[16 * pg + 1]), b = fmaxf(v[16 * pg + 2], v[16 * pg + 3]);
-#pragma unroll
-                        for (int e = 4; e < 16; e += 4) {
-                            a = fmax3(a, v[16 * pg + e], v[16 * pg + e + 1]);
-                            b = fmax3(b, v[16 * pg + e + 2], v[16 * pg + e + 3]);
-                        }
-                        mx = fmaxf(mx, fmaf(fmaxf(a, b), f[pg], lb[pg]));
                     }
-                    const bool first = m_used == -INFINITY;
-                    const float m_new = fmaxf(m_used, mx);
-                    const bool rescale = !first && m_new > m_used + 8.f;
-                    const float alpha = rescale ? exp2_approx(m_used - m_new) : 1.f;
-                    if (first || rescale) m_used = m_new;
-                    // O was last written by the P V product before, which the tensor
-                    // core finished before this tile's S (issued after it) completed
-                    if (__any_sync(0xffffffffu, rescale)) {
-#pragma unroll 1
-                        for (int cc = 0; cc < D; cc += 32) {
-                            float o[32];
-                            tc::tmem_ld32(ocol + cc, o);
-                            tc::tmem_wait_ld();
+                    tc::tmem_wait_ld();
+                    // hidden: past the row's position; below its window and behind the first tokens
+                    const int key0 = (tile0(u) + j) * kQpKeys + part * kHalf;
+                    const int lim = pos - key0, low = lim - p.window + 1, sk = p.sinks - key0;
+                    if (__any_sync(0xffffffffu, lim < kHalf - 1 || (low > 0 && sk < kHalf))) {
+                        auto below = [](int n) { return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u); };
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] *= alpha;
-                            tc::tmem_st32(ocol + cc, o);
+                        for (int cc = 0; cc < kHalf; cc += 32) {
+                            const uint32_t see = below(lim + 1 - cc) & (~below(low - cc) | below(sk - cc));
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (!(see & (1u << e))) v[cc + e] = -INFINITY;
                         }
                     }
-                    // P = 2^(y - m_used + 7) over the same columns, a page at a time: 8 columns
-                    // of rounded pairs.
-                    // A row that has seen no key yet has nothing to subtract.
-                    const float off = (m_used == -INFINITY ? 0.f : m_used) - 7.f;
-                    l *= alpha;
-#pragma unroll
-                    for (int pg = 0; pg < kQpPages; ++pg) {
-                        const float c = lb[pg] - off;
-                        const uint64_t f2 = f2_pack(f[pg], f[pg]), c2 = f2_pack(c, c);
-                        uint64_t sum2 = f2_pack(0.f, 0.f);
-                        uint32_t hi[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            float a, b;
-                            f2_unpack(f2_fma(f2_pack(v[16 * pg + 2 * e], v[16 * pg + 2 * e + 1]), f2, c2), a, b);
-                            a = exp2_approx(a);
-                            b = exp2_approx(b);
-                            const uint64_t ab = f2_pack(a, b);
-                            sum2 = f2_add(sum2, ab);
-                            hi[e] = pack2<__half>(a, b);
-                        }
-                        float s0, s1;
-                        f2_unpack(sum2, s0, s1);
-                        l = fmaf(s0 + s1, exp2_approx(-lb[pg]), l);
-                        const uint32_t to = scol + 32 * (pg >> 1) + 8 * (pg & 1);
-                        tc::tmem_st8(to, hi);
-                        if (pg == kQpPages / 2 - 1 || pg == kQpPages - 1) {   // a part of P is ready
-                            tc::tmem_wait_st();
-                            tc::fence_before_sync();
-                            __syncwarp();
-                            if (lane == 0) tc::mbar_arrive_cta(&bars->p_full[t][pg == kQpPages - 1]);
-                        }
-                    }
-                } else {
-                    // Half of the keys at a time, and no look for the largest y first: twice
-                    // the work on a weight, and code that, unrolled for 128 keys, does not
-                    // stay in the instruction cache (3 x 4,000 rows in fp16 794 us, 725 so;
-                    // rounded once, the loop takes 590 us for 545).
+                    // A row that has no maximum yet takes this half's (O has not been
+                    // written for it, or only with weights of 0).  Others go on with the
+                    // one they have, and look whether it still serves by the sums of P: a
+                    // page's sum of at most 2^15 has no weight above.
+                    bool raise = m_used == -INFINITY;
+                    float sum = 0.f;
 #pragma unroll 1
-                    for (int part = 0; part < 2; ++part) {
-                        constexpr int kHalf = kQpKeys / 2;
-                        float v[kHalf];
-                        tc::tmem_ld32(scol + part * kHalf, *reinterpret_cast<float(*)[32]>(v));
-                        tc::tmem_ld32(scol + part * kHalf + 32, *reinterpret_cast<float(*)[32]>(v + 32));
-                        // y = v f + lb with f, lb of the key's page
-                        float f[kHalf / 16], lb[kHalf / 16];
-#pragma unroll
-                        for (int pg = 0; pg < kHalf / 16; ++pg) {
-                            const float2 sc = page_scales[(st * 2 + part) * (kHalf / 16) + pg];
-                            f[pg] = sc.x * rowscale;
-                            lb[pg] = sc.y;
-                        }
-                        tc::tmem_wait_ld();
-                        // hidden: past the row's position; below its window and behind the first tokens
-                        const int key0 = (tile0(u) + j) * kQpKeys + part * kHalf;
-                        const int lim = pos - key0, low = lim - p.window + 1, sk = p.sinks - key0;
-                        if (__any_sync(0xffffffffu, lim < kHalf - 1 || (low > 0 && sk < kHalf))) {
-                            auto below = [](int n) { return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u); };
-#pragma unroll
-                            for (int cc = 0; cc < kHalf; cc += 32) {
-                                const uint32_t see = below(lim + 1 - cc) & (~below(low - cc) | below(sk - cc));
-#pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    if (!(see & (1u << e))) v[cc + e] = -INFINITY;
-                            }
-                        }
-                        // A row that has no maximum yet takes this half's (O has not been
-                        // written for it, or only with weights of 0).  Others go on with the
-                        // one they have, and look whether it still serves by the sums of P: a
-                        // page's sum of at most 2^15 has no weight above.
-                        bool raise = m_used == -INFINITY;
-                        float sum = 0.f;
-#pragma unroll 1
-                        for (int go = 0; go < 2; ++go) {   // (raised to the largest y there is, it serves)
-                            if (__any_sync(0xffffffffu, raise)) {
-                                // m_used becomes the largest y so far; O and l follow.  O was last
-                                // written by the P V product of the tile before, which the tensor
-                                // core finished before this tile's S (issued after it) completed,
-                                // or by the first half's
-                                if (part == 1) ok = wait_all(&bars->half_done[t], g);
-                                if (!ok) break;
-                                tc::fence_after_sync();
-                                float mx = m_used;
-#pragma unroll
-                                for (int pg = 0; pg < kHalf / 16; ++pg) {
-                                    float a = fmaxf(v[16 * pg], v[16 * pg + 1]), b = fmaxf(v[16 * pg + 2], v[16 * pg + 3]);
-#pragma unroll
-                                    for (int e = 4; e < 16; e += 4) {
-                                        a = fmax3(a, v[16 * pg + e], v[16 * pg + e + 1]);
-                                        b = fmax3(b, v[16 * pg + e + 2], v[16 * pg + e + 3]);
-                                    }
-                                    mx = fmaxf(mx, fmaf(fmaxf(a, b), f[pg], lb[pg]));   // (f > 0)
-                                }
-                                const float alpha = raise && m_used > -INFINITY ? exp2_approx(m_used - mx) : 1.f;
-                                if (raise) m_used = mx;
-                                l *= alpha;
-                                if (__any_sync(0xffffffffu, alpha != 1.f)) {
-#pragma unroll 1
-                                    for (int cc = 0; cc < D; cc += 32) {
-                                        float o[32];
-                                        tc::tmem_ld32(ocol + cc, o);
-                                        tc::tmem_wait_ld();
-#pragma unroll
-                                        for (int e = 0; e < 32; ++e) o[e] *= alpha;
-                                        tc::tmem_st32(ocol + cc, o);
-                                    }
-                                }
-                            }
-                            // P = 2^(y - m_used + 7) over the same columns, a page at a time: 8
-                            // columns of rounded pairs (and 16 further 8 of residual pairs).
-                            // (A row that has seen no key yet has nothing to subtract.)
-                            const float off = (m_used == -INFINITY ? 0.f : m_used) - 7.f;
-                            float top = 0.f;
-                            sum = 0.f;
+                    for (int go = 0; go < 2; ++go) {   // (raised to the largest y there is, it serves)
+                        if (__any_sync(0xffffffffu, raise)) {
+                            // m_used becomes the largest y so far; O and l follow.  O was last
+                            // written by the P V product of the tile before, which the tensor
+                            // core finished before this tile's S (issued after it) completed,
+                            // or by the first half's
+                            if (part == 1) ok = wait_all(&bars->half_done[t], g);
+                            if (!ok) break;
+                            tc::fence_after_sync();
+                            float mx = m_used;
 #pragma unroll
                             for (int pg = 0; pg < kHalf / 16; ++pg) {
-                                const float c = lb[pg] - off;
-                                const uint64_t f2 = f2_pack(f[pg], f[pg]), c2 = f2_pack(c, c);
-                                uint64_t sum2 = f2_pack(0.f, 0.f);
-                                uint32_t hi[8], lo[8];
+                                float a = fmaxf(v[16 * pg], v[16 * pg + 1]), b = fmaxf(v[16 * pg + 2], v[16 * pg + 3]);
 #pragma unroll
-                                for (int e = 0; e < 8; ++e) {
-                                    float a, b;
-                                    f2_unpack(f2_fma(f2_pack(v[16 * pg + 2 * e], v[16 * pg + 2 * e + 1]), f2, c2), a, b);
-                                    a = exp2_approx(a);
-                                    b = exp2_approx(b);
-                                    const uint64_t ab = f2_pack(a, b);
-                                    sum2 = f2_add(sum2, ab);
-                                    pack2_split2<__half>(ab, a, b, hi[e], lo[e]);
+                                for (int e = 4; e < 16; e += 4) {
+                                    a = fmax3(a, v[16 * pg + e], v[16 * pg + e + 1]);
+                                    b = fmax3(b, v[16 * pg + e + 2], v[16 * pg + e + 3]);
                                 }
-                                float s0, s1;
-                                f2_unpack(sum2, s0, s1);
-                                s0 += s1;
-                                top = fmaxf(top, s0);
-                                sum = fmaf(s0, exp2_approx(-lb[pg]), sum);
-                                const uint32_t to = scol + part * kHalf + 32 * (pg >> 1) + 8 * (pg & 1);
-                                tc::tmem_st8(to, hi);
-                                tc::tmem_st8(to + 16, lo);
+                                mx = fmaxf(mx, fmaf(fmaxf(a, b), f[pg], lb[pg]));   // (f > 0)
                             }
-                            raise = top > 32768.f;
-                            if (!__any_sync(0xffffffffu, raise)) break;
+                            const float alpha = raise && m_used > -INFINITY ? exp2_approx(m_used - mx) : 1.f;
+                            if (raise) m_used = mx;
+                            l *= alpha;
+                            if (__any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+                                for (int cc = 0; cc < D; cc += 32) {
+                                    float o[32];
+                                    tc::tmem_ld32(ocol + cc, o);
+                                    tc::tmem_wait_ld();
+#pragma unroll
+                                    for (int e = 0; e < 32; ++e) o[e] *= alpha;
+                                    tc::tmem_st32(ocol + cc, o);
+                                }
+                            }
                         }
-                        if (!ok) break;
-                        l += sum;
-                        tc::tmem_wait_st();   // a part of P is ready
-                        tc::fence_before_sync();
-                        __syncwarp();
-                        if (lane == 0) tc::mbar_arrive_cta(&bars->p_full[t][part]);
+                        // P = 2^(y - m_used + 7) over the same columns, a page at a time: 8
+                        // columns of rounded pairs (and 16 further 8 of residual pairs).
+                        // (A row that has seen no key yet has nothing to subtract.)
+                        const float off = (m_used == -INFINITY ? 0.f : m_used) - 7.f;
+                        float top = 0.f;
+                        sum = 0.f;
+#pragma unroll
+                        for (int pg = 0; pg < kHalf / 16; ++pg) {
+                            const float c = lb[pg] - off;
+                            const uint64_t f2 = f2_pack(f[pg], f[pg]), c2 = f2_pack(c, c);
+                            uint64_t sum2 = f2_pack(0.f, 0.f);
+                            uint32_t hi[8], lo[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                float a, b;
+                                f2_unpack(f2_fma(f2_pack(v[16 * pg + 2 * e], v[16 * pg + 2 * e + 1]), f2, c2), a, b);
+                                a = exp2_approx(a);
+                                b = exp2_approx(b);
+                                const uint64_t ab = f2_pack(a, b);
+                                sum2 = f2_add(sum2, ab);
+                                pack2_split2<__half>(ab, a, b, hi[e], lo[e]);
+                            }
+                            float s0, s1;
+                            f2_unpack(sum2, s0, s1);
+                            s0 += s1;
+                            top = fmaxf(top, s0);
+                            sum = fmaf(s0, exp2_approx(-lb[pg]), sum);
+                            const uint32_t to = scol + part * kHalf + 32 * (pg >> 1) + 8 * (pg & 1);
+                            tc::tmem_st8(to, hi);
+                            tc::tmem_st8(to + 16, lo);
+                        }
+                        raise = top > 32768.f;
+                        if (!__any_sync(0xffffffffu, raise)) break;
                     }
+                    if (!ok) break;
+                    l += sum;
+                    tc::tmem_wait_st();   // a part of P is ready
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive_cta(&bars->p_full[t][part]);
                 }
                 if (!ok) break;
                 if (lane == 0) tc::mbar_arrive_cta(&bars->scales_empty[st]);
