@@ -203,6 +203,13 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
     return d;
 }
 
+// The larger of two; NaN where one is.
+__device__ __forceinline__ float fmax_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
 // Pack two floats into a 16-bit pair (round to nearest even); `lo` goes to
 // the low half (the lower-indexed element of an MMA fragment).
 template <typename T>

@@ -685,12 +685,14 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                     float v[kHalf];
                     tc::tmem_ld32(scol + part * kHalf, *reinterpret_cast<float(*)[32]>(v));
                     tc::tmem_ld32(scol + part * kHalf + 32, *reinterpret_cast<float(*)[32]>(v + 32));
-                    // y = v f + lb with f, lb of the key's page
+                    // y = v f + lb with f, lb of the key's page.  f is kept from falling to 0
+                    // (rows or keys of zeros have tiny scales), where a hidden v, -infinity,
+                    // would make NaN of it; |v| is below 2^25, so y moves by less than 2^-101.
                     float f[kHalf / 16], lb[kHalf / 16];
 #pragma unroll
                     for (int pg = 0; pg < kHalf / 16; ++pg) {
                         const float2 sc = page_scales[(st * 2 + part) * (kHalf / 16) + pg];
-                        f[pg] = sc.x * rowscale;
+                        f[pg] = fmax_nan(sc.x * rowscale, 0x1p-126f);
                         lb[pg] = sc.y;
                     }
                     tc::tmem_wait_ld();
