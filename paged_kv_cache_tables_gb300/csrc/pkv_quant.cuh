@@ -46,6 +46,27 @@ __device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d
     return r;
 }
 
+// The same in e5m2 (beyond 57,344 its code), and back.
+__device__ __forceinline__ uint32_t to_e5m2x4(float a, float b, float c, float d) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 lo, hi;\n\t"
+        "cvt.rn.satfinite.e5m2x2.f32 lo, %2, %1;\n\t"
+        "cvt.rn.satfinite.e5m2x2.f32 hi, %4, %3;\n\t"
+        "mov.b32 %0, {lo, hi};\n\t}"
+        : "=r"(r)
+        : "f"(a), "f"(b), "f"(c), "f"(d));
+    return r;
+}
+
+__device__ __forceinline__ void e5m2x4_to_f16x4(uint32_t codes, uint32_t &first, uint32_t &second) {
+    asm("{\n\t.reg .b16 lo, hi;\n\t"
+        "mov.b32 {lo, hi}, %2;\n\t"
+        "cvt.rn.f16x2.e5m2x2 %0, lo;\n\t"
+        "cvt.rn.f16x2.e5m2x2 %1, hi;\n\t}"
+        : "=r"(first), "=r"(second)
+        : "r"(codes));
+}
+
 __device__ __forceinline__ float2 f16x2_to_f32(uint32_t pair) { return __half22float2(*reinterpret_cast<__half2 *>(&pair)); }
 
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {

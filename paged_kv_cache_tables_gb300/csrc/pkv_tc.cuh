@@ -89,10 +89,12 @@ __device__ __forceinline__ uint64_t smem_desc_sw64(uint32_t saddr, uint32_t lbo,
     return d;
 }
 
-// Instruction descriptor, kind::f8f6f4 with e4m3 A and B, both K-major: fp32
-// accumulator, M x N tile.
-__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
+// Instruction descriptor, kind::f8f6f4 with A and B each e4m3 or e5m2, both K-major:
+// fp32 accumulator, M x N tile.
+__host__ __device__ constexpr uint32_t idesc_f8(bool a_e5m2, bool b_e5m2, int M, int N) {
     return (1u << 4)                            // D format: f32
+           | ((uint32_t)a_e5m2 << 7)            // A format: e4m3, or e5m2
+           | ((uint32_t)b_e5m2 << 10)           // B format
            | ((uint32_t)(N >> 3) << 17)         // N / 8
            | ((uint32_t)(M >> 4) << 24);        // M / 16
 }

@@ -10,13 +10,16 @@
 // below that, and the largest at least 2^7, whatever the scales are.
 //
 // Both products run on the codes without their scales:
-//   S = q' k^T   in e4m3 (kind::f8f6f4, twice the rate of 16 bits): K goes from the
+//   S = q' k^T   in 8 bits (kind::f8f6f4, twice the rate of 16): K goes from the
 //                cache to the tensor cores as it is.  A query row is f times the
-//                sum of e4m3 terms, each the rounding of what the ones before
-//                leave, f the power of two with its largest element in (224, 448]:
-//                two terms hold bf16's 8 bits, three fp16's 11, down to 2^-10 (2^-18
-//                of the largest element at most).  As many steps as in 16 bits, or
-//                one and a half times for fp16.
+//                sum of terms, each the rounding of what the ones before leave, f
+//                the power of two with its largest element in (224, 448]: one of
+//                e4m3's four bits, then of e5m2's three, whose range goes down to
+//                2^-16 where e4m3's ends at 2^-9.  Two terms hold bf16's 8 bits, three
+//                fp16's 11, of elements down to 2^-13.8 of the row's largest;
+//                smaller ones are off by at most 2^-21.8 of it, or 2^-24.8 in fp16 (with
+//                e4m3 terms alone: down to 2^-9.8 and 2^-6.8, off by 2^-17.8).  As
+//                many steps as in 16 bits, or one and a half times for fp16.
 //   O += P v     in fp16: v is converted on the way (exact), P is value and residual,
 //                two products, for any output.  (With P rounded once, 2^-11 of a
 //                weight, 3 x 4,000 rows of bf16 would take 538 us instead of 724, and
@@ -31,8 +34,9 @@
 //   1      one thread issues the MMAs of both query tiles, turn by turn
 //   2, 3   V's codes to fp16, in the layout of an MN-major operand; rows that no row
 //          of the unit sees become zero (they may hold NaN codes)
-//   4-11   softmax: a warpgroup a query tile, a row per thread; each row's terms are
-//          made by its thread, the next unit's while the last P V of this one runs
+//   4-11   softmax: a warpgroup a query tile, a row per thread; its rows' terms are
+//          made by head_dim / 8 lanes each, the next unit's while the last P V of this
+//          one runs
 // Units go out longest first, found by bisection over up to 32 chunks a lane each
 // (8 x 512 behind 0 to 4,096 tokens 131 us chunk by chunk, 114 so).  Where one query
 // tile a unit leaves SMs without one, the unit's keys go to the CTAs of a cluster,
@@ -453,7 +457,9 @@ __global__ void __launch_bounds__(kQpThreads, 1)
             // prompts of 2,000).  The query tiles take turns: P V of a key tile and S of
             // the next are one turn, so that a tile's softmax runs beside the other's turn.
             if (tc::elect_one()) {
-                constexpr uint32_t idesc_s = tc::idesc_e4m3(kQpRows, kQpKeys);
+                // (the query's first term is e4m3, the others e5m2; K e4m3)
+                constexpr uint32_t idesc_s = tc::idesc_f8(false, false, kQpRows, kQpKeys);
+                constexpr uint32_t idesc_s5 = tc::idesc_f8(true, false, kQpRows, kQpKeys);
                 constexpr uint32_t idesc_o = tc::idesc_f16(false, false, true, kQpRows, D);
                 auto code_desc = [&](uint32_t at) { return D == 128 ? tc::smem_desc_sw128(at, 16, 1024) : tc::smem_desc_sw64(at, 16, 512); };
                 // descriptors: the upper half, and the lower one of each operand's first byte
@@ -470,7 +476,7 @@ __global__ void __launch_bounds__(kQpThreads, 1)
 #pragma unroll
                     for (int i = 0; i < Sh::TERMS * STEPS; ++i) {
                         const uint32_t qo = ((i / STEPS) * Sh::Q_TERM + (i % STEPS) * 32) >> 4, ko = ((i % STEPS) * 32) >> 4;
-                        tc::mma_f8_ss(tmem + t * 256, qb + qo, kb + ko, code_high, idesc_s, i > 0);
+                        tc::mma_f8_ss(tmem + t * 256, qb + qo, kb + ko, code_high, i < STEPS ? idesc_s : idesc_s5, i > 0);
                     }
                     tc::mma_commit(&bars->s_full[t]);
                     if (t == TILES - 1) tc::mma_commit(&bars->k_empty[k & 1]);
@@ -641,9 +647,14 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                         uint32_t c[2];
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            c[e] = to_e4m3x4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
                             uint32_t lo, hi;
-                            e4m3x4_to_f16x4(c[e], lo, hi);
+                            if (term == 0) {
+                                c[e] = to_e4m3x4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                                e4m3x4_to_f16x4(c[e], lo, hi);
+                            } else {
+                                c[e] = to_e5m2x4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                                e5m2x4_to_f16x4(c[e], lo, hi);
+                            }
                             const float2 fl = f16x2_to_f32(lo), fh = f16x2_to_f32(hi);
                             v[4 * e] -= fl.x;
                             v[4 * e + 1] -= fl.y;
