@@ -13,8 +13,9 @@
 // The codes of K are multiplied as they are: a query is split into e4m3 terms,
 //     q = f (t_0 + t_1 / 16 [+ t_2 / 256]),
 // f a power of two per head that puts its largest element into [128, 256).  Each
-// term takes four bits, so two hold a bf16 element and three an fp16 one exactly,
-// down to 2^-14 of the head's largest; smaller ones are off by at most 2^-22 of it.
+// term takes four bits, so two hold a bf16 element exactly, down to 2^-13 of the
+// head's largest, and three an fp16 one, down to 2^-14; smaller ones are off by at
+// most 2^-21 of it, or 2^-25.
 //
 // Layout.  Tokens are the rows of S^T = K Q^T, head_dim those of O^T = V^T P^T.
 // Four heads are the eight columns of a tile: of S^T a head's two terms, of P^T
