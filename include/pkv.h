@@ -487,9 +487,19 @@ int pkv_kv_gather_e4m3(void *k, void *v, const void *k_cache, const void *v_cach
  * pkv_paged_decode_attention_e4m3 -- pkv_paged_window_decode_attention over a
  * cache held in 8 bits; a window of at least max_blocks_per_seq * block_size is
  * the whole context.  Arguments, limits and guarantees as there; num_q_heads <=
- * 65,536 (PKV_ERR_UNSUPPORTED).  kv_scales of
- * blocks that are read must be positive and finite (any such value will do, not
- * just powers of two).  A block id outside the pool reads zeros.
+ * 65,536 (PKV_ERR_UNSUPPORTED).  A block id outside the pool reads zeros.
+ * kv_scales of blocks that are read are positive and finite, powers of two or not;
+ * V's lie between 2^-80 and 2^120, and those of the blocks that one query sees
+ * within a factor of 2^100 of one another.  (Append writes 2^-60 to 2^120: only
+ * values beyond 2^48 next to tiles of zeros fall outside.)  Scores times log2 e,
+ * plus the log2 of V's scale, stay below 2^22 in magnitude: of larger ones fp32
+ * holds too few bits behind the point for weights relative to a maximum.  A query's
+ * largest element times a K scale that it sees times `scale` stays below 2^100, even
+ * where the codes are zeros.  None of this is checked: outside of it outputs are not
+ * specified.
+ * Besides its own rounding an output is off by up to n 2^-32 of 448 b, for n
+ * positions, b V's scale at the one whose score plus log2 of its scale is largest:
+ * values far below what b can hold show only in so far.
  */
 int pkv_paged_decode_attention_e4m3(void *out, const void *q, const void *k_cache, const void *v_cache,
                                     const float *kv_scales, const int32_t *block_tables, int max_blocks_per_seq,
@@ -499,10 +509,8 @@ int pkv_paged_decode_attention_e4m3(void *out, const void *q, const void *k_cach
 
 /*
  * pkv_paged_prefill_attention_e4m3 -- pkv_paged_window_prefill_attention over a
- * cache held in 8 bits, with the window and kv_scales of
- * pkv_paged_decode_attention_e4m3, and its limit.  Scores times log2 e, plus the
- * log2 of V's scale, are to stay below 2^22 in magnitude: of larger ones fp32
- * holds too few bits behind the point for weights relative to a maximum.
+ * cache held in 8 bits, with the window, the limits and the scales of
+ * pkv_paged_decode_attention_e4m3.
  */
 int pkv_paged_prefill_attention_e4m3(void *out, const void *q, const int32_t *cu_seqlens, int num_seqs, int max_q_len,
                                      int total_q, const void *k_cache, const void *v_cache, const float *kv_scales,
