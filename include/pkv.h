@@ -458,7 +458,7 @@ int pkv_paged_window_prefill_attention(void *out, const void *q, const int32_t *
  * scheduler and pkv_step_tables lay a step out, and slots must be unique: else
  * what that block holds afterwards is not specified.  slot_mapping, padding
  * rows and slots outside the pool as in pkv_kv_append.  num_tokens *
- * num_kv_heads < 2^30 (PKV_ERR_UNSUPPORTED).  One launch.
+ * num_kv_heads < 2^30, num_kv_heads <= 65,536 (PKV_ERR_UNSUPPORTED).  One launch.
  */
 int pkv_kv_append_e4m3(const void *k, int64_t k_stride, const void *v, int64_t v_stride, const int64_t *slot_mapping,
                        int num_tokens, void *k_cache, void *v_cache, float *kv_scales, int num_blocks, int block_size,

@@ -357,6 +357,7 @@ extern "C" int pkv_kv_append_e4m3(const void *k, int64_t k_stride, const void *v
     if (dtype != PKV_DTYPE_F16 && dtype != PKV_DTYPE_BF16) return PKV_ERR_UNSUPPORTED;
     if (block_size != 16 || (head_dim != 64 && head_dim != 128)) return PKV_ERR_UNSUPPORTED;
     if ((int64_t)num_tokens * num_kv_heads >= (int64_t)1 << 30) return PKV_ERR_UNSUPPORTED;
+    if (num_kv_heads > 1 << 16) return PKV_ERR_UNSUPPORTED;   // (offsets in a token's row are 32-bit)
     if (num_tokens == 0) return PKV_OK;
     if (!k || !v || !slot_mapping || !k_cache || !v_cache || !kv_scales) return PKV_ERR_INVALID_ARG;
     if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(slot_mapping, 8) ||
