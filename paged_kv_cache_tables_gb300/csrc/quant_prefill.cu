@@ -795,6 +795,7 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                         }
                         raise = top > 32768.f;
                         if (!__any_sync(0xffffffffu, raise)) break;
+                        tc::tmem_wait_st();   // (stores to the same columns need not keep their order)
                     }
                     if (!ok) break;
                     l += sum;

@@ -42,3 +42,24 @@ def test_rows_that_see_few_keys(cuda_lib, n, d):
         got = st.prefill(BF16)
         ref.assert_within(got, *bound16(st, BF16), "%d keys" % n)
         assert torch.equal(got, st.prefill(F32).to(BF16))
+
+
+@pytest.mark.parametrize("ctx,qn", SHAPES)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_scores_that_rise_all_along(cuda_lib, ctx, qn, d, dtype):
+    """Each page's scores 2^8 or more above the page's before, so that every part of the keys moves the maximum on and its
+    weights are made, and stored, twice; the same bits at every call."""
+    st = Step(ctx, qn, 8, 2, d, dtype, WHOLE, 0, seed=9, poison=False)
+    st.kc.zero_()
+    st.kc[..., 3] = 0x38                     # 1 in one dimension
+    st.q[..., 3] = 1
+    for s, c in enumerate(ctx):
+        nb = -(-c // 16)
+        st.scales[st.table[s].long()[:nb], :, 0] = (5.6 * d ** 0.5 * (torch.arange(nb) + 1.0)).view(nb, 1)   # 8.08 in log2
+    st.k, st.dev["scales"], st.dev["q"] = st.kc.cuda().view(st.k.dtype), st.scales.cuda(), st.q.cuda()
+    got = st.prefill(dtype)
+    ref.assert_within(got, *bound16(st, dtype))
+    for _ in range(3):
+        assert torch.equal(st.prefill(dtype), got)
+    assert st.status.item() == 0
