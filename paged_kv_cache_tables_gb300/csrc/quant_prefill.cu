@@ -38,19 +38,20 @@
 //          made by head_dim / 8 lanes each, the next unit's while the last P V of this
 //          one runs
 // Units go out longest first, found by bisection over up to 32 chunks a lane each
-// (8 x 512 behind 0 to 4,096 tokens 131 us chunk by chunk, 114 so).  Where one query
-// tile a unit leaves SMs without one, the unit's keys go to the CTAs of a cluster,
-// and the parts are joined through its shared memory (16 rows behind 4,096: 54 us
-// in 8 CTAs, 19 in 64).
+// (us, and chunk by chunk: 8 x 512 behind 0 to 4,096 tokens 140 and 154, 5 x 2,000 of
+// head_dim 64 97 and 107; 3 x 4,000 behind a window, whose units are alike, 694 and
+// 681).  Where one query tile a unit leaves SMs without one, the unit's keys go to
+// the CTAs of a cluster, and the parts are joined through its shared memory (us, and in
+// one CTA a unit: 16 rows behind 4,096 17.9 and 62; 50 behind 20,000 94 and 284).
 //
 // What bounds it: a key tile for two query tiles of head_dim 128 is 3,072 cycles of
 // products, a third of them the residual's, and a chain, S, softmax, P V, of which
 // two run at a time.  Beside the products' time without the residual's, at the
 // measured rate of 16 bits and the contexts that were timed: 8 chunks of 512 rows
-// behind 0 to 4,096 tokens 153 us for 74 (over a 16-bit cache 160); 3 x 4,000 rows,
-// window 4,096, 724 for 392 (641 to 684); 5 prompts of 2,000, head_dim 64, fp16
-// 98 for 25 (102), bound by the softmax and the issue of products that are half as
-// long.
+// behind 0 to 4,096 tokens 140 us for 74 (over a 16-bit cache 160); 3 x 4,000 rows,
+// window 4,096, 694 for 392 (641 to 684); 5 prompts of 2,000, head_dim 64, 94 for 25
+// in bf16 and 97 in fp16 (97, 102), bound by the softmax and the issue of products
+// that are half as long.
 // Measured and left (3 x 4,000 unless stated): a fourth warpgroup for V and the scales,
 // an issuer each for the query tiles; two threads a row, both warpgroups on one
 // query tile; a suspended wait; P V from a third of P: none faster.  P in columns of
@@ -367,8 +368,11 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                         tc::mbar_arrive_cta(&bars->unit_full[n & 1]);
                     }
                     // its query rows on their way to L2: they are read when the unit before is
-                    // done (3 x 4,000 rows 551 us without, 530; 8 x 512 114 and 111; fp16 of
-                    // head_dim 64, whose units are long, 100 without and 102)
+                    // done (us with and without, 16-bit outputs: 3 x 4,000 rows 694 and 712, in
+                    // fp16 742 and 770; 8 x 512 140 and 148, 157 and 162; 32-bit outputs alike.
+                    // Heads of 64, whose rows are half as long, bf16 and fp16: 3 x 4,000 613 and
+                    // 600, 641 and 623; 8 x 512 128 and 126, 134 and 130; 5 x 2,000 98 and 97, 103
+                    // and 100)
                     if constexpr (D == 128) {
                         const int lines = p.G * (D / 64);   // of 128 bytes, of a token
                         const uint8_t *rows = static_cast<const uint8_t *>(p.q) + ((int64_t)u.row0 * p.Hq + (int64_t)h * p.G) * (D * 2);
@@ -612,10 +616,10 @@ __global__ void __launch_bounds__(kQpThreads, 1)
             }
             float scale = 0.f;
             // (a loop, and the rows moved up in it: unrolled, this code, which runs once a
-            // unit, takes longer to come from memory than to run.  8 x 512 rows 134 us
-            // unrolled, 111 two rows at a time, 108.5 four; where a CTA has one unit, 1 x 512
-            // 60 two at a time, 66 four)
-            constexpr int PER = TILES == 2 ? 4 : 2;
+            // unit, takes longer to come from memory than to run: 8 x 512 rows a fifth
+            // longer.  Four rows at a time or two: 140 us and 147, 3 x 4,000 694 and 706, with
+            // 32-bit outputs 153 and 148, 715 and 701; others within 1 %)
+            constexpr int PER = 4;
 #pragma unroll 1
             for (int i0 = 0; i0 < N; i0 += PER) {
 #pragma unroll
@@ -688,8 +692,8 @@ __global__ void __launch_bounds__(kQpThreads, 1)
                 if (!ok) break;
                 tc::fence_after_sync();
                 // Half of the keys at a time, and no look for the largest y first: the code,
-                // unrolled for 128 keys, does not stay in the instruction cache (3 x 4,000
-                // rows in fp16 794 us, 725 so).
+                // unrolled for 128 keys, does not stay in the instruction cache (a tenth
+                // slower).
 #pragma unroll 1
                 for (int part = 0; part < 2; ++part) {
                     constexpr int kHalf = kQpKeys / 2;
