@@ -363,14 +363,19 @@ extern "C" int pkv_kv_append_e4m3(const void *k, int64_t k_stride, const void *v
     if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(slot_mapping, 8) ||
         !aligned(kv_scales, 8) || k_stride < 0 || v_stride < 0 || k_stride % 8 != 0 || v_stride % 8 != 0)
         return PKV_ERR_INVALID_ARG;
-    // Tokens a CTA, and CTAs that share them: few where the rows are few (256 decodes
-    // 2.4 us in spans of 8 shared by four CTAs, 4.9 of 16 by two; one chunk of 512 3.4
-    // and 3.1), else 16, by as many as leave a warp 8 KB of a block's rows (a prompt of
-    // 16,383 rows, 16 heads of 64, 20 us in spans of 16 by two, 27.5 in spans of 8 by
-    // four; 6,000 rows of 32 heads of 128 25.1 us by eight, 30.7 by two; 16,383 of one
-    // head 5.2 by one, 6.0 by two).
-    const int span = num_tokens <= 1024 ? 8 : 16;
-    const int slices = num_tokens <= 1024 ? 4 : std::max(1, std::min(8, num_kv_heads * head_dim / 512));
+    // Tokens a CTA, and CTAs that share them.  16 tokens, by as many CTAs as leave a
+    // warp 8 KB of a block's rows (a prompt of 16,383 rows, 16 heads of 64, 20 us in
+    // spans of 16 by two, 27.5 in spans of 8 by four; 6,000 rows of 32 heads of 128 25.1
+    // us by eight, 30.7 by two; 16,383 of one head 5.2 by one, 6.0 by two).  Where rows
+    // are few, 8 by four (us, and in spans of 16; 8 heads of 128 and 16 of 64): 256
+    // decodes 2.0 and 4.4, 2.2 and 5.0; 1,000 2.9 and 4.5, 3.0 and 5.1; 4 chunks of 250
+    // 3.9 and 4.8, 3.4 and 5.3; 500 decodes and a chunk of 500 4.0 and 4.5, 3.2 and 5.1; but
+    // a chunk of 512 alone 3.0 and 2.5, 2.5 and 2.7, one of 1,000 3.8 and 2.6, 3.1 and
+    // 2.8.  Rows of 32 heads of 128 have eight CTAs a span of 16, and gain nothing from
+    // spans of 8: 256 decodes 4.5 and 4.5, a chunk of 512 5.9 and 3.1.
+    const bool few = num_tokens <= 1024 && num_kv_heads * head_dim < 4096;
+    const int span = few ? 8 : 16;
+    const int slices = few ? 4 : std::max(1, std::min(8, num_kv_heads * head_dim / 512));
     const QuantAppendParams prm = {k, v, k_stride, v_stride, slot_mapping, static_cast<uint8_t *>(k_cache),
                                    static_cast<uint8_t *>(v_cache), kv_scales, dev_status, num_tokens, num_blocks,
                                    num_kv_heads, span};
