@@ -9,12 +9,12 @@
 // scale(a) the least power of two with a <= 448 scale(a).
 //
 // What bounds them: HBM, and for few rows the chain slot, row and scale, maximum,
-// store.  Append of 256 decodes (8 heads of 128, bf16) 2.4 us, 4,327 mixed rows 7.6
-// us (52 % of the measured copy rate), a prompt of 16,383 rows (16 heads of 64,
-// fp16) 20 us (74 %; 8 heads of 128 18.7, 80 %); with a warp for every (token, head, K or V), most of which
-// found another one to do their work, 4.9, 16 and 78 us.  Read back: 64 sequences
-// of up to 8,000 tokens (742 MB) 114 us, 96 %; 32-bit rows 190 us, 96 %; 777 rows 4.5
-// us.  With 16 codes and 32 bytes of output a thread, halves of whose sectors were
+// store.  Append of 256 decodes (8 heads of 128, bf16) 2.0 us, 4,327 mixed rows 7.0
+// us (56 % of the measured copy rate), a prompt of 16,383 rows (16 heads of 64,
+// fp16) 19.8 us (75 %; 8 heads of 128 18.7, 80 %); with a warp for every (token, head,
+// K or V), most of which found another one to do their work, 4.9, 16 and 78 us.
+// Read back: 64 sequences of up to 8,000 tokens (742 MB) 114 us, 96 %; 32-bit rows 190
+// us, 96 %; 777 rows 4.1 us.  With 16 codes and 32 bytes of output a thread, halves of whose sectors were
 // stored apart, and each row's sequence searched for by itself, 192 us.
 #include <cuda_runtime.h>
 

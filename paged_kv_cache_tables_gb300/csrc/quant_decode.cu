@@ -36,11 +36,15 @@
 // warp runs a ring of its own, filled by 16-byte asynchronous copies.
 //
 // What bounds it: HBM.  256 sequences x 8 KV heads of 1,400 tokens (740 MB of codes
-// and scales): 113 us, 96 % of the measured copy rate; 16-bit caches take twice
-// the bytes.  7 x 8 of 60,000 to 131,072: 222 us, 98 %.  256 of 32 to 8,192 tokens:
-// 128 us (86 %): what is left there is the order (below) and the last ranges.
-// Groups of 8 heads: 78 us for 372 MB (70 %), bound by the products and the
-// softmax, 350 instructions a block and warp instead of 200.
+// and scales): 112.5 us, 97 % of the measured copy rate (a 16-bit cache, twice the
+// bytes, 205); fp16 queries, whose third term is a product more, 120.  7 x 8 of
+// 60,000 to 131,072: 208 us, 97 % of the floor of the lengths that were timed.  256 of
+// 32 to 8,192 tokens: 118 us, 95 % (fp16 123): what is left there is the order (below)
+// and the last ranges.  With a window of 1,024 and 64 first tokens 57, 84 %: a range
+// is at most 69 blocks and starts with its length, table and scales; 64 x 8 behind a
+// window of 4,096 89, 90 %.  Groups of 8 heads: 78 us for 372 MB (70 %), bound by the
+// products and the softmax, 350 instructions a block and warp instead of 200; of 16
+// 67 for 188 MB (42 %), two ranges that load and convert the same blocks.
 // Measured and left: codes of K converted to fp16 and tokens as columns, 390
 // instructions a block, 119 us; with tokens as rows, 290, 113 us; TMA instead of
 // the copies, whose issue costs a lane 48 cycles and some 20 instructions a tile, 7
@@ -80,15 +84,20 @@ struct QuantDecodeParams {
 // Two forms for up to 4 heads a KV head.  PAIRS: two blocks a step, three CTAs an
 // SM, for long ranges, where a warp's time for a step is a chain of latencies that
 // two blocks share; otherwise one block a step and four CTAs, for short ranges,
-// where what counts is how many are under way.  us, PAIRS / not (with TMA): 256
-// sequences x 8 of 32 to 8,192 tokens 127 / 144, 40 x 8 of 2,048 30.6 / 35.4; 1,000
-// x 8 of 100 to 600 117 / 108, 256 x 8 of 30 to 130 22.5 / 19.0, 64 x 8 of 1,000 (512
-// CTAs: one wave of four an SM, or two of three) 31.5 / 25.3.  With heads of 64 pairs
-// leave registers for four CTAs, and are for split ranges too (64 x 8 of 64 to 4,096
-// 21.6 / 23.3, 128 x 8 of 2,000 48 / 52 in three CTAs; with heads of 128 split ranges
-// take longer, 16 x 8 of 8,000 57 / 47).  More heads (NT ==
-// 2, up to 8, larger groups in parts) have one form: their accumulators leave
-// registers for one block a step and three CTAs (two, with pairs: 81 us for 79).
+// where what counts is how many are under way.  us, PAIRS / not (both with TMA, on
+// other lengths than above): 256 sequences x 8 of 32 to 8,192 tokens 127 / 144, 40 x 8
+// of 2,048 30.6 / 35.4; 1,000 x 8 of 100 to 600 117 / 108, 256 x 8 of 30 to 130 22.5 /
+// 19.0.  In between, up to 128 blocks, a call whose CTAs are more than three an SM and
+// no more than four (58 to 76 sequences x 8) is one wave in the second form and two in
+// the first: of equal length 28.5 / 25.5 (60 of 1,000), 29.9 / 26.4 (64 of 1,000), 55.7
+// / 46.8 (64 of 2,000), 58.6 / 52.8 (76 of 2,000), fp16 46.6 / 38.2 (72 of 1,400).  (Of
+// unequal length the second wave may be the short ones and hide, 26.7 / 29.7 for 60 of
+// 300 to 2,000, 28.3 / 34.0 for 72, but the host does not know lengths.)  With heads of
+// 64 pairs leave registers for four CTAs, and are for split ranges too (64 x 8 of 64 to
+// 4,096 21.6 / 23.3, 128 x 8 of 2,000 48 / 52 in three CTAs; with heads of 128 split
+// ranges take longer, 16 x 8 of 8,000 57 / 47).  More heads (NT == 2, up to 8, larger
+// groups in parts) have one form: their accumulators leave registers for one block a
+// step and three CTAs (two, with pairs: 81 us for 79).
 template <int D, int NT, bool PAIRS>
 struct QuantShape {
     static constexpr int TILE_BYTES = 16 * D;
@@ -673,8 +682,8 @@ static int quant_decode(QuantDecodeParams &prm, int64_t blocks, int sms, cudaStr
                                power_below(std::min<int64_t>(12 * sms / ranges, blocks / 96)));
     const int64_t ctas = ranges * ranks;
     // The longest first, where that evens out more than finding them costs a CTA
-    // (256 x 8 of 32 to 8,192 tokens: 147 us in the order of the batch, 127; of
-    // 1,400 each 112 and 116).
+    // (256 x 8 of 32 to 8,192 tokens, other lengths than above: 147 us in the order
+    // of the batch, 127; of 1,400 each 112 and 116).
     prm.ordered = ctas > 3 * sms && blocks > ctas / 13 && prm.num_seqs <= kQdMaxOrdered;
     if (prm.G > 4) return launch_quant_decode<T, D, 2, false>(prm, (int)ctas, ranks, stream);
     const bool pairs = D == 64 ? blocks > 48 * ranks
