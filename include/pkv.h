@@ -491,7 +491,7 @@ int pkv_kv_gather_e4m3(void *k, void *v, const void *k_cache, const void *v_cach
  * kv_scales of blocks that are read are positive and finite, powers of two or not;
  * V's lie between 2^-80 and 2^120, and those of the blocks that one query sees
  * within a factor of 2^100 of one another.  (Append writes 2^-60 to 2^120: only
- * values beyond 2^48 next to tiles of zeros fall outside.)  Scores times log2 e,
+ * values beyond 2^47 next to tiles of zeros fall outside.)  Scores times log2 e,
  * plus the log2 of V's scale, stay below 2^22 in magnitude: of larger ones fp32
  * holds too few bits behind the point for weights relative to a maximum.  A query's
  * largest element times a K scale that it sees times `scale` stays below 2^100, even

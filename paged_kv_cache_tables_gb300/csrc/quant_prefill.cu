@@ -44,10 +44,10 @@
 // the CTAs of a cluster, and the parts are joined through its shared memory (us, and in
 // one CTA a unit: 16 rows behind 4,080 17.9 and 62; 50 behind 20,000 94 and 284).
 //
-// What bounds it: a key tile for two query tiles of head_dim 128 is 3,072 cycles of
-// products, a third of them the residual's, and a chain, S, softmax, P V, of which
-// two run at a time; the tensor pipe is active for 70 to 77 % of the time.  us in
-// bf16, fp16 and bf16 with 32-bit outputs, and over a 16-bit cache in bf16: 8 chunks
+// What bounds it: a key tile for two query tiles of head_dim 128 is 2,048 cycles of
+// products and half as many again for the residual's, and a chain, S, softmax, P V,
+// of which two run at a time; the tensor pipe is active for 70 to 77 % of the time.
+// us in bf16, fp16 and bf16 with 32-bit outputs, and over a 16-bit cache in bf16: 8 chunks
 // of 512 rows behind 0 to 4,096 tokens 141, 157, 154 and 147, where products of 16
 // bits without a residual would take 74; 3 x 4,000 rows, window 4,096, 690, 742, 714
 // and 673 for 392; 5 prompts of 2,000, head_dim 64, 94, 97, 98 and 94 for 25, bound by
